@@ -58,8 +58,13 @@ typedef enum {
 #define PA_DEVERR_SEQ_LEN  0x4u /* a length < 0, beyond the table width or the host bound  */
 #define PA_DEVERR_TIMEOUT  0x8u /* a bounded wait on a shared-memory barrier gave up       */
 #define PA_DEVERR_ORDER   0x10u /* a group order entry outside [0, num_groups)              */
+#define PA_DEVERR_KEEP    0x20u /* a kept position that is not ascending or out of range     */
+#define PA_DEVERR_VALUE   0x40u /* a NaN or +inf among logits or beam scores                  */
 
-typedef enum { PA_DTYPE_BF16 = 0 } pa_dtype;
+typedef enum {
+    PA_DTYPE_BF16 = 0,
+    PA_DTYPE_F32 = 1          /* logits of pa_beam_select only */
+} pa_dtype;
 
 /*
  * One layer's view of the physical block pool.  [P1] "A strong answer": the
@@ -459,6 +464,175 @@ pa_status pa_decode_grouped(void *out, const void *q, const pa_kv_pool *pool, co
                             int32_t max_suffix_len, float scale, const void *new_k, const void *new_v,
                             uint32_t flags, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions.  A head's first rot_dim components are rot_dim / 2 pairs;
+ * at position t pair i is turned by the angle t * w_i:
+ *     (x, y) -> mscale * (x cos - y sin, y cos + x sin)
+ * and components rot_dim .. head_dim - 1 pass unchanged.  The pages have no
+ * counterpart: they take the cached keys as given.  A decode step turns its
+ * queries and keys before the slot writer and pa_decode see them.
+ *
+ * Frequencies are given to the device as turns[i] = w_i / (2 pi) as a 64-bit
+ * fraction of a full turn (2^64 = one turn).  The phase of position t is the
+ * product t * turns[i] modulo 2^64: integer wrap-around drops whole turns
+ * exactly, so positions of any size and sign keep an angle error of at most
+ * |t| * 2^-64 turns, where a product in fp32 would have lost the angle.
+ * ------------------------------------------------------------------------- */
+
+/* How pa_rotary_frequencies scales w_i = base^(-2 i / rot_dim) for contexts
+ * longer than the trained one (factor s >= 1; L = original_len). */
+#define PA_ROTARY_PLAIN       0 /* w_i                                                       */
+#define PA_ROTARY_LINEAR      1 /* w_i / s (positions interpolated)                          */
+#define PA_ROTARY_BASE        2 /* base' = base * s^(rot_dim / (rot_dim - 2)) (rot_dim 2: w_i) */
+#define PA_ROTARY_PARTS       3 /* (1 - g) w_i / s + g w_i, g = (L w_i / 2 pi - low) / (high - low)
+                                 * clamped to [0, 1]: by the turns a pair makes over L          */
+#define PA_ROTARY_PARTS_INDEX 4 /* the same mix with 1 - g linear in i between the pair that makes
+                                 * `high` turns over L (rounded down, >= 0) and the one that makes
+                                 * `low` (rounded up, <= rot_dim - 1)                           */
+
+typedef struct {
+    int32_t rot_dim;       /* even, >= 2                                       */
+    int32_t scaling;       /* PA_ROTARY_*                                      */
+    double base;           /* > 1, e.g. 10000                                  */
+    double factor;         /* s; ignored by PA_ROTARY_PLAIN                    */
+    double original_len;   /* L; the two by-parts modes only                   */
+    double low, high;      /* 0 < low < high; the two by-parts modes only      */
+} pa_rotary_params;
+
+/* Host: turns_out[rot_dim / 2] for the parameters.  PA_ERR_INVALID_ARG for a
+ * NULL pointer, a value outside the ranges above or not finite, or an unknown
+ * mode. */
+pa_status pa_rotary_frequencies(const pa_rotary_params *params, uint64_t *turns_out);
+
+/* Host: turns_out[n] of n angular frequencies in radians per position (for
+ * frequencies of the caller's own).  Any finite value; else
+ * PA_ERR_INVALID_ARG. */
+pa_status pa_rotary_turns(const double *angular, int64_t n, uint64_t *turns_out);
+
+#define PA_ROTARY_INTERLEAVED 0x1u /* pairs (2 i, 2 i + 1); else (i, i + rot_dim / 2)           */
+#define PA_ROTARY_INVERSE     0x2u /* turns by -t * w_i: with the same mscale this is the
+                                    * transpose, i.e. the gradient of the forward call        */
+
+typedef struct {
+    const uint64_t *turns; /* device, [rot_dim / 2], 8-byte aligned            */
+    int32_t rot_dim;       /* even, 2 .. head_dim                              */
+    uint32_t flags;        /* PA_ROTARY_*                                      */
+    float mscale;          /* finite; 1 unless a scaling asks for another      */
+} pa_rotary;
+
+/*
+ * Rotates one tensor.
+ *   out        device, [num_tokens][num_heads][head_dim] bf16, dense
+ *   x          device, the same shape with x_stride elements from token to
+ *              token (0 = dense; else >= num_heads * head_dim, a multiple of
+ *              8), heads dense.  x = out (with a dense x) rotates in place;
+ *              other overlaps give an unspecified result
+ *   positions  device, [num_tokens] int64
+ * Computed in fp32 from angles reduced as above, rounded once to bf16.
+ * head_dim: a multiple of 8, at most 1024.  Errors as pa_reshape_and_cache;
+ * PA_ERR_INVALID_ARG for a bad rotary description.
+ */
+pa_status pa_rotate(void *out, const void *x, int64_t x_stride, const int64_t *positions,
+                    int64_t num_tokens, int32_t num_heads, int32_t head_dim, const pa_rotary *rotary,
+                    cudaStream_t stream);
+
+/*
+ * Rotary positions and slot writer in one call: q_out = rotated q; rotated k
+ * and v are stored at their slots as pa_reshape_and_cache stores them.
+ *   q_out      device, [num_tokens][num_q_heads][d] bf16, dense (what pa_decode
+ *              and pa_prefill_chunk take); may equal a dense q
+ *   q, k, v    device, [num_tokens][heads][d] bf16 with q_stride, k_stride,
+ *              v_stride elements from token to token (0 = dense; else a
+ *              multiple of 8 that holds the token's heads): views of one fused
+ *              projection are read in place
+ *   positions  device, [num_tokens] int64
+ *   slot_mapping  as pa_reshape_and_cache: a negative slot skips the token's k
+ *              and v (its q is still rotated), one >= NB * b raises
+ *              PA_DEVERR_SLOT and is skipped
+ * num_q_heads = 0 (q and q_out ignored) stores keys and values only.  The pool
+ * must not overlap the inputs.  head_dim at most 1024.
+ */
+pa_status pa_rotate_and_cache(const pa_kv_pool *pool, void *q_out, const void *q, int64_t q_stride,
+                              const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const int64_t *positions, const int64_t *slot_mapping, int64_t num_tokens,
+                              int32_t num_q_heads, const pa_rotary *rotary, cudaStream_t stream);
+
+/*
+ * Compaction: the kept tokens of each sequence move to consecutive positions,
+ * K and V of every kv-head of this layer's view.  Row i of sequence s moves
+ * from position keep[s][i] (through src_tables) to position starts[s] + i
+ * (through dst_tables).  [P1] feature table (beam-search row), [P3] "Shared
+ * prefixes need matching computation": the pages copy whole blocks; which
+ * tokens inside them stay is this library's addition -- accepted tokens of a
+ * draft, a sliding window behind its first tokens, any subset.
+ *   src_tables, dst_tables  device, [num_seqs][max_blocks_per_seq] int32.  The
+ *              same pointer: in place.  Different: the blocks written must not
+ *              be read by any row of this call (a compacted fork)
+ *   seq_lens   device, [num_seqs] int32: tokens cached
+ *   keep       device, [num_seqs][max_keep] int32: positions, strictly
+ *              ascending, starts[s] + i <= keep[s][i] < seq_lens[s].  (In place
+ *              that order is what makes every row read before it is written.)
+ *   keep_lens  device, [num_seqs] int32, in [0, max_keep] (0: nothing moves)
+ *   starts     device, [num_seqs] int32, or NULL for zeros
+ *   rotary     NULL: keys move as they are.  Else the keys (rotated when they
+ *              were cached) are turned by new position - old position, so that
+ *              they lie at their new positions; mscale and the flag
+ *              PA_ROTARY_INVERSE are ignored, since a key holds its mscale
+ *              already.  A row that does not move is not touched.
+ * The new length of sequence s is starts[s] + keep_lens[s]; rows behind it are
+ * left as they were.  Blocks written in place must belong to one sequence:
+ * pa_bm_unshare before, pa_bm_truncate after.
+ * A bad position raises PA_DEVERR_KEEP and its row is skipped; a bad length
+ * raises PA_DEVERR_SEQ_LEN and its sequence is skipped; a bad table entry raises
+ * PA_DEVERR_BLOCK_ID and its rows are skipped; the results of that sequence are then
+ * undefined, within its own blocks.  head_dim: a multiple of 8, at most 256;
+ * num_seqs and num_kv_heads at most 65,535; with rotary, rot_dim <= head_dim.
+ */
+pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, const int32_t *dst_tables,
+                            int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *keep,
+                            int32_t max_keep, const int32_t *keep_lens, const int32_t *starts,
+                            int32_t num_seqs, const pa_rotary *rotary, cudaStream_t stream);
+
+/*
+ * Beam search's selection.  [P1] feature table (beam-search row), [P2]
+ * beam/copy-on-write follow-up: beams fork and share blocks; which of them
+ * fork is decided here.  For each group of num_beams consecutive rows,
+ *     score(j, v) = beam_scores[j] + logits[j][v] - log sum_u exp logits[j][u]
+ * and the num_out largest scores are written in descending order, equal scores
+ * by the lower j * vocab + v first.
+ *   scores_out   device, [num_groups][num_out] fp32
+ *   parents_out  device, [num_groups][num_out] int32: j, the beam continued
+ *   tokens_out   device, [num_groups][num_out] int32: v
+ *   logits       device, [num_groups * num_beams] rows of vocab values, bf16 or
+ *                fp32 (logits_dtype), row_stride elements apart (0 = vocab; any
+ *                stride >= vocab), base 16-byte aligned
+ *   beam_scores  device, [num_groups][num_beams] fp32: cumulative log
+ *                probabilities; -inf: the beam is not in use (all but one beam
+ *                of a prompt's first step)
+ *   finished     device, [num_groups][num_beams] uint8 or NULL: a non-zero beam
+ *                has ended; its logits are not read and it stands with the one
+ *                candidate (end_token, beam_scores[j])
+ * -inf logits have no probability; a row of nothing else, like an unused beam
+ * and the other tokens of a finished one, has scores of -inf only.  Where a
+ * group has fewer than num_out other candidates, those of -inf fill up, lowest
+ * j * vocab + v first.  A row with a NaN or +inf logit, or a beam score of NaN or
+ * +inf, raises PA_DEVERR_VALUE and counts as such a row.
+ * Ordering and the sum of exponentials: fp32 exponentials relative to the
+ * running maximum, summed in fp32 per thread and fp64 across threads; scores
+ * compared in fp64 and rounded once to fp32.
+ *   workspace    device, 256-byte aligned, pa_beam_select_workspace_size bytes;
+ *                overwritten
+ * Supported: 1 <= num_beams <= 64; 1 <= num_out <= 64 and <= num_beams * vocab;
+ * 0 <= end_token < vocab where finished is given; num_groups * num_beams at
+ * most 65,535; num_beams * vocab at most 2^31 - 1.
+ */
+size_t pa_beam_select_workspace_size(int32_t num_groups, int32_t num_beams, int32_t vocab, int32_t num_out);
+pa_status pa_beam_select(float *scores_out, int32_t *parents_out, int32_t *tokens_out, const void *logits,
+                         int32_t logits_dtype, int64_t row_stride, const float *beam_scores,
+                         const uint8_t *finished, int32_t end_token, int32_t num_groups, int32_t num_beams,
+                         int32_t vocab, int32_t num_out, void *workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
+
 /*
  * Check of the bounded waits: launches one CTA whose wait on a shared-memory
  * barrier that nothing arrives at gives up after limit_ns (1 us .. 1 s, else
@@ -567,6 +741,36 @@ pa_status pa_bm_fork(pa_bm *bm, int32_t parent, int32_t *child_out);
 
 /* Releases a sequence; blocks whose refcount drops to 0 return to the pool. */
 pa_status pa_bm_free_seq(pa_bm *bm, int32_t seq);
+
+/*
+ * Beam reordering: afterwards seqs[j] holds the blocks and the length that
+ * seqs[parents[j]] held before (pa_beam_select's parents), for all j at once; no
+ * block moves.  Blocks no beam holds any more return to the pool; a beam that
+ * goes on in several is shared between them, and the next append to each forks
+ * its partly filled block (pa_bm_append_tokens).  seqs are distinct, parents in
+ * [0, n): else PA_ERR_INVALID_ARG; PA_ERR_NOT_FOUND / PA_ERR_SWAPPED if any
+ * sequence is.  On an error nothing changes.
+ */
+pa_status pa_bm_reorder(pa_bm *bm, const int32_t *seqs, const int32_t *parents, int32_t n);
+
+/*
+ * Gives seq private copies of its shared blocks from the one holding position
+ * first_token on (blocks that another table or the prefix cache also holds):
+ * writes one (src, dst) pair per replaced block to pairs_out ([cap][2]) and
+ * *n_pairs_out; the caller runs pa_copy_blocks on them before writing.  What an
+ * in-place pa_compact_tokens needs.  PA_ERR_NO_BLOCKS (too few blocks) and
+ * PA_ERR_INVALID_ARG (cap too small, first_token < 0) leave the sequence
+ * unchanged.
+ */
+pa_status pa_bm_unshare(pa_bm *bm, int32_t seq, int64_t first_token, int32_t *pairs_out, int32_t cap,
+                        int32_t *n_pairs_out);
+
+/*
+ * Shortens seq to n_tokens tokens and releases the blocks behind them (after a
+ * compaction, or for rejected draft tokens).  n_tokens above the length:
+ * PA_ERR_INVALID_ARG.
+ */
+pa_status pa_bm_truncate(pa_bm *bm, int32_t seq, int64_t n_tokens);
 
 /* Writes seq's table into table_out[0..cap) (-1 past its blocks). */
 pa_status pa_bm_get_table(const pa_bm *bm, int32_t seq, int32_t *table_out, int32_t cap,

@@ -24,7 +24,10 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3:
 PA_SWAP_OUT, PA_SWAP_IN = 0, 1
 PA_DECODE_EARLY_METADATA = 0x1
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_SEQ_LEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
-PA_DTYPE_BF16 = 0
+DEVERR_KEEP, DEVERR_VALUE = 0x20, 0x40
+PA_DTYPE_BF16, PA_DTYPE_F32 = 0, 1
+PA_ROTARY_INTERLEAVED, PA_ROTARY_INVERSE = 0x1, 0x2
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3, "parts_index": 4}
 
 # Every function declared in include/pa.h with (restype, argtypes).
 _P, _I64, _I32, _U32, _F, _SZ = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32,
@@ -39,6 +42,19 @@ class PaCapacity(ctypes.Structure):
                 ("prefix_bytes_paged", ctypes.c_double)]
 
 
+class PaRotaryParams(ctypes.Structure):
+    """``pa_rotary_params``: rotary frequencies and their scaling."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
+
+
+class PaRotary(ctypes.Structure):
+    """``pa_rotary``: device frequencies and how they are applied."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("mscale", ctypes.c_float)]
+
+
 class PaKvPool(ctypes.Structure):
     """``pa_kv_pool``: one layer's view of the block pool (strides in elements)."""
     _fields_ = [("base", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("num_kv_heads", ctypes.c_int32),
@@ -47,6 +63,7 @@ class PaKvPool(ctypes.Structure):
 
 
 _POOL = ctypes.POINTER(PaKvPool)
+_ROTARY = ctypes.POINTER(PaRotary)
 SIGNATURES = {
     "pa_status_string": (ctypes.c_char_p, [_I32]),
     "pa_version": (_I32, []),
@@ -68,6 +85,13 @@ SIGNATURES = {
     "pa_cascade_plan": (_I32, [_P, _I32, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "pa_decode_grouped": (_I32, [_P, _P, _POOL, _P, _I32, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F,
                                  _P, _P, _U32, _P]),
+    "pa_rotary_frequencies": (_I32, [ctypes.POINTER(PaRotaryParams), _P]),
+    "pa_rotary_turns": (_I32, [_P, _I64, _P]),
+    "pa_rotate": (_I32, [_P, _P, _I64, _P, _I64, _I32, _I32, _ROTARY, _P]),
+    "pa_rotate_and_cache": (_I32, [_POOL, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _ROTARY, _P]),
+    "pa_compact_tokens": (_I32, [_POOL, _P, _P, _I32, _P, _P, _I32, _P, _P, _I32, _ROTARY, _P]),
+    "pa_beam_select_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "pa_beam_select": (_I32, [_P, _P, _P, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P]),
     "pa_get_device_error": (_I32, [ctypes.POINTER(_U32), _I32, _P]),
     "pa_check_wait_timeout": (_I32, [ctypes.c_uint64, _P]),
     "pa_set_stream_k_ctas": (_I32, [_I32]),
@@ -80,6 +104,9 @@ SIGNATURES = {
     "pa_bm_append_tokens": (_I32, [_P, _I32, _I64, _P, _P, ctypes.POINTER(_I32)]),
     "pa_bm_fork": (_I32, [_P, _I32, ctypes.POINTER(_I32)]),
     "pa_bm_free_seq": (_I32, [_P, _I32]),
+    "pa_bm_reorder": (_I32, [_P, _P, _P, _I32]),
+    "pa_bm_unshare": (_I32, [_P, _I32, _I64, _P, _I32, ctypes.POINTER(_I32)]),
+    "pa_bm_truncate": (_I32, [_P, _I32, _I64]),
     "pa_bm_get_table": (_I32, [_P, _I32, _P, _I32, ctypes.POINTER(_I32), ctypes.POINTER(_I64)]),
     "pa_bm_num_free": (_I64, [_P]),
     "pa_bm_refcount": (_I32, [_P, _I64]),
@@ -456,6 +483,173 @@ def cascade_plan(tables, seq_lens, group_size: int, block_size: int) -> dict:
     _check(lib().pa_cascade_plan(ptr(t), W, ptr(L), B, int(group_size), int(block_size), ptr(pt), ptr(pl), ptr(go),
                                  ptr(st), ptr(sl)), "pa_cascade_plan")
     return {"prefix_tables": pt, "prefix_lens": pl, "group_order": go, "suffix_tables": st, "suffix_lens": sl}
+
+
+# ---- rotary positions, compaction and beam selection ------------------------
+
+_NULL = ctypes.c_void_p(0)
+
+
+def _same_device(*tensors) -> None:
+    """The library launches on the current device: every tensor has to be there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensors must be on the current device cuda:{cur}, got {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(pointer, token stride) of a bf16 CUDA tensor [tokens][heads][d] whose
+    tokens may be strided (a view of a fused projection); heads are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if t.numel() and ((d > 1 and s2 != 1) or (h > 1 and s1 != d) or (n > 1 and s0 < h * d)):
+        raise ValueError(f"{name} must be [tokens][heads][head_dim] with dense heads")
+    return ctypes.c_void_p(t.data_ptr()), (s0 if n > 1 else 0)
+
+
+def _rotary(freqs: torch.Tensor, interleaved: bool, mscale: float, inverse: bool = False) -> PaRotary:
+    turns = _dev(freqs, torch.int64, "freqs")
+    flags = (PA_ROTARY_INTERLEAVED if interleaved else 0) | (PA_ROTARY_INVERSE if inverse else 0)
+    return PaRotary(turns, 2 * freqs.numel(), flags, mscale)
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                       original_len: float = 0.0, low: float = 1.0, high: float = 32.0) -> np.ndarray:
+    """pa_rotary_frequencies: the turns per position of each of rot_dim / 2
+    pairs as 64-bit fractions (int64 numpy array of their bits; copy it to the
+    device once as ``freqs``).  scaling: "plain", "linear", "base", "parts" or
+    "parts_index"."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
+    params = PaRotaryParams(int(rot_dim), ROTARY_SCALINGS[scaling], base, factor, original_len, low, high)
+    out = np.empty(max(int(rot_dim) // 2, 1), dtype=np.int64)
+    _check(lib().pa_rotary_frequencies(ctypes.byref(params), out.ctypes.data_as(_P)), "pa_rotary_frequencies")
+    return out
+
+
+def rotary_turns(angular) -> np.ndarray:
+    """pa_rotary_turns: the same for angular frequencies (radians per position)
+    of the caller's own."""
+    w = np.ascontiguousarray(angular, dtype=np.float64).reshape(-1)
+    out = np.empty(len(w), dtype=np.int64)
+    _check(lib().pa_rotary_turns(w.ctypes.data_as(_P), len(w), out.ctypes.data_as(_P)), "pa_rotary_turns")
+    return out
+
+
+def rotate(out: torch.Tensor, x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
+           interleaved: bool = False, mscale: float = 1.0, inverse: bool = False, stream=None) -> None:
+    """pa_rotate: x [tokens][heads][d] bf16 (tokens may be strided) turned to
+    ``positions`` (int64) into the dense ``out``, which may be x itself."""
+    if x.dim() != 3 or out.shape != x.shape or positions.numel() != x.shape[0]:
+        raise ValueError("x and out must be [tokens][heads][head_dim] with one position per token")
+    src, stride = _rows(x, "x")
+    _same_device(out, x, positions, freqs)
+    rot = _rotary(freqs, interleaved, mscale, inverse)
+    _check(lib().pa_rotate(_dev(out, torch.bfloat16, "out"), src, stride, _dev(positions, torch.int64, "positions"),
+                           x.shape[0], x.shape[1], x.shape[2], ctypes.byref(rot), _stream(stream)), "pa_rotate")
+
+
+def rotate_and_cache(pool: torch.Tensor, q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor,
+                     v: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor, freqs: torch.Tensor,
+                     interleaved: bool = False, mscale: float = 1.0, layer: Optional[int] = None,
+                     stream=None) -> None:
+    """pa_rotate_and_cache: q rotated into q_out, k rotated and v stored at their
+    slots.  q, k, v: [tokens][heads][d] bf16, tokens may be strided; q_out dense
+    (may be q); q and q_out both None stores keys and values only."""
+    desc = pool_desc(pool, layer)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    n = k.shape[0]
+    if k.dim() != 3 or v.shape != k.shape or tuple(k.shape[1:]) != (desc.num_kv_heads, desc.head_dim):
+        raise ValueError("k and v must be [tokens][num_kv_heads][head_dim]")
+    if positions.numel() != n or slot_mapping.numel() != n:
+        raise ValueError("positions and slot_mapping must hold one entry per token")
+    _same_device(pool, q_out, q, k, v, positions, slot_mapping, freqs)
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    qo, qp, qs, hq = _NULL, _NULL, 0, 0
+    if q is not None:
+        if q.dim() != 3 or q_out.shape != q.shape or q.shape[0] != n or q.shape[2] != desc.head_dim:
+            raise ValueError("q and q_out must be [tokens][num_q_heads][head_dim]")
+        qp, qs = _rows(q, "q")
+        qo, hq = _dev(q_out, torch.bfloat16, "q_out"), q.shape[1]
+    rot = _rotary(freqs, interleaved, mscale)
+    _check(lib().pa_rotate_and_cache(ctypes.byref(desc), qo, qp, qs, kp, ks, vp, vs,
+                                     _dev(positions, torch.int64, "positions"),
+                                     _dev(slot_mapping, torch.int64, "slot_mapping"), n, hq, ctypes.byref(rot),
+                                     _stream(stream)), "pa_rotate_and_cache")
+
+
+def compact_tokens(pool: torch.Tensor, src_tables: torch.Tensor, dst_tables: torch.Tensor, seq_lens: torch.Tensor,
+                   keep: torch.Tensor, keep_lens: torch.Tensor, starts: Optional[torch.Tensor] = None,
+                   freqs: Optional[torch.Tensor] = None, interleaved: bool = False, layer: Optional[int] = None,
+                   stream=None) -> None:
+    """pa_compact_tokens: row i of sequence s moves from position keep[s][i]
+    (src_tables) to starts[s] + i (dst_tables; the same tensor compacts in
+    place).  freqs: turn the keys to their new positions."""
+    desc = pool_desc(pool, layer)
+    B = src_tables.shape[0]
+    if src_tables.dim() != 2 or dst_tables.shape != src_tables.shape:
+        raise ValueError("src_tables and dst_tables must be [num_seqs][max_blocks] of one shape")
+    if keep.dim() != 2 or keep.shape[0] != B or keep_lens.numel() != B or seq_lens.numel() != B:
+        raise ValueError("keep, keep_lens and seq_lens do not match the batch")
+    if starts is not None and starts.numel() != B:
+        raise ValueError("starts must hold one entry per sequence")
+    _same_device(pool, src_tables, dst_tables, seq_lens, keep, keep_lens, starts, freqs)
+    rot = ctypes.byref(_rotary(freqs, interleaved, 1.0)) if freqs is not None else None
+    _check(lib().pa_compact_tokens(ctypes.byref(desc), _dev(src_tables, torch.int32, "src_tables"),
+                                   _dev(dst_tables, torch.int32, "dst_tables"), src_tables.shape[1],
+                                   _dev(seq_lens, torch.int32, "seq_lens"), _dev(keep, torch.int32, "keep"),
+                                   keep.shape[1], _dev(keep_lens, torch.int32, "keep_lens"),
+                                   _dev(starts, torch.int32, "starts") if starts is not None else _NULL, B, rot,
+                                   _stream(stream)), "pa_compact_tokens")
+
+
+def beam_select_workspace_size(num_groups: int, num_beams: int, vocab: int, num_out: int) -> int:
+    return int(lib().pa_beam_select_workspace_size(num_groups, num_beams, vocab, num_out))
+
+
+def beam_select(scores_out: torch.Tensor, parents_out: torch.Tensor, tokens_out: torch.Tensor, logits: torch.Tensor,
+                beam_scores: torch.Tensor, finished: Optional[torch.Tensor] = None, end_token: int = 0,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pa_beam_select: the best [groups][num_out] continuations of logits
+    [groups][beams][vocab] (bf16 or fp32; rows may be strided) on top of
+    beam_scores [groups][beams].  finished: uint8 or bool [groups][beams];
+    workspace a uint8 CUDA tensor of beam_select_workspace_size(...) bytes."""
+    if logits.dim() != 3 or beam_scores.shape != logits.shape[:2]:
+        raise ValueError("logits must be [groups][beams][vocab] and beam_scores [groups][beams]")
+    G, J, V = logits.shape
+    if scores_out.dim() != 2 or scores_out.shape[0] != G or parents_out.shape != scores_out.shape or \
+            tokens_out.shape != scores_out.shape:
+        raise ValueError("scores_out, parents_out and tokens_out must be [groups][num_out]")
+    if not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    s0, s1, s2 = logits.stride()
+    stride = s1 if J > 1 else s0 if G > 1 else V
+    if logits.numel() and ((V > 1 and s2 != 1) or stride < V or (J > 1 and G > 1 and s0 != J * s1)):
+        raise ValueError("logits must be rows of dense vocabularies, evenly strided")
+    done = _NULL
+    if finished is not None:
+        if finished.shape != beam_scores.shape or finished.dtype not in (torch.uint8, torch.bool):
+            raise ValueError("finished must be uint8 or bool [groups][beams]")
+        done = _dev(finished, finished.dtype, "finished")
+    _same_device(scores_out, parents_out, tokens_out, logits, beam_scores, finished, workspace)
+    ws_ptr, ws_bytes = _NULL, 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _dev(workspace, torch.uint8, "workspace"), workspace.numel()
+    _check(lib().pa_beam_select(_dev(scores_out, torch.float32, "scores_out"),
+                                _dev(parents_out, torch.int32, "parents_out"),
+                                _dev(tokens_out, torch.int32, "tokens_out"), ctypes.c_void_p(logits.data_ptr()),
+                                PA_DTYPE_BF16 if logits.dtype == torch.bfloat16 else PA_DTYPE_F32, stride,
+                                _dev(beam_scores, torch.float32, "beam_scores"), done, int(end_token), G, J, V,
+                                scores_out.shape[1], ws_ptr, ws_bytes, _stream(stream)), "pa_beam_select")
 
 
 def check_wait_timeout(limit_ns: int, stream=None) -> None:

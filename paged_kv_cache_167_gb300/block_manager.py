@@ -59,6 +59,29 @@ class BlockManager:
     def free_seq(self, seq: int) -> None:
         _check(lib().pa_bm_free_seq(self._h, seq), "pa_bm_free_seq")
 
+    def reorder(self, seqs, parents) -> None:
+        """Beam reordering: seqs[j] goes on from what seqs[parents[j]] holds, for
+        all j at once."""
+        ids, par = self._tokens(seqs), self._tokens(parents)
+        if ids.ndim != 1 or ids.shape != par.shape:
+            raise ValueError("one parent per sequence")
+        _check(lib().pa_bm_reorder(self._h, ids.ctypes.data_as(ctypes.c_void_p), par.ctypes.data_as(ctypes.c_void_p),
+                                   len(ids)), "pa_bm_reorder")
+
+    def unshare(self, seq: int, first_token: int = 0) -> np.ndarray:
+        """Gives seq private copies of its shared blocks from the one holding
+        ``first_token`` on; returns the (src, dst) pairs to run through
+        copy_blocks."""
+        pairs = np.empty((self.num_blocks, 2), dtype=np.int32)   # no table is longer than the pool
+        n = _I32()
+        _check(lib().pa_bm_unshare(self._h, seq, first_token, pairs.ctypes.data_as(ctypes.c_void_p), len(pairs),
+                                   ctypes.byref(n)), "pa_bm_unshare")
+        return pairs[:n.value]
+
+    def truncate(self, seq: int, n_tokens: int) -> None:
+        """Shortens seq to n_tokens tokens, releasing the blocks behind them."""
+        _check(lib().pa_bm_truncate(self._h, seq, n_tokens), "pa_bm_truncate")
+
     def table(self, seq: int) -> Tuple[np.ndarray, int]:
         """(physical block ids, token count) of a sequence."""
         nb, nt = _I32(), _I64()

@@ -425,6 +425,132 @@ pa_status pa_decode_grouped(void *out, const void *q, const pa_kv_pool *pool, co
     return launch_prefill(a, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace pa {
+namespace {
+
+// A rotary description that fits heads of head_dim components.
+bool rotary_ok(const pa_rotary *r, int32_t head_dim) {
+    return r && r->turns && (reinterpret_cast<uintptr_t>(r->turns) & 7u) == 0 && r->rot_dim >= 2 &&
+           r->rot_dim % 2 == 0 && r->rot_dim <= head_dim &&
+           (r->flags & ~(PA_ROTARY_INTERLEAVED | PA_ROTARY_INVERSE)) == 0 && std::isfinite(r->mscale);
+}
+
+// Resolves a token stride (0 = dense): whole 16-byte vectors, no shorter than a row.
+bool token_stride(int64_t *stride, int64_t row) {
+    if (*stride == 0) *stride = row;
+    return *stride >= row && *stride % 8 == 0;
+}
+
+bool beam_shape_ok(int32_t num_groups, int32_t num_beams, int32_t vocab, int32_t num_out) {
+    return num_groups >= 0 && num_beams >= 1 && vocab >= 1 && num_out >= 1 &&
+           (int64_t)num_beams * vocab <= (int64_t)INT32_MAX && num_out <= (int64_t)num_beams * vocab &&
+           (int64_t)num_groups * num_beams <= 65535;
+}
+
+constexpr int32_t kMaxBeams = 64, kMaxBeamOut = 64;
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+pa_status pa_rotate(void *out, const void *x, int64_t x_stride, const int64_t *positions, int64_t num_tokens,
+                    int32_t num_heads, int32_t head_dim, const pa_rotary *rotary, cudaStream_t stream) {
+    if (num_tokens < 0 || num_tokens > INT32_MAX || num_heads < 0 || num_heads > 65535 || head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim % 8 != 0 || head_dim > 1024) return PA_ERR_UNSUPPORTED;
+    if (!rotary_ok(rotary, head_dim)) return PA_ERR_INVALID_ARG;
+    if (!token_stride(&x_stride, (int64_t)num_heads * head_dim)) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0 || num_heads == 0) return PA_OK;
+    if (!out || !x || !positions || !aligned16(out) || !aligned16(x)) return PA_ERR_INVALID_ARG;
+    return launch_rotate(out, x, x_stride, positions, num_tokens, num_heads, head_dim, *rotary, stream) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+pa_status pa_rotate_and_cache(const pa_kv_pool *pool, void *q_out, const void *q, int64_t q_stride, const void *k,
+                              int64_t k_stride, const void *v, int64_t v_stride, const int64_t *positions,
+                              const int64_t *slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                              const pa_rotary *rotary, cudaStream_t stream) {
+    PoolView view;
+    pa_status st = resolve_pool(pool, &view);
+    if (st != PA_OK) return st;
+    if (view.head_dim > 1024) return PA_ERR_UNSUPPORTED;
+    if (num_tokens < 0 || num_tokens > INT32_MAX || num_q_heads < 0) return PA_ERR_INVALID_ARG;
+    if ((int64_t)num_q_heads + 2ll * view.num_kv_heads > 65535) return PA_ERR_INVALID_ARG;
+    if (!rotary_ok(rotary, view.head_dim)) return PA_ERR_INVALID_ARG;
+    const int64_t kv_row = (int64_t)view.num_kv_heads * view.head_dim;
+    if (!token_stride(&k_stride, kv_row) || !token_stride(&v_stride, kv_row)) return PA_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && !token_stride(&q_stride, (int64_t)num_q_heads * view.head_dim)) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!k || !v || !positions || !slot_mapping || !aligned16(k) || !aligned16(v)) return PA_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out))) return PA_ERR_INVALID_ARG;
+    return launch_rotate_and_cache(view, q_out, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping,
+                                   num_tokens, num_q_heads, *rotary, stream) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, const int32_t *dst_tables,
+                            int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *keep,
+                            int32_t max_keep, const int32_t *keep_lens, const int32_t *starts, int32_t num_seqs,
+                            const pa_rotary *rotary, cudaStream_t stream) {
+    PoolView view;
+    pa_status st = resolve_pool(pool, &view);
+    if (st != PA_OK) return st;
+    if (view.head_dim > 256) return PA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || num_seqs > 65535 || max_keep < 0 || view.num_kv_heads > 65535) return PA_ERR_INVALID_ARG;
+    if (rotary && !rotary_ok(rotary, view.head_dim)) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || max_keep == 0) return PA_OK;
+    if (!src_tables || !dst_tables || !seq_lens || !keep || !keep_lens || max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    return launch_compact(view, src_tables, dst_tables, max_blocks_per_seq, seq_lens, keep, max_keep, keep_lens,
+                          starts, num_seqs, rotary, stream) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+size_t pa_beam_select_workspace_size(int32_t num_groups, int32_t num_beams, int32_t vocab, int32_t num_out) {
+    if (!beam_shape_ok(num_groups, num_beams, vocab, num_out) || num_beams > kMaxBeams || num_out > kMaxBeamOut)
+        return 0;
+    return num_groups ? beam_workspace((int64_t)num_groups * num_beams, vocab, num_out) : 0;
+}
+
+pa_status pa_beam_select(float *scores_out, int32_t *parents_out, int32_t *tokens_out, const void *logits,
+                         int32_t logits_dtype, int64_t row_stride, const float *beam_scores, const uint8_t *finished,
+                         int32_t end_token, int32_t num_groups, int32_t num_beams, int32_t vocab, int32_t num_out,
+                         void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!beam_shape_ok(num_groups, num_beams, vocab, num_out)) return PA_ERR_INVALID_ARG;
+    if (logits_dtype != PA_DTYPE_BF16 && logits_dtype != PA_DTYPE_F32) return PA_ERR_UNSUPPORTED;
+    if (num_beams > kMaxBeams || num_out > kMaxBeamOut) return PA_ERR_UNSUPPORTED;
+    if (row_stride == 0) row_stride = vocab;
+    if (row_stride < vocab || (finished && (end_token < 0 || end_token >= vocab))) return PA_ERR_INVALID_ARG;
+    if (num_groups == 0) return PA_OK;
+    if (!scores_out || !parents_out || !tokens_out || !logits || !aligned16(logits) || !beam_scores)
+        return PA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < beam_workspace((int64_t)num_groups * num_beams, vocab, num_out) ||
+        reinterpret_cast<uintptr_t>(workspace) % kWsAlign != 0)
+        return PA_ERR_WORKSPACE;
+    BeamArgs a;
+    a.scores_out = scores_out;
+    a.parents_out = parents_out;
+    a.tokens_out = tokens_out;
+    a.logits = logits;
+    a.bf16 = logits_dtype == PA_DTYPE_BF16;
+    a.row_stride = row_stride;
+    a.beam_scores = beam_scores;
+    a.finished = finished;
+    a.end_token = end_token;
+    a.num_groups = num_groups;
+    a.num_beams = num_beams;
+    a.vocab = vocab;
+    a.num_out = num_out;
+    a.workspace = workspace;
+    return launch_beam_select(a, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 pa_status pa_check_wait_timeout(uint64_t limit_ns, cudaStream_t stream) {
     if (limit_ns < 1000u || limit_ns > 1000000000u) return PA_ERR_INVALID_ARG;
     return launch_wait_timeout(limit_ns, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -300,6 +300,80 @@ pa_status pa_bm_free_seq(pa_bm *bm, int32_t seq) {
     return PA_OK;
 }
 
+pa_status pa_bm_reorder(pa_bm *bm, const int32_t *seqs, const int32_t *parents, int32_t n) {
+    if (!bm || n < 0 || (n > 0 && (!seqs || !parents))) return PA_ERR_INVALID_ARG;
+    for (int32_t j = 0; j < n; ++j) {
+        if (parents[j] < 0 || parents[j] >= n) return PA_ERR_INVALID_ARG;
+        if (!bm->valid_seq(seqs[j])) return PA_ERR_NOT_FOUND;
+        if (bm->seqs[seqs[j]].swapped) return PA_ERR_SWAPPED;
+    }
+    try {
+        std::set<int32_t> distinct(seqs, seqs + n);
+        if ((int32_t)distinct.size() != n) return PA_ERR_INVALID_ARG;
+        // the new tables first: the old ones are read until the last is built
+        std::vector<pa_bm::Seq> next((size_t)n);
+        for (int32_t j = 0; j < n; ++j) next[j] = bm->seqs[seqs[parents[j]]];
+        for (const pa_bm::Seq &s : next)
+            for (int32_t blk : s.blocks) bm->ref_inc(blk);
+        for (int32_t j = 0; j < n; ++j)
+            for (int32_t blk : bm->seqs[seqs[j]].blocks) bm->release_block(blk);
+        for (int32_t j = 0; j < n; ++j) std::swap(bm->seqs[seqs[j]], next[j]);
+    } catch (const std::bad_alloc &) {
+        return PA_ERR_NO_BLOCKS;
+    }
+    return PA_OK;
+}
+
+pa_status pa_bm_unshare(pa_bm *bm, int32_t seq, int64_t first_token, int32_t *pairs_out, int32_t cap,
+                        int32_t *n_pairs_out) {
+    if (!bm || !n_pairs_out || first_token < 0 || cap < 0) return PA_ERR_INVALID_ARG;
+    if (!bm->valid_seq(seq)) return PA_ERR_NOT_FOUND;
+    pa_bm::Seq &s = bm->seqs[seq];
+    if (s.swapped) return PA_ERR_SWAPPED;
+    const size_t first = (size_t)(first_token / bm->block_size);
+    int64_t shared = 0;
+    for (size_t i = first; i < s.blocks.size(); ++i) shared += bm->refcount[s.blocks[i]] > 1;
+    if (shared > cap || (shared > 0 && !pairs_out)) return PA_ERR_INVALID_ARG;
+    if (bm->available() < shared) return PA_ERR_NO_BLOCKS;
+    // All fresh blocks are taken before any shared one is released: a released
+    // block that only the prefix cache still holds may be evicted by the next
+    // allocation, and would then be both a source and a destination.
+    std::vector<size_t> at;
+    try {
+        at.reserve((size_t)shared);
+    } catch (const std::bad_alloc &) {
+        return PA_ERR_NO_BLOCKS;
+    }
+    for (size_t i = first; i < s.blocks.size(); ++i)
+        if (bm->refcount[s.blocks[i]] > 1) at.push_back(i);
+    int32_t n = 0;
+    for (size_t i : at) {
+        pairs_out[2 * n] = s.blocks[i];
+        pairs_out[2 * n++ + 1] = bm->pop_block();
+    }
+    for (int32_t k = 0; k < n; ++k) {
+        bm->release_block(pairs_out[2 * k]);
+        s.blocks[at[(size_t)k]] = pairs_out[2 * k + 1];
+    }
+    *n_pairs_out = n;
+    return PA_OK;
+}
+
+pa_status pa_bm_truncate(pa_bm *bm, int32_t seq, int64_t n_tokens) {
+    if (!bm || n_tokens < 0) return PA_ERR_INVALID_ARG;
+    if (!bm->valid_seq(seq)) return PA_ERR_NOT_FOUND;
+    pa_bm::Seq &s = bm->seqs[seq];
+    if (s.swapped) return PA_ERR_SWAPPED;
+    if (n_tokens > s.tokens) return PA_ERR_INVALID_ARG;
+    const size_t left = (size_t)blocks_for(n_tokens, bm->block_size);
+    while (s.blocks.size() > left) {
+        bm->release_block(s.blocks.back());
+        s.blocks.pop_back();
+    }
+    s.tokens = n_tokens;
+    return PA_OK;
+}
+
 pa_status pa_bm_get_table(const pa_bm *bm, int32_t seq, int32_t *table_out, int32_t cap, int32_t *num_blocks_out,
                           int64_t *num_tokens_out) {
     if (!bm || cap < 0 || (cap > 0 && !table_out)) return PA_ERR_INVALID_ARG;

@@ -28,23 +28,6 @@ std::mutex g_mutex;
 unsigned int *g_error_ptr[kMaxDevices];
 int g_sm_count[kMaxDevices];
 
-// Launch with programmatic stream serialisation: the kernel's launch overlaps
-// the previous kernel's tail; its griddepcontrol.wait orders the data.
-template <typename Kernel, typename Arg>
-cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, cudaStream_t stream, const Arg &arg) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, arg);
-}
-
 int current_device() {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;

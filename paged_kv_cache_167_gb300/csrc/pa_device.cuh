@@ -132,6 +132,25 @@ __device__ __forceinline__ void bulk_g2s(void *smem_dst, const void *gmem_src, u
         : "memory");
 }
 
+// ---- launch --------------------------------------------------------------
+
+// Launch with programmatic stream serialisation: the kernel's launch overlaps
+// the previous kernel's tail; its griddepcontrol.wait orders the data.
+template <typename Kernel, typename Arg>
+cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, cudaStream_t stream, const Arg &arg, size_t smem = 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, arg);
+}
+
 // ---- numeric helpers ------------------------------------------------------
 
 // Two bf16 packed in a 32-bit word -> (low, high) as fp32, exactly.

@@ -54,6 +54,36 @@ cudaError_t launch_copy_blocks(const PoolView &pool, const int32_t *pairs, int32
 cudaError_t launch_swap_blocks(const PoolView &pool, void *host_dev, int64_t host_blocks, const int32_t *pairs,
                                int32_t num_pairs, int32_t direction, cudaStream_t stream);
 
+// ---- rotary positions (pa_rotary.cu); arguments validated, strides resolved --
+cudaError_t launch_rotate(void *out, const void *x, int64_t x_stride, const int64_t *positions, int64_t num_tokens,
+                          int32_t num_heads, int32_t head_dim, const pa_rotary &rotary, cudaStream_t stream);
+cudaError_t launch_rotate_and_cache(const PoolView &pool, void *q_out, const void *q, int64_t q_stride,
+                                    const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                    const int64_t *positions, const int64_t *slots, int64_t num_tokens,
+                                    int32_t num_q_heads, const pa_rotary &rotary, cudaStream_t stream);
+
+// ---- compaction of cached tokens (pa_compact.cu) ----------------------------
+cudaError_t launch_compact(const PoolView &pool, const int32_t *src_tables, const int32_t *dst_tables,
+                           int32_t max_blocks, const int32_t *seq_lens, const int32_t *keep, int32_t max_keep,
+                           const int32_t *keep_lens, const int32_t *starts, int32_t num_seqs,
+                           const pa_rotary *rotary, cudaStream_t stream);
+
+// ---- beam selection (pa_beam.cu) --------------------------------------------
+struct BeamArgs {
+    float *scores_out;
+    int32_t *parents_out, *tokens_out;
+    const void *logits;
+    bool bf16;                 // else fp32
+    int64_t row_stride;        // elements
+    const float *beam_scores;
+    const uint8_t *finished;   // may be null
+    int32_t end_token;
+    int32_t num_groups, num_beams, vocab, num_out;
+    void *workspace;           // beam_workspace bytes, 256-byte aligned
+};
+size_t beam_workspace(int64_t rows, int32_t vocab, int32_t num_out);
+cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream);
+
 // ---- decode (pa_decode_*.cu) -----------------------------------------------
 struct DecodeArgs {
     void *out;
