@@ -617,9 +617,10 @@ pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, c
  * group has fewer than num_out other candidates, those of -inf fill up, lowest
  * j * vocab + v first.  A row with a NaN or +inf logit, or a beam score of NaN or
  * +inf, raises PA_DEVERR_VALUE and counts as such a row.
- * Ordering and the sum of exponentials: fp32 exponentials relative to the
- * running maximum, summed in fp32 per thread and fp64 across threads; scores
- * compared in fp64 and rounded once to fp32.
+ * Within a row candidates are ordered by their logits, across rows by scores
+ * compared in fp64 and rounded once to fp32.  The exponentials are fp32, summed
+ * in fp32 over the elements a warp holds together and exactly beyond; rows of
+ * equal logits have equal sums.
  *   workspace    device, 256-byte aligned, pa_beam_select_workspace_size bytes;
  *                overwritten
  * Supported: 1 <= num_beams <= 64; 1 <= num_out <= 64 and <= num_beams * vocab;

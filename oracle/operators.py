@@ -71,14 +71,13 @@ def compact(pool: np.ndarray, src_tables, dst_tables, keep, keep_lens, starts=No
     return after, size
 
 
-def log_sum_exp(x: np.ndarray) -> float:
-    """Of one row; -inf where no entry is above it; NaN with a NaN or +inf."""
-    if np.isnan(x).any() or np.isposinf(x).any():
-        return math.nan
-    top = float(x.max()) if x.size else -math.inf
-    if top == -math.inf:
-        return -math.inf
-    return top + math.log(math.fsum(np.exp(x - top)))
+def log_softmax(x: np.ndarray) -> np.ndarray:
+    """Of one row; all -inf where no entry is above it, or with a NaN or +inf.
+    The maximum is subtracted first, so that a row of lowest values is uniform."""
+    if np.isnan(x).any() or np.isposinf(x).any() or not (x > -math.inf).any():
+        return np.full(x.shape, -math.inf)
+    below = x - x.max()
+    return below - math.log(math.fsum(np.exp(below)))
 
 
 def beam_scores(logits: np.ndarray, scores, finished: Optional[np.ndarray] = None, end_token: int = 0) -> np.ndarray:
@@ -92,9 +91,7 @@ def beam_scores(logits: np.ndarray, scores, finished: Optional[np.ndarray] = Non
         if finished is not None and finished[j]:
             y[j, end_token] = s
             continue
-        total = log_sum_exp(np.asarray(logits[j], np.float64))
-        if math.isfinite(total):
-            y[j] = s + (np.asarray(logits[j], np.float64) - total)
+        y[j] = s + log_softmax(np.asarray(logits[j], np.float64))
     return y
 
 

@@ -4,20 +4,33 @@
 // score(j, v) = beam_scores[j] + x - log sum exp x.  Two kernels, one pass over
 // the logits:
 //
-// 1. scan: CTA (slice, row) reads its slice of one row once.  Each thread keeps
-//    the running maximum and the sum of exponentials relative to it (rescaled
-//    when the maximum rises), and which vector its maximum came from.  The n-th
-//    largest of the threads' maxima is a lower bound of the slice's n-th largest
-//    element, so only the few threads whose maximum reaches it can hold a
-//    candidate: their elements (and no others) are read again, from L2, and
-//    those at or above the bound are ranked.  Keys are (value, lower index
-//    first), so they are unique, ties need no further rule, and a row of equal
-//    values collects no more than one vector per bounding thread.
-// 2. merge: one CTA per group joins the slices' sums in fp64, turns the lists
-//    (each sorted) into fp64 scores and picks the n best by the same bound, taken
-//    over the lists' heads.
+// 1. scan: a row is cut into chunks of 1024 vectors of 16 bytes, four for each
+//    thread of a CTA.  A warp's part of a chunk is summed by itself (32 lanes'
+//    local maxima and sums of exponentials, joined by shuffles: no running
+//    maximum, no divergence) and written as one (reference, sum) pair; which
+//    elements meet in which sum goes by their index in the row alone.  CTA
+//    (slice, row) takes an equal share of the row's chunks and reads them once;
+//    each of its threads keeps the maximum over them and the chunk
+//    it came from.  The n-th largest of the maxima of 4 n groups of threads is a
+//    lower bound of the slice's n-th largest element (and close to it: some 9
+//    elements reach it at n = 8), so only the few threads whose maximum reaches it
+//    can hold a candidate: their elements (and no others) are read again, from
+//    cache, and those at or above the bound are ranked.  Keys are (value, lower
+//    index first), so they are unique and ties need no further rule.
+// 2. merge: one CTA per group adds up each row's partial sums, turns the
+//    slices' lists (each sorted) into fp64 scores and picks the n best by the
+//    same bound, taken over the lists' heads.
+//
+// The exponentials: 2^(x L - c) with L = log2(e) rounded to fp32 and c = m L
+// rounded to an integer: one fused multiply-add (x L is not rounded by itself)
+// and one hardware 2^x.  The sum is then relative to c / L, which fp64 holds, so
+// c's rounding biases nothing, L's own (2^-26) acts on the distance to the
+// maximum only, and sums of different references join by exact shifts: above the
+// warp they are integers in units of 2^-32, and equal rows have equal sums
+// wherever they lie and however the grid cuts them.  A warp that meets a value
+// beyond 2^22 in size, where c would have no fraction left to lose (a row of the
+// type's lowest value, say), sums differences to its maximum instead.
 #include <algorithm>
-#include <cfloat>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -27,9 +40,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;            // vectors a thread loads at once
+constexpr int kChunk = kThreads * kUnroll;
+constexpr int kStages = 3;            // chunks in flight or at work
+constexpr int kPart = 33;             // a warp's 32 neighbouring vectors and the one behind them
+constexpr size_t kScanSmem = (size_t)kStages * kWarps * kUnroll * kPart * sizeof(uint4);
+constexpr int kCtasPerSm = 4;
 constexpr int kCap = 1024;            // candidates ranked at once
-constexpr float kLog2eHi = 1.44269502162933349609375f;     // log2(e) rounded to fp32
-constexpr float kLog2eLo = 1.92596299112661746887e-8f;     // and the rest
+constexpr float kLog2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
+constexpr float kFar = 4194304.f;                      // 2^22
 
 // fp32 bits in increasing order; both zeros and the subnormals (which the
 // fp32 maximum flushes, and whose scores fp64 cannot tell apart) are one value.
@@ -46,8 +65,44 @@ __device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
 }
 constexpr uint64_t kLeastKey = (uint64_t)(0x007fffffu + 1) << 32;   // above every key of -inf (order 0x007fffff)
 
-// exp(t) for t <= 0: 2^(t log2 e), the product carried to more than fp32
-__device__ __forceinline__ float exp_neg(float t) { return fast_exp2(__fmaf_rn(t, kLog2eHi, t * kLog2eLo)); }
+// Sixteen bytes from global to shared memory, past the registers.
+__device__ __forceinline__ void copy_async(uint4 *to, const uint4 *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// Two fp32 in one 64-bit register, for the paired multiply-add and add.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The reference c of a maximum, an integer below 2^24; finite for -inf, so that
+// 0 * 2^(c - c') is 0.
+__device__ __forceinline__ float reference_of(float m) {
+    return rintf(__fmul_rn(fminf(fmaxf(m, -kFar), kFar), kLog2e));
+}
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && fabsf(m) < INFINITY; }
 
 struct BeamParams {
     const void *logits;
@@ -55,9 +110,14 @@ struct BeamParams {
     const float *beam_scores;
     const uint8_t *finished;
     int32_t end_token;
-    int32_t num_beams, vocab, num_out, slices;
-    // workspace, one entry per (row, slice)
-    double *sums;
+    int32_t num_beams, vocab, num_out;
+    int32_t row_vectors;             // ceil(vocab / elements of a vector)
+    int32_t row_chunks;              // ceil(row_vectors / kChunk)
+    int32_t slices;                  // of a row
+    int32_t depth;                   // of the lists' fronts in the merge
+    // workspace
+    float2 *sums;                    // [rows][row_chunks][kWarps]: (reference, sum), or (maximum, -sum)
+    // and for each (row, slice):
     float *maxima;
     int32_t *counts;
     float *values;                   // [..][num_out], descending
@@ -81,6 +141,17 @@ template <> struct Elements<uint16_t> {                        // bf16
             x[2 * i + 1] = f.y;
         }
     }
+    // of several vectors; NaN is passed over, as fmaxf does
+    static __device__ __forceinline__ float maximum(const uint4 (&v)[kUnroll]) {
+        auto h = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162 *>(&w); };
+        __nv_bfloat162 t[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            t[u] = __hmax2(__hmax2(h(v[u].x), h(v[u].y)), __hmax2(h(v[u].z), h(v[u].w)));
+        const __nv_bfloat162 m = __hmax2(__hmax2(t[0], t[1]), __hmax2(t[2], t[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    static __device__ __forceinline__ uint32_t minus_inf_word() { return 0xff80ff80u; }
 };
 template <> struct Elements<float> {
     static constexpr int kVec = 4;
@@ -91,6 +162,15 @@ template <> struct Elements<float> {
         x[2] = __uint_as_float(v.z);
         x[3] = __uint_as_float(v.w);
     }
+    static __device__ __forceinline__ float maximum(const uint4 (&v)[kUnroll]) {
+        float t[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            t[u] = fmaxf(fmaxf(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
+                         fmaxf(__uint_as_float(v[u].z), __uint_as_float(v[u].w)));
+        return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    }
+    static __device__ __forceinline__ uint32_t minus_inf_word() { return 0xff800000u; }
 };
 
 // A row read in vectors j of elements [j * kVec, (j + 1) * kVec), -inf behind the
@@ -110,30 +190,37 @@ struct Row {
     __device__ __forceinline__ Row(const T *row, int32_t n)
         : x(row), vocab(n), skew((uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T)) {}
 
-    __device__ __forceinline__ uint4 load(int32_t j) const {
-        const int32_t e0 = j * kVec;
-        const uint4 *at = reinterpret_cast<const uint4 *>(x + (e0 - (int32_t)skew));
-        if (skew == 0) {
-            if (vocab - e0 >= kVec) return __ldg(at);
-        } else if ((int64_t)e0 + 2 * kVec - skew <= vocab) {
-            const uint4 a = __ldg(at), b = __ldg(at + 1);
-            uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            const uint32_t bytes = skew * sizeof(T);
-            if (bytes & 8u) {
+    // Vectors [0, whole()) lie inside the row together with the aligned ones
+    // they are taken from, aligned() and the one after each.
+    __device__ __forceinline__ int32_t whole() const {
+        return skew == 0 ? vocab / kVec : (int32_t)(((int64_t)vocab + skew) / kVec) - 1;
+    }
+    __device__ __forceinline__ const uint4 *aligned() const { return reinterpret_cast<const uint4 *>(x - skew); }
+    // The vector that begins skew elements into a.
+    __device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b) const {
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint32_t bytes = skew * sizeof(T);
+        if (bytes & 8u) {
 #pragma unroll
-                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-            }
-            if (bytes & 4u) {
-#pragma unroll
-                for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-            }
-            if (sizeof(T) == 2) {
-                const uint32_t shift = (bytes & 2u) * 8;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], shift);
-            }
-            return make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
         }
+        if (bytes & 4u) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        if (sizeof(T) == 2) {
+            const uint32_t shift = (bytes & 2u) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], shift);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ uint4 load(int32_t j) const {
+        if (j < whole()) {
+            const uint4 a = __ldg(aligned() + j);
+            return skew == 0 ? a : shifted(a, __ldg(aligned() + j + 1));
+        }
+        const int32_t e0 = j * kVec;
         uint32_t e[kVec], w[4];      // the row's last elements, one by one
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -163,128 +250,207 @@ __device__ __forceinline__ bool beam_runs(const BeamParams &p, int row) {
     return score > -INFINITY && score < INFINITY;
 }
 
+// A warp's part of a chunk: top is the maximum of each lane's vectors.  Returns
+// (reference, sum of 2^(x L - reference)), or (maximum, -sum of e^(x - maximum))
+// where a value is far.  A NaN or +inf makes the sum NaN or inf.
+template <typename E>
+__device__ __forceinline__ float2 chunk_sum(const uint4 (&v)[kUnroll], float top) {
+    if (__any_sync(0xffffffffu, is_far(top))) {
+        float most = top;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float e[E::kVec];
+            E::unpack(v[u], e);
+#pragma unroll
+            for (int i = 0; i < E::kVec; ++i) sum += fast_exp2((e[i] - most) * kLog2e);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        return make_float2(most, -sum);
+    }
+    const float c = reference_of(top);
+    const uint64_t minus_c = pair(-c, -c), scale = pair(kLog2e, kLog2e);
+    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        float e[E::kVec];
+        E::unpack(v[u], e);
+#pragma unroll
+        for (int i = 0; i < E::kVec; i += 4) {
+            const float2 s = unpair(pair_fma(pair(e[i], e[i + 1]), scale, minus_c));
+            const float2 t = unpair(pair_fma(pair(e[i + 2], e[i + 3]), scale, minus_c));
+            sum0 = pair_add(sum0, pair(fast_exp2(s.x), fast_exp2(s.y)));
+            sum1 = pair_add(sum1, pair(fast_exp2(t.x), fast_exp2(t.y)));
+        }
+    }
+    const float2 s = unpair(pair_add(sum0, sum1));
+    const int reference = __reduce_max_sync(0xffffffffu, (int)c);
+    float sum = (s.x + s.y) * fast_exp2((float)((int)c - reference));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return make_float2((float)reference, sum);
+}
+
+struct ScanShared {
+    __align__(16) uint64_t keys[kCap];              // the groups' bounds first, then the candidates
+    int32_t holders[kThreads];
+    int num_holders, num_found;
+    uint64_t bound;
+    float warp_max[kWarps];
+};
+static_assert(sizeof(ScanShared) <= kScanSmem, "the selection reuses the copies' shared memory");
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const BeamParams p) {
     using E = Elements<T>;
     constexpr int VN = E::kVec;
-    constexpr int kUnroll = 4;
-    __shared__ uint64_t keys[kCap];          // the threads' bounds first, then the candidates
-    __shared__ int32_t holders[kThreads];
-    __shared__ int num_holders, num_found;
-    __shared__ uint64_t bound;
-    __shared__ float warp_max[kWarps];
-    __shared__ double warp_sum[kWarps];
+    extern __shared__ __align__(16) unsigned char dyn[];
+    uint4 *parts = reinterpret_cast<uint4 *>(dyn);  // [stage][warp][load][kPart] while the slice streams by
+    ScanShared &sh = *reinterpret_cast<ScanShared *>(dyn);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slice = blockIdx.x, row = blockIdx.y;
-    const int64_t entry = (int64_t)row * p.slices + slice;
-    const int n = p.num_out;
+    const int row = blockIdx.y, n = p.num_out;
+    const int64_t entry = (int64_t)row * p.slices + blockIdx.x;
     if (!beam_runs(p, row)) {
-        if (tid == 0) {
-            p.counts[entry] = 0;
-            p.maxima[entry] = -INFINITY;
-            p.sums[entry] = 0.0;
-        }
+        if (tid == 0) p.counts[entry] = 0;
         return;
     }
+    // (at most 2^19 chunks and 608 slices: the products fit)
+    const int32_t first = (int32_t)((uint32_t)p.row_chunks * blockIdx.x / (uint32_t)p.slices);
+    const int32_t last = (int32_t)((uint32_t)p.row_chunks * (blockIdx.x + 1) / (uint32_t)p.slices);
     const Row<T> x(static_cast<const T *>(p.logits) + (int64_t)row * p.row_stride, p.vocab);
-    const int32_t vectors = (p.vocab + VN - 1) / VN;
-    const int32_t lo = (int32_t)((int64_t)vectors * slice / p.slices);
-    const int32_t hi = (int32_t)((int64_t)vectors * (slice + 1) / p.slices);
-
-    float m = -INFINITY, sum = 0.f;
-    int32_t best = lo;
-    for (int32_t j0 = lo + tid; j0 < hi; j0 += kThreads * kUnroll) {
+    const int32_t whole = x.whole(), vectors = p.row_vectors;
+    const uint32_t none = E::minus_inf_word();
+    // A thread copies its own vectors; those of a warp are neighbours, and a row
+    // that does not begin on 16 bytes needs the one behind them too.
+    const uint4 *at = x.aligned();
+    const int32_t available = x.skew == 0 ? whole : whole + 1;
+    auto part = [&](int32_t chunk, int u) {
+        return parts + ((((chunk - first) % kStages) * kWarps + warp) * kUnroll + u) * kPart + lane;
+    };
+    auto start = [&](int32_t chunk) {
+        if (chunk < last) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int32_t j = chunk * kChunk + u * kThreads + tid;
+                if (j < available) copy_async(part(chunk, u), at + j);
+                if (x.skew != 0 && lane == 31 && j + 1 < available) copy_async(part(chunk, u) + 1, at + j + 1);
+            }
+        }
+        copy_commit();                              // (an empty group where nothing is left)
+    };
+    float m = -INFINITY;
+    int32_t best = first;
+    float2 *sums = p.sums + ((int64_t)row * p.row_chunks + first) * kWarps + warp;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) start(first + s);
+    for (int32_t k = first; k < last; ++k) {
+        copy_wait<kStages - 1>();                   // chunk k has landed; the later ones may be under way
+        __syncwarp();
         uint4 v[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (j0 + u * kThreads < hi) v[u] = x.load(j0 + u * kThreads);
-#pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int32_t j = j0 + u * kThreads;
-            if (j >= hi) break;
-            float e[VN];
-            E::unpack(v[u], e);
-            float top = e[0];
-#pragma unroll
-            for (int i = 1; i < VN; ++i) top = fmaxf(top, e[i]);
-            if (top > m) {
-                sum *= exp_neg(m - top);
-                m = top;
-                best = j;
+            const int32_t j = k * kChunk + u * kThreads + tid;
+            v[u] = make_uint4(none, none, none, none);
+            if (j < whole) {
+                const uint4 *a = part(k, u);
+                v[u] = x.skew == 0 ? a[0] : x.shifted(a[0], a[1]);
+            } else if (j < vectors) {
+                v[u] = x.load(j);                   // the row's last one or two
             }
-            const float ref = m == -INFINITY ? 0.f : m;      // NaN and +inf end up in the sum as NaN
-#pragma unroll
-            for (int i = 0; i < VN; ++i) sum += exp_neg(e[i] - ref);
         }
+        __syncwarp();                               // every lane has read what its neighbours copied
+        start(k + kStages);
+        const float top = E::maximum(v);
+        if (top > m) {
+            m = top;
+            best = k;
+        }
+        const float2 s = chunk_sum<E>(v, top);
+        if (lane == 0) *sums = s;
+        sums += kWarps;
     }
+    copy_wait<0>();
+    __syncthreads();                                // the copies' shared memory is free
 
-    // slice maximum and sum
+    // the slice's maximum, and the bounds of the groups (2^k neighbouring threads)
     float top = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) warp_max[warp] = top;
-    // the thread's best key lies between those of its vector's last and first element
-    const uint64_t least = m > -INFINITY ? key_of(order_of(m), (uint32_t)best * VN + (VN - 1)) : 0;
-    const uint64_t most = m > -INFINITY ? key_of(order_of(m), (uint32_t)best * VN) : 0;
-    keys[tid] = least;
-    if (tid == 0) bound = kLeastKey;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_max[w]);
-    double part = top == -INFINITY ? (double)sum : (double)sum * (double)exp_neg(m - top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == 0) warp_sum[warp] = part;
-    // the n-th largest of the threads' bounds
-    int above = 0;
-    for (int t = 0; t < kThreads; ++t) above += keys[t] > least;
-    if (least != 0 && above == n - 1 && least > kLeastKey) bound = least;
-    __syncthreads();
+    if (lane == 0) sh.warp_max[warp] = top;
+    // the thread's best key lies between those of its best chunk's last and first element
+    const uint32_t begin = ((uint32_t)best * kChunk + tid) * VN;
+    const uint64_t least = m > -INFINITY ? key_of(order_of(m), begin + (kUnroll - 1) * kThreads * VN + (VN - 1)) : 0;
+    const uint64_t most = m > -INFINITY ? key_of(order_of(m), begin) : 0;
+    const int group_log = n <= 8 ? 3 : n <= 16 ? 2 : n <= 32 ? 1 : 0, groups = kThreads >> group_log;
+    uint64_t group = least;
+    for (int o = 1; o < (1 << group_log); o <<= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, group, o);
+        group = other > group ? other : group;
+    }
+    if ((tid & ((1 << group_log) - 1)) == 0) sh.keys[tid >> group_log] = group;
     if (tid == 0) {
-        double total = 0.0;
-        for (int w = 0; w < kWarps; ++w) total += warp_sum[w];
-        p.sums[entry] = total;
+        sh.bound = kLeastKey;
+        sh.num_holders = sh.num_found = 0;
+    }
+    __syncthreads();
+    if (tid < groups) {                             // the n-th largest of the groups' bounds
+        const uint64_t mine = sh.keys[tid];
+        int above = 0;
+        for (int t = 0; t < groups; t += 2) {
+            const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sh.keys + t);
+            above += (k.x > mine) + (k.y > mine);
+        }
+        if (mine != 0 && above == n - 1) sh.bound = mine;
+    }
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.warp_max[i]);
         p.maxima[entry] = top;
     }
+    __syncthreads();
+    const int32_t end = min(last * kChunk, vectors);
     int found;
     while (true) {
-        const uint64_t limit = bound;
-        if (tid == 0) num_holders = num_found = 0;
+        const uint64_t limit = sh.bound;
+        if (most >= limit) sh.holders[atomicAdd(&sh.num_holders, 1)] = tid;
         __syncthreads();
-        if (most >= limit) holders[atomicAdd(&num_holders, 1)] = tid;
-        __syncthreads();
-        for (int w = warp; w < num_holders; w += kWarps)
-            for (int32_t j = lo + holders[w] + lane * kThreads; j < hi; j += 32 * kThreads) {
+        for (int h = warp; h < sh.num_holders; h += kWarps)
+            for (int32_t j = first * kChunk + sh.holders[h] + lane * kThreads; j < end; j += 32 * kThreads) {
                 float e[VN];
                 E::unpack(x.load(j), e);
 #pragma unroll
                 for (int i = 0; i < VN; ++i) {
                     const uint64_t key = key_of(order_of(e[i]), (uint32_t)j * VN + i);
                     if (e[i] > -INFINITY && key >= limit) {
-                        const int at = atomicAdd(&num_found, 1);
-                        if (at < kCap) keys[at] = key;
+                        const int at = atomicAdd(&sh.num_found, 1);
+                        if (at < kCap) sh.keys[at] = key;
                     }
                 }
             }
         __syncthreads();
-        found = num_found;
+        found = sh.num_found;
         if (found <= kCap) break;
-        // More than are ranked at once (many large values in few threads): the
-        // n-th largest of those held is a higher bound; kCap - n elements drop out.
-        for (int c = tid; c < kCap; c += kThreads) {
-            const uint64_t mine = keys[c];
+        // More than are ranked at once (many large or equal values in few threads):
+        // the n-th largest of those held is a higher bound; kCap - n elements drop out.
+        for (int k = tid; k < kCap; k += kThreads) {
+            const uint64_t mine = sh.keys[k];
             int rank = 0;
-            for (int t = 0; t < kCap; ++t) rank += keys[t] > mine;
-            if (rank == n - 1) bound = mine;
+            for (int t = 0; t < kCap; ++t) rank += sh.keys[t] > mine;
+            if (rank == n - 1) sh.bound = mine;
         }
         __syncthreads();
+        if (tid == 0) sh.num_holders = sh.num_found = 0;
+        __syncthreads();
     }
-    for (int c = tid; c < found; c += kThreads) {
-        const uint64_t mine = keys[c];
+    for (int k = tid; k < found; k += kThreads) {
+        const uint64_t mine = sh.keys[k];
         int rank = 0;
-        for (int t = 0; t < found; ++t) rank += keys[t] > mine;
+        for (int t = 0; t < found; ++t) rank += sh.keys[t] > mine;
         if (rank < n) {
             p.values[entry * n + rank] = value_of((uint32_t)(mine >> 32));
             p.indices[entry * n + rank] = (int32_t)(0xffffffffu - (uint32_t)mine);
@@ -300,8 +466,8 @@ struct Candidate {
     int32_t index;
 };
 __device__ __forceinline__ int64_t order_of(double s) {
-    const int64_t b = __double_as_longlong(s + 0.0);
-    return b ^ (int64_t)((uint64_t)(b >> 63) >> 1);
+    const int64_t b = __double_as_longlong(s);
+    return b == INT64_MIN ? 0 : b ^ (int64_t)((uint64_t)(b >> 63) >> 1);   // -0 is 0
 }
 __device__ __forceinline__ double score_of(int64_t o) {
     return __longlong_as_double(o ^ (int64_t)((uint64_t)(o >> 63) >> 1));
@@ -310,152 +476,239 @@ __device__ __forceinline__ bool better(const Candidate &a, const Candidate &b) {
     return a.score > b.score || (a.score == b.score && a.index < b.index);
 }
 
+// log(t 2^-32) for t > 0.  t = m 2^e with m in [0.707, 1.414]; log m = 2 artanh(z)
+// with z = (m - 1) / (m + 1), |z| < 0.1716, artanh(z) = z (1 + z^2 / 3 + z^4 / 5 + ...).
+// The bracket less 1 is below 0.01, so fp32 holds it to 2^-30; the rest is
+// fp64, of which this part has two lanes an SM.  Within 2^-29 of the value.
+__device__ __forceinline__ double log_units(unsigned long long t) {
+    const double d = (double)t;
+    const int64_t b = __double_as_longlong(d);
+    int e = (int)(b >> 52) - 1023;
+    double m = __longlong_as_double((b & 0x000fffffffffffffll) | 0x3ff0000000000000ll);   // [1, 2)
+    if (m > 1.4142135623730951) {
+        m *= 0.5;
+        ++e;
+    }
+    const double up = m + 1.0;
+    double r = (double)(1.0f / (float)up);
+    r += r * (1.0 - up * r);
+    const double z = (m - 1.0) * r;
+    const float q = (float)z * (float)z;
+    const float series = q * (1.f / 3 + q * (1.f / 5 + q * (1.f / 7 + q * (1.f / 9 + q * (1.f / 11 + q * (1.f / 13))))));
+    return (e - 32) * 0.693147180559945309417232 + 2.0 * (z + z * (double)series);
+}
+
 struct Beam {
-    double score, lse;
+    double base, offset;             // score(v) = (x - base) + offset
+    unsigned long long total;        // the row's sum, 2^-32 units
+    float top;
     int32_t kind;                    // 0: nothing but -inf, 1: runs, 2: ended
+    int32_t flat;                    // j * vocab
 };
 
-__device__ __forceinline__ int list_count(const BeamParams &p, const Beam &b, int64_t entry, int slice) {
-    return b.kind == 1 ? __ldcg(p.counts + entry) : b.kind == 2 && slice == 0 ? 1 : 0;
-}
-__device__ __forceinline__ Candidate list_item(const BeamParams &p, const Beam &b, int j, int64_t entry, int i) {
-    Candidate c;
-    if (b.kind == 2) {
-        c.score = order_of(b.score);
-        c.index = j * p.vocab + p.end_token;
-    } else {
-        c.score = order_of(b.score + ((double)__ldcg(p.values + entry * p.num_out + i) - b.lse));
-        c.index = j * p.vocab + __ldcg(p.indices + entry * p.num_out + i);
-    }
-    return c;
-}
-
-// Dynamic shared memory: beams [num_beams], list heads [num_beams * slices],
-// candidates [num_out * min(num_out, lists)], chosen indices [num_out].
+// Dynamic shared memory: the lists' fronts (their first `depth` candidates)
+// [lists * depth], the candidates to rank [kCap], beams [num_beams], counts
+// [lists].
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
     extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ int num_found;
+    __shared__ Candidate best[kThreads];
     __shared__ Candidate bound;
+    __shared__ int num_found;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int tid = threadIdx.x, g = blockIdx.x, n = p.num_out, lists = p.num_beams * p.slices;
-    Beam *beams = reinterpret_cast<Beam *>(dyn);
-    Candidate *heads = reinterpret_cast<Candidate *>(beams + p.num_beams);
-    Candidate *found = heads + lists;
-    int32_t *chosen = reinterpret_cast<int32_t *>(found + n * min(n, lists));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, n = p.num_out;
+    const int lists = p.num_beams * p.slices, row0 = g * p.num_beams, depth = p.depth;
+    const int64_t entry0 = (int64_t)row0 * p.slices;
+    Candidate *front = reinterpret_cast<Candidate *>(dyn);
+    Candidate *found = front + lists * depth;
+    Beam *beams = reinterpret_cast<Beam *>(found + kCap);
+    int32_t *counts = reinterpret_cast<int32_t *>(beams + p.num_beams);
     if (tid == 0) {
         num_found = 0;
         bound.score = INT64_MIN;
         bound.index = INT32_MAX;
     }
-    for (int j = tid; j < p.num_beams; j += kThreads) {
-        const int row = g * p.num_beams + j;
-        const float score = __ldg(p.beam_scores + row);
-        Beam b = {(double)score, 0.0, 0};
+    // the fronts, raw, and every list's count: loads that depend on nothing
+    for (int e = tid; e < lists * depth; e += kThreads) {
+        const int l = e / depth, i = e - l * depth;
+        const int64_t at = (entry0 + l) * n + i;
+        front[e].score = (int64_t)__float_as_uint(__ldcg(p.values + at));
+        front[e].index = __ldcg(p.indices + at);
+    }
+    for (int l = tid; l < lists; l += kThreads) counts[l] = __ldcg(p.counts + entry0 + l);
+    // a warp per row: its maximum, and its sum relative to that
+    for (int j = warp; j < p.num_beams; j += kWarps) {
+        const float score = __ldg(p.beam_scores + row0 + j);
+        const bool done = p.finished && __ldg(p.finished + row0 + j);
+        int kind = score > -INFINITY && score < INFINITY ? (done ? 2 : 1) : 0;
         bool bad = !(score < INFINITY);
-        if (!bad && score > -INFINITY) {
-            if (p.finished && __ldg(p.finished + row)) {
-                b.kind = 2;
-            } else {
-                float top = -INFINITY;
-                double total = 0.0;
-                for (int s = 0; s < p.slices; ++s) top = fmaxf(top, __ldcg(p.maxima + (int64_t)row * p.slices + s));
-                for (int s = 0; s < p.slices; ++s) {
-                    const int64_t e = (int64_t)row * p.slices + s;
-                    const double part = __ldcg(p.sums + e);
-                    const float m = __ldcg(p.maxima + e);
-                    total += m == top || part != part ? part : part * exp((double)m - (double)top);
-                }
-                bad = !(top < INFINITY) || total != total;
-                if (!bad && top > -INFINITY) {
-                    b.kind = 1;
-                    b.lse = (double)top + log(total);
+        float top = -INFINITY;
+        unsigned long long total = 0;
+        if (kind == 1) {
+            for (int i = lane; i < p.slices; i += 32)
+                top = fmaxf(top, __ldcg(p.maxima + entry0 + j * p.slices + i));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool far = is_far(top);
+            const float reference = reference_of(top);
+            const float2 *part = p.sums + (int64_t)(row0 + j) * p.row_chunks * kWarps;
+            for (int k = lane; k < p.row_chunks * kWarps; k += 32) {
+                const float2 s = __ldcg(part + k);
+                bad |= !(fabsf(s.y) < INFINITY);
+                if (!far && s.y >= 0.f) {
+                    const float down = reference - s.x;
+                    if (down < 64.f) total += __float2ull_rn(s.y * 4294967296.f) >> (int)down;
+                } else if (s.y != 0.f) {            // the sum's reference above the row's, in powers of two
+                    const float up = s.y > 0.f ? __fmaf_rn(-top, kLog2e, s.x)
+                                     : far     ? (s.x - top) * kLog2e
+                                               : __fmaf_rn(s.x, kLog2e, -reference);
+                    total += __float2ull_rn(fabsf(s.y) * fast_exp2(up) * 4294967296.f);
                 }
             }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            bad = __any_sync(0xffffffffu, bad);
+            if (bad || top == -INFINITY) kind = 0;
         }
-        if (bad) raise_error(p.err, PA_DEVERR_VALUE);
-        beams[j] = b;
+        if (lane == 0) {
+            if (bad) raise_error(p.err, PA_DEVERR_VALUE);
+            beams[j].offset = score;
+            beams[j].total = total;
+            beams[j].top = top;
+            beams[j].kind = kind;
+            beams[j].flat = j * p.vocab;
+        }
     }
     __syncthreads();
-    for (int l = tid; l < lists; l += kThreads) {
-        const int j = l / p.slices, s = l - j * p.slices;
-        const int64_t entry = ((int64_t)g * p.num_beams + j) * p.slices + s;
+    for (int j = tid; j < p.num_beams; j += kThreads) {    // fp64 once for all rows, side by side
+        if (beams[j].kind != 1) continue;
+        const float top = beams[j].top;
+        beams[j].base = is_far(top) ? (double)top : (double)reference_of(top) * (1.0 / (double)kLog2e);
+        beams[j].offset -= log_units(beams[j].total);
+    }
+    __syncthreads();
+    auto candidate = [&](const Beam &b, float v, int32_t token) {
+        Candidate c;
+        c.score = order_of(b.kind == 2 ? b.offset : ((double)v - b.base) + b.offset);
+        c.index = b.flat + (b.kind == 2 ? p.end_token : token);
+        return c;
+    };
+    for (int e = tid; e < lists * depth; e += kThreads) {
+        const int l = e / depth, i = e - l * depth, j = l / p.slices;
+        const Beam &b = beams[j];
+        // an ended beam's one candidate is in its first list
+        const int count = b.kind == 1 ? counts[l] : b.kind == 2 && l == j * p.slices ? 1 : 0;
         Candidate c = {INT64_MIN, INT32_MAX};
-        if (list_count(p, beams[j], entry, s) > 0) c = list_item(p, beams[j], j, entry, 0);
-        heads[l] = c;
+        if (i < count) c = candidate(b, __uint_as_float((uint32_t)front[e].score), front[e].index);
+        front[e] = c;
     }
     __syncthreads();
-    for (int l = tid; l < lists; l += kThreads) {
-        const Candidate mine = heads[l];
+    // the n-th largest of the maxima of 4 n groups of the fronts: a lower bound of
+    // the n-th largest candidate
+    const int groups = n <= 8 ? 32 : n <= 16 ? 64 : n <= 32 ? 128 : 256;
+    if (tid < groups) {
+        Candidate c = {INT64_MIN, INT32_MAX};
+        for (int e = tid; e < lists * depth; e += groups)
+            if (better(front[e], c)) c = front[e];
+        best[tid] = c;
+    }
+    __syncthreads();
+    if (tid < groups) {
+        const Candidate mine = best[tid];
         int rank = 0;
-        for (int t = 0; t < lists; ++t) rank += better(heads[t], mine);
+        for (int t = 0; t < groups; ++t) rank += better(best[t], mine);
         if (rank == n - 1 && mine.score != INT64_MIN) bound = mine;
     }
     __syncthreads();
-    for (int l = tid; l < lists; l += kThreads) {
-        if (heads[l].score == INT64_MIN || better(bound, heads[l])) continue;
-        const int j = l / p.slices, s = l - j * p.slices;
-        const int64_t entry = ((int64_t)g * p.num_beams + j) * p.slices + s;
-        const int count = list_count(p, beams[j], entry, s);
-        for (int i = 0; i < count; ++i) {
-            const Candidate c = list_item(p, beams[j], j, entry, i);
-            if (better(bound, c)) break;
-            found[atomicAdd(&num_found, 1)] = c;
+    int total;
+    while (true) {
+        // the candidates at or above the bound (hardly more than n: the groups are many)
+        const Candidate limit = bound;
+        for (int e = tid; e < lists * n; e += kThreads) {
+            const int l = e / n, i = e - l * n;
+            Candidate c = front[l * depth + min(i, depth - 1)];
+            if (c.score == INT64_MIN || better(limit, c)) continue;
+            if (i >= depth) {                              // behind a front that is all above the bound
+                const Beam &b = beams[l / p.slices];
+                if (b.kind != 1 || i >= counts[l]) continue;
+                const int64_t at = (entry0 + l) * n + i;
+                c = candidate(b, __ldcg(p.values + at), __ldcg(p.indices + at));
+                if (better(limit, c)) continue;
+            }
+            const int at = atomicAdd(&num_found, 1);
+            if (at < kCap) found[at] = c;
         }
+        __syncthreads();
+        total = num_found;
+        if (total <= kCap) break;
+        for (int k = tid; k < kCap; k += kThreads) {       // as in the scan: a higher bound, again
+            const Candidate mine = found[k];
+            int rank = 0;
+            for (int t = 0; t < kCap; ++t) rank += better(found[t], mine);
+            if (rank == n - 1) bound = mine;
+        }
+        __syncthreads();
+        if (tid == 0) num_found = 0;
+        __syncthreads();
     }
-    __syncthreads();
-    const int total = num_found, listed = total < n ? total : n;
-    for (int c = tid; c < total; c += kThreads) {
-        const Candidate mine = found[c];
+    const int listed = total < n ? total : n;
+    for (int k = tid; k < total; k += kThreads) {
+        const Candidate mine = found[k];
         int rank = 0;
         for (int t = 0; t < total; ++t) rank += better(found[t], mine);
         if (rank >= n) continue;
-        chosen[rank] = mine.index;
         const int64_t o = (int64_t)g * n + rank;
         p.scores_out[o] = (float)score_of(mine.score);
         p.parents_out[o] = mine.index / p.vocab;
         p.tokens_out[o] = mine.index % p.vocab;
     }
-    __syncthreads();
-    if (tid == 0 && listed < n) {
-        // every candidate above -inf is listed: the lowest other indices fill up
-        int at = listed;
-        for (int f = 0; at < n; ++f) {
-            bool taken = false;
-            for (int c = 0; c < listed; ++c) taken |= chosen[c] == f;
-            if (taken) continue;
-            const int64_t o = (int64_t)g * n + at++;
-            p.scores_out[o] = -INFINITY;
-            p.parents_out[o] = f / p.vocab;
-            p.tokens_out[o] = f % p.vocab;
-        }
+    if (listed == n || tid != 0) return;
+    // every candidate above -inf is listed: the lowest other indices fill up
+    int at = listed;
+    for (int f = 0; at < n; ++f) {
+        bool taken = false;
+        for (int k = 0; k < listed; ++k) taken |= found[k].index == f;
+        if (taken) continue;
+        const int64_t o = (int64_t)g * n + at++;
+        p.scores_out[o] = -INFINITY;
+        p.parents_out[o] = f / p.vocab;
+        p.tokens_out[o] = f % p.vocab;
     }
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Slices per row: enough CTAs to fill the SMs several times over, none shorter
-// than 4096 elements.
-int beam_slices(int64_t rows, int64_t vocab) {
-    const int64_t want = (4 * 152 + rows - 1) / rows, most = (vocab + 4095) / 4096;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 32}));
+int32_t chunks_of(int32_t vocab, int32_t vec) {
+    return (int32_t)(((int64_t)vocab + (int64_t)vec * kChunk - 1) / ((int64_t)vec * kChunk));
 }
 
-size_t merge_smem(int beams, int slices, int n) {
+// Slices of a row: about four CTAs for each of the GB300's 152 SMs (the
+// workspace is sized without a device at hand), no slice without a chunk.
+int32_t slices_of(int64_t rows, int32_t row_chunks) {
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(row_chunks, (kCtasPerSm * 152 + rows - 1) / rows));
+}
+
+// Front entries of each list: together 4 n or more, or the whole lists.
+int32_t depth_of(int32_t lists, int32_t n) { return std::min(n, (4 * n + lists - 1) / lists); }
+
+size_t merge_smem(int32_t beams, int32_t slices, int32_t n) {
     const int lists = beams * slices;
-    return beams * sizeof(Beam) + (size_t)lists * sizeof(Candidate) + (size_t)n * std::min(n, lists) * sizeof(Candidate) +
-           n * sizeof(int32_t);
+    return ((size_t)lists * depth_of(lists, n) + kCap) * sizeof(Candidate) + beams * sizeof(Beam) +
+           lists * sizeof(int32_t);
 }
 
 }  // namespace
 
+// For either type: fp32's vectors, the shorter ones, make the more chunks.
 size_t beam_workspace(int64_t rows, int32_t vocab, int32_t num_out) {
-    const size_t entries = (size_t)rows * beam_slices(rows, vocab);
-    return round_up(entries * 8) + 2 * round_up(entries * 4) + 2 * round_up(entries * num_out * 4);
+    const int32_t chunks = chunks_of(vocab, 4);
+    const size_t entries = (size_t)rows * slices_of(rows, chunks);
+    return round_up((size_t)rows * chunks * kWarps * sizeof(float2)) + 2 * round_up(entries * 4) + 2 * round_up(entries * num_out * 4);
 }
 
 cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.num_groups * a.num_beams;
+    const int32_t vec = a.bf16 ? 8 : 4;
     BeamParams p = {};
     p.logits = a.logits;
     p.row_stride = a.row_stride;
@@ -465,11 +718,13 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     p.num_beams = a.num_beams;
     p.vocab = a.vocab;
     p.num_out = a.num_out;
-    p.slices = beam_slices(rows, a.vocab);
+    p.row_vectors = (int32_t)(((int64_t)a.vocab + vec - 1) / vec);
+    p.row_chunks = chunks_of(a.vocab, vec);
+    p.slices = slices_of(rows, p.row_chunks);
     const size_t entries = (size_t)rows * p.slices;
     char *w = static_cast<char *>(a.workspace);
-    p.sums = reinterpret_cast<double *>(w);
-    w += round_up(entries * 8);
+    p.sums = reinterpret_cast<float2 *>(w);
+    w += round_up((size_t)rows * p.row_chunks * kWarps * sizeof(float2));
     p.maxima = reinterpret_cast<float *>(w);
     w += round_up(entries * 4);
     p.counts = reinterpret_cast<int32_t *>(w);
@@ -482,16 +737,16 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     p.tokens_out = a.tokens_out;
     p.err = device_error_word();
     if (!p.err) return cudaErrorUnknown;
+    p.depth = depth_of(a.num_beams * p.slices, a.num_out);
     const dim3 grid(p.slices, (unsigned)rows);
-    cudaError_t e = a.bf16 ? launch_pdl(beam_scan_kernel<uint16_t>, grid, dim3(kThreads), stream, p)
-                           : launch_pdl(beam_scan_kernel<float>, grid, dim3(kThreads), stream, p);
+    const auto scan = a.bf16 ? beam_scan_kernel<uint16_t> : beam_scan_kernel<float>;
+    // more than the 48 KB a kernel may take unasked: a setting of the loaded kernel
+    cudaError_t e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScanSmem);
+    if (e == cudaSuccess) e = launch_pdl(scan, grid, dim3(kThreads), stream, kScanSmem, p);
     if (e != cudaSuccess) return e;
+    // (at most 36 KB: 640 lists, 256 front entries beyond them)
     const size_t smem = merge_smem(a.num_beams, p.slices, a.num_out);
-    if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(beam_merge_kernel, dim3(a.num_groups), dim3(kThreads), stream, p, smem);
+    return launch_pdl(beam_merge_kernel, dim3(a.num_groups), dim3(kThreads), stream, smem, p);
 }
 
 }  // namespace pa

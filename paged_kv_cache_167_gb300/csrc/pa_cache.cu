@@ -296,7 +296,7 @@ cudaError_t launch_append_last(const PoolView &pool, const int32_t *tables, int3
     const int64_t cap = (int64_t)device_sm_count() * 8;
     int64_t blocks = (total + threads - 1) / threads;
     if (cap > 0 && blocks > cap) blocks = cap;
-    return launch_pdl(append_last_kernel, dim3((unsigned)blocks), dim3(threads), stream, p);
+    return launch_pdl(append_last_kernel, dim3((unsigned)blocks), dim3(threads), stream, 0, p);
 }
 
 // One CTA waits on a shared-memory barrier that no thread ever arrives at,
@@ -343,7 +343,7 @@ cudaError_t launch_reshape_and_cache(const PoolView &pool, const void *k, const 
     const int64_t max_blocks = (int64_t)device_sm_count() * 8;
     int64_t blocks = (total + threads - 1) / threads;
     if (max_blocks > 0 && blocks > max_blocks) blocks = max_blocks;
-    return launch_pdl(reshape_and_cache_kernel, dim3((unsigned)blocks), dim3(threads), stream, p);
+    return launch_pdl(reshape_and_cache_kernel, dim3((unsigned)blocks), dim3(threads), stream, 0, p);
 }
 
 cudaError_t launch_copy_blocks(const PoolView &pool, const int32_t *pairs, int32_t num_pairs,
@@ -360,7 +360,7 @@ cudaError_t launch_copy_blocks(const PoolView &pool, const int32_t *pairs, int32
     p.pairs = pairs;
     p.num_pairs = num_pairs;
     p.err = err;
-    return launch_pdl(copy_blocks_kernel, dim3(num_pairs, 2), dim3(256), stream, p);
+    return launch_pdl(copy_blocks_kernel, dim3(num_pairs, 2), dim3(256), stream, 0, p);
 }
 
 cudaError_t launch_swap_blocks(const PoolView &pool, void *host_dev, int64_t host_blocks, const int32_t *pairs,
@@ -379,7 +379,7 @@ cudaError_t launch_swap_blocks(const PoolView &pool, void *host_dev, int64_t hos
     p.pairs = pairs;
     p.direction = direction;
     p.err = err;
-    return launch_pdl(swap_blocks_kernel, dim3(num_pairs, 2), dim3(256), stream, p);
+    return launch_pdl(swap_blocks_kernel, dim3(num_pairs, 2), dim3(256), stream, 0, p);
 }
 
 }  // namespace pa

@@ -121,7 +121,7 @@ template <int V, bool INTERLEAVED>
 cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num_seqs, cudaStream_t stream) {
     const size_t smem = (size_t)kTileRows * p.d * 2;       // 32 KB at the widest head
     return launch_pdl(compact_kernel<V, INTERLEAVED>, dim3(num_kv_heads, 2, num_seqs), dim3(kCompactThreads), stream,
-                      p, smem);
+                      smem, p);
 }
 
 }  // namespace

@@ -136,8 +136,9 @@ __device__ __forceinline__ void bulk_g2s(void *smem_dst, const void *gmem_src, u
 
 // Launch with programmatic stream serialisation: the kernel's launch overlaps
 // the previous kernel's tail; its griddepcontrol.wait orders the data.
-template <typename Kernel, typename Arg>
-cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, cudaStream_t stream, const Arg &arg, size_t smem = 0) {
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, size_t smem,
+                       const Args &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -148,7 +149,7 @@ cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, cudaStream_t stream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, arg);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // ---- numeric helpers ------------------------------------------------------

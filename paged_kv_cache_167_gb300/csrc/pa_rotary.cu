@@ -118,8 +118,8 @@ cudaError_t launch_rotate_v(RotateParams &p, int64_t tokens, cudaStream_t stream
     const bool four = wide >= 4ll * device_sm_count();
     const int per = four ? 4 * y : y;
     const dim3 grid((unsigned)tokens, (unsigned)((heads + per - 1) / per), gz), block(x, y);
-    return four ? launch_pdl(rotate_kernel<V, INTERLEAVED, 4, CACHE>, grid, block, stream, p)
-                : launch_pdl(rotate_kernel<V, INTERLEAVED, 1, CACHE>, grid, block, stream, p);
+    return four ? launch_pdl(rotate_kernel<V, INTERLEAVED, 4, CACHE>, grid, block, stream, 0, p)
+                : launch_pdl(rotate_kernel<V, INTERLEAVED, 1, CACHE>, grid, block, stream, 0, p);
 }
 
 template <bool CACHE>

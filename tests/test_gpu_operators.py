@@ -503,6 +503,38 @@ def test_beam_select_crowded_threads(pa, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_beam_select_extreme_values(pa, dtype):
+    """Logits far beyond any model's, up to where fp32 steps exceed any score."""
+    V = 6001
+    x, _ = _random_beams(7, 2, V, seed=8, dtype=torch.float32)
+    x[0] *= 1e9
+    x[1] = torch.sign(x[1]) * 3e37
+    x[2] = x[2] * 1e5 + 2e6
+    x[3] = -3e38
+    x[3, 0, ::3] = -1e30
+    x[4, 0] = 2.0 ** 28
+    x[4, 1] = -(2.0 ** 28)
+    x[5] = x[5].round() + 2.0 ** 22                      # either side of 2^22, fp32 steps of 1/2
+    x[6] = x[6].round() - 2.0 ** 22
+    x = x.to(dtype)
+    s = torch.zeros((7, 2), device="cuda")
+    s[:, 1] = -0.5
+    _check_selection(_select(pa, x, s, 9), x, s, 9, what=f"extreme {dtype}")
+    assert pa.get_device_error() == 0
+
+
+def test_beam_select_equal_rows_at_any_alignment(pa):
+    """Twin beams have equal sums, and so equal scores, wherever their rows
+    begin: their candidates alternate, the lower beam first."""
+    for dtype, V in ((torch.bfloat16, 5003), (torch.float32, 9997), (torch.bfloat16, 40001)):
+        x, s = _random_beams(1, 8, V, seed=9, dtype=dtype)
+        x[0, 1:] = x[0, 0]
+        s.fill_(-3.0)
+        out = _select(pa, x, s, 24)
+        _check_selection(out, x, s, 24, what=f"twins {dtype} {V}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("stride", [2050, 2051, 2500])
 def test_beam_select_strided_rows(pa, stride, dtype):
     V = 2049
