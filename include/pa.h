@@ -586,7 +586,7 @@ pa_status pa_rotate_and_cache(const pa_kv_pool *pool, void *q_out, const void *q
  * raises PA_DEVERR_SEQ_LEN and its sequence is skipped; a bad table entry raises
  * PA_DEVERR_BLOCK_ID and its rows are skipped; the results of that sequence are then
  * undefined, within its own blocks.  head_dim: a multiple of 8, at most 256;
- * num_seqs and num_kv_heads at most 65,535; with rotary, rot_dim <= head_dim.
+ * num_seqs at most 65,535, num_kv_heads at most 32,767; with rotary, rot_dim <= head_dim.
  */
 pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, const int32_t *dst_tables,
                             int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *keep,

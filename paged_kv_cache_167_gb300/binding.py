@@ -487,35 +487,47 @@ def cascade_plan(tables, seq_lens, group_size: int, block_size: int) -> dict:
 
 # ---- rotary positions, compaction and beam selection ------------------------
 
-_NULL = ctypes.c_void_p(0)
+# These calls are short (a few microseconds on the GPU), so their checks are:
+# pointers go to the library as plain integers, and the current stream's handle
+# comes from the call torch's own extensions use.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _same_device(*tensors) -> None:
-    """The library launches on the current device: every tensor has to be there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensors must be on the current device cuda:{cur}, got {t.device}")
+def _handle(stream, device: int) -> int:
+    if stream is None:
+        return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _rows(t: torch.Tensor, name: str):
-    """(pointer, token stride) of a bf16 CUDA tensor [tokens][heads][d] whose
-    tokens may be strided (a view of a fused projection); heads are dense."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+def _refuse(t, dtype, name: str, device: int):
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} must be on the current device cuda:{device}, got {t.device}")
+
+
+def _at(t: torch.Tensor, dtype, name: str, device: int) -> int:
+    """Address of a dense tensor on the current device (where the library launches)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, dtype, name, device)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, device: int):
+    """(address, token stride) of a bf16 tensor [tokens][heads][d] whose tokens
+    may be strided (a view of a fused projection); heads are dense."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.get_device() != device:
+        _refuse(t, torch.bfloat16, name, device)
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
-    if t.numel() and ((d > 1 and s2 != 1) or (h > 1 and s1 != d) or (n > 1 and s0 < h * d)):
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d) or (n > 1 and s0 < h * d):
         raise ValueError(f"{name} must be [tokens][heads][head_dim] with dense heads")
-    return ctypes.c_void_p(t.data_ptr()), (s0 if n > 1 else 0)
+    return t.data_ptr(), (s0 if n > 1 else 0)
 
 
-def _rotary(freqs: torch.Tensor, interleaved: bool, mscale: float, inverse: bool = False) -> PaRotary:
-    turns = _dev(freqs, torch.int64, "freqs")
+def _rotary(freqs: torch.Tensor, interleaved: bool, mscale: float, device: int, inverse: bool = False) -> PaRotary:
     flags = (PA_ROTARY_INTERLEAVED if interleaved else 0) | (PA_ROTARY_INVERSE if inverse else 0)
-    return PaRotary(turns, 2 * freqs.numel(), flags, mscale)
+    return PaRotary(_at(freqs, torch.int64, "freqs", device), 2 * freqs.numel(), flags, mscale)
 
 
 def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -547,11 +559,12 @@ def rotate(out: torch.Tensor, x: torch.Tensor, positions: torch.Tensor, freqs: t
     ``positions`` (int64) into the dense ``out``, which may be x itself."""
     if x.dim() != 3 or out.shape != x.shape or positions.numel() != x.shape[0]:
         raise ValueError("x and out must be [tokens][heads][head_dim] with one position per token")
-    src, stride = _rows(x, "x")
-    _same_device(out, x, positions, freqs)
-    rot = _rotary(freqs, interleaved, mscale, inverse)
-    _check(lib().pa_rotate(_dev(out, torch.bfloat16, "out"), src, stride, _dev(positions, torch.int64, "positions"),
-                           x.shape[0], x.shape[1], x.shape[2], ctypes.byref(rot), _stream(stream)), "pa_rotate")
+    dev = torch.cuda.current_device()
+    src, stride = _rows(x, "x", dev)
+    rot = _rotary(freqs, interleaved, mscale, dev, inverse)
+    _check(lib().pa_rotate(_at(out, torch.bfloat16, "out", dev), src, stride,
+                           _at(positions, torch.int64, "positions", dev), x.shape[0], x.shape[1], x.shape[2],
+                           ctypes.byref(rot), _handle(stream, dev)), "pa_rotate")
 
 
 def rotate_and_cache(pool: torch.Tensor, q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor,
@@ -564,25 +577,29 @@ def rotate_and_cache(pool: torch.Tensor, q_out: Optional[torch.Tensor], q: Optio
     desc = pool_desc(pool, layer)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
-    n = k.shape[0]
-    if k.dim() != 3 or v.shape != k.shape or tuple(k.shape[1:]) != (desc.num_kv_heads, desc.head_dim):
+    shape = k.shape
+    n = shape[0]
+    if len(shape) != 3 or v.shape != shape or shape[1] != desc.num_kv_heads or shape[2] != desc.head_dim:
         raise ValueError("k and v must be [tokens][num_kv_heads][head_dim]")
     if positions.numel() != n or slot_mapping.numel() != n:
         raise ValueError("positions and slot_mapping must hold one entry per token")
-    _same_device(pool, q_out, q, k, v, positions, slot_mapping, freqs)
-    kp, ks = _rows(k, "k")
-    vp, vs = _rows(v, "v")
-    qo, qp, qs, hq = _NULL, _NULL, 0, 0
+    dev = torch.cuda.current_device()
+    if pool.get_device() != dev:
+        _refuse(pool, torch.bfloat16, "pool", dev)
+    kp, ks = _rows(k, "k", dev)
+    vp, vs = _rows(v, "v", dev)
+    qo, qp, qs, hq = None, None, 0, 0
     if q is not None:
-        if q.dim() != 3 or q_out.shape != q.shape or q.shape[0] != n or q.shape[2] != desc.head_dim:
+        shape = q.shape
+        if len(shape) != 3 or q_out.shape != shape or shape[0] != n or shape[2] != desc.head_dim:
             raise ValueError("q and q_out must be [tokens][num_q_heads][head_dim]")
-        qp, qs = _rows(q, "q")
-        qo, hq = _dev(q_out, torch.bfloat16, "q_out"), q.shape[1]
-    rot = _rotary(freqs, interleaved, mscale)
+        qp, qs = _rows(q, "q", dev)
+        qo, hq = _at(q_out, torch.bfloat16, "q_out", dev), shape[1]
+    rot = _rotary(freqs, interleaved, mscale, dev)
     _check(lib().pa_rotate_and_cache(ctypes.byref(desc), qo, qp, qs, kp, ks, vp, vs,
-                                     _dev(positions, torch.int64, "positions"),
-                                     _dev(slot_mapping, torch.int64, "slot_mapping"), n, hq, ctypes.byref(rot),
-                                     _stream(stream)), "pa_rotate_and_cache")
+                                     _at(positions, torch.int64, "positions", dev),
+                                     _at(slot_mapping, torch.int64, "slot_mapping", dev), n, hq, ctypes.byref(rot),
+                                     _handle(stream, dev)), "pa_rotate_and_cache")
 
 
 def compact_tokens(pool: torch.Tensor, src_tables: torch.Tensor, dst_tables: torch.Tensor, seq_lens: torch.Tensor,
@@ -593,21 +610,25 @@ def compact_tokens(pool: torch.Tensor, src_tables: torch.Tensor, dst_tables: tor
     (src_tables) to starts[s] + i (dst_tables; the same tensor compacts in
     place).  freqs: turn the keys to their new positions."""
     desc = pool_desc(pool, layer)
-    B = src_tables.shape[0]
-    if src_tables.dim() != 2 or dst_tables.shape != src_tables.shape:
+    shape = src_tables.shape
+    if len(shape) != 2 or dst_tables.shape != shape:
         raise ValueError("src_tables and dst_tables must be [num_seqs][max_blocks] of one shape")
+    B = shape[0]
     if keep.dim() != 2 or keep.shape[0] != B or keep_lens.numel() != B or seq_lens.numel() != B:
         raise ValueError("keep, keep_lens and seq_lens do not match the batch")
     if starts is not None and starts.numel() != B:
         raise ValueError("starts must hold one entry per sequence")
-    _same_device(pool, src_tables, dst_tables, seq_lens, keep, keep_lens, starts, freqs)
-    rot = ctypes.byref(_rotary(freqs, interleaved, 1.0)) if freqs is not None else None
-    _check(lib().pa_compact_tokens(ctypes.byref(desc), _dev(src_tables, torch.int32, "src_tables"),
-                                   _dev(dst_tables, torch.int32, "dst_tables"), src_tables.shape[1],
-                                   _dev(seq_lens, torch.int32, "seq_lens"), _dev(keep, torch.int32, "keep"),
-                                   keep.shape[1], _dev(keep_lens, torch.int32, "keep_lens"),
-                                   _dev(starts, torch.int32, "starts") if starts is not None else _NULL, B, rot,
-                                   _stream(stream)), "pa_compact_tokens")
+    dev = torch.cuda.current_device()
+    if pool.get_device() != dev:
+        _refuse(pool, torch.bfloat16, "pool", dev)
+    i32 = torch.int32
+    rot = ctypes.byref(_rotary(freqs, interleaved, 1.0, dev)) if freqs is not None else None
+    _check(lib().pa_compact_tokens(ctypes.byref(desc), _at(src_tables, i32, "src_tables", dev),
+                                   _at(dst_tables, i32, "dst_tables", dev), shape[1],
+                                   _at(seq_lens, i32, "seq_lens", dev), _at(keep, i32, "keep", dev), keep.shape[1],
+                                   _at(keep_lens, i32, "keep_lens", dev),
+                                   _at(starts, i32, "starts", dev) if starts is not None else None, B, rot,
+                                   _handle(stream, dev)), "pa_compact_tokens")
 
 
 def beam_select_workspace_size(num_groups: int, num_beams: int, vocab: int, num_out: int) -> int:
@@ -624,32 +645,35 @@ def beam_select(scores_out: torch.Tensor, parents_out: torch.Tensor, tokens_out:
     if logits.dim() != 3 or beam_scores.shape != logits.shape[:2]:
         raise ValueError("logits must be [groups][beams][vocab] and beam_scores [groups][beams]")
     G, J, V = logits.shape
-    if scores_out.dim() != 2 or scores_out.shape[0] != G or parents_out.shape != scores_out.shape or \
-            tokens_out.shape != scores_out.shape:
+    shape = scores_out.shape
+    if len(shape) != 2 or shape[0] != G or parents_out.shape != shape or tokens_out.shape != shape:
         raise ValueError("scores_out, parents_out and tokens_out must be [groups][num_out]")
-    if not logits.is_cuda:
-        raise TypeError("logits must be a CUDA tensor")
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    s0, s1, s2 = logits.stride()
-    stride = s1 if J > 1 else s0 if G > 1 else V
-    if logits.numel() and ((V > 1 and s2 != 1) or stride < V or (J > 1 and G > 1 and s0 != J * s1)):
-        raise ValueError("logits must be rows of dense vocabularies, evenly strided")
-    done = _NULL
+    dev = torch.cuda.current_device()
+    kind = logits.dtype
+    if kind != torch.bfloat16 and kind != torch.float32:
+        raise TypeError(f"logits must be bfloat16 or float32, got {kind}")
+    if logits.get_device() != dev:
+        _refuse(logits, kind, "logits", dev)
+    stride = V
+    if not logits.is_contiguous():
+        s0, s1, s2 = logits.stride()
+        stride = s1 if J > 1 else s0 if G > 1 else V
+        if (V > 1 and s2 != 1) or stride < V or (J > 1 and G > 1 and s0 != J * s1):
+            raise ValueError("logits must be rows of dense vocabularies, evenly strided")
+    done = None
     if finished is not None:
         if finished.shape != beam_scores.shape or finished.dtype not in (torch.uint8, torch.bool):
             raise ValueError("finished must be uint8 or bool [groups][beams]")
-        done = _dev(finished, finished.dtype, "finished")
-    _same_device(scores_out, parents_out, tokens_out, logits, beam_scores, finished, workspace)
-    ws_ptr, ws_bytes = _NULL, 0
+        done = _at(finished, finished.dtype, "finished", dev)
+    ws, ws_bytes = None, 0
     if workspace is not None:
-        ws_ptr, ws_bytes = _dev(workspace, torch.uint8, "workspace"), workspace.numel()
-    _check(lib().pa_beam_select(_dev(scores_out, torch.float32, "scores_out"),
-                                _dev(parents_out, torch.int32, "parents_out"),
-                                _dev(tokens_out, torch.int32, "tokens_out"), ctypes.c_void_p(logits.data_ptr()),
-                                PA_DTYPE_BF16 if logits.dtype == torch.bfloat16 else PA_DTYPE_F32, stride,
-                                _dev(beam_scores, torch.float32, "beam_scores"), done, int(end_token), G, J, V,
-                                scores_out.shape[1], ws_ptr, ws_bytes, _stream(stream)), "pa_beam_select")
+        ws, ws_bytes = _at(workspace, torch.uint8, "workspace", dev), workspace.numel()
+    _check(lib().pa_beam_select(_at(scores_out, torch.float32, "scores_out", dev),
+                                _at(parents_out, torch.int32, "parents_out", dev),
+                                _at(tokens_out, torch.int32, "tokens_out", dev), logits.data_ptr(),
+                                PA_DTYPE_BF16 if kind == torch.bfloat16 else PA_DTYPE_F32, stride,
+                                _at(beam_scores, torch.float32, "beam_scores", dev), done, end_token, G, J, V,
+                                shape[1], ws, ws_bytes, _handle(stream, dev)), "pa_beam_select")
 
 
 def check_wait_timeout(limit_ns: int, stream=None) -> None:

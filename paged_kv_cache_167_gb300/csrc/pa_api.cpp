@@ -501,7 +501,7 @@ pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, c
     pa_status st = resolve_pool(pool, &view);
     if (st != PA_OK) return st;
     if (view.head_dim > 256) return PA_ERR_UNSUPPORTED;
-    if (num_seqs < 0 || num_seqs > 65535 || max_keep < 0 || view.num_kv_heads > 65535) return PA_ERR_INVALID_ARG;
+    if (num_seqs < 0 || num_seqs > 65535 || max_keep < 0 || view.num_kv_heads > 32767) return PA_ERR_INVALID_ARG;
     if (rotary && !rotary_ok(rotary, view.head_dim)) return PA_ERR_INVALID_ARG;
     if (num_seqs == 0 || max_keep == 0) return PA_OK;
     if (!src_tables || !dst_tables || !seq_lens || !keep || !keep_lens || max_blocks_per_seq <= 0)

@@ -1,25 +1,40 @@
 // pa_compact.cu -- compaction of a sequence's kept tokens to consecutive
 // positions, in place or into other blocks, keys re-rotated on the way.
 //
-// One CTA walks the rows of one (sequence, K or V, kv-head) in tiles of
-// kTileRows: the tile's rows are gathered into shared memory, and only then
-// written.  In place that order is enough: row i is written at position
-// start + i <= keep[i] < keep[i + 1], so no later tile reads what an earlier
-// one has written, and within a tile every row is read before any is written.
+// The rows of one (sequence, K or V, kv-head) are taken in tiles of up to 16 KB.
+// A tile is gathered into shared memory by asynchronous 16-byte copies, two tiles
+// ahead of the one being written; the positions and table entries that say where
+// its rows lie are fetched further ahead still, so that no step waits for that
+// chain of loads.
+//
+// In place, row i is written at start + i <= keep[i] < keep[i + 1]: what a tile
+// writes lies before everything that later tiles read, so it is enough that a
+// tile is written only when it and all earlier ones have been read.  One CTA has
+// that from a barrier per tile.  Where there are too few (sequence, K or V,
+// head) for the SMs, a cluster of up to 16 CTAs takes the tiles in turn, and the
+// barrier is the cluster's (arrived at for one tile while the one before is
+// written); out of place the tiles are free of one another and any number of CTAs
+// share them.  The cluster's barrier is a relaxed one: what it
+// orders are reads that have ended (their bytes are in shared memory) before
+// writes that have not begun; nobody reads what was written, so no store has to
+// be waited for.
+#include <algorithm>
+
 #include "pa_internal.h"
 #include "pa_rotary.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kTileRows = 64;
-constexpr int kCompactThreads = 256;
+constexpr int kLoads = 4;                                  // 16-byte copies a thread has in a tile
+constexpr int kMaxRows = 96;
 
 struct CompactParams {
     uint16_t *pool;
     int64_t num_blocks;
     int64_t block_stride, kv_stride;   // elements
     int32_t block_size, d;
+    int32_t block_log;                 // of a block_size that is a power of two, else -1
     const int32_t *src_tables, *dst_tables;
     int32_t max_blocks;
     const int32_t *seq_lens;
@@ -29,25 +44,46 @@ struct CompactParams {
     const int32_t *starts;             // may be null
     const uint64_t *turns;             // null: keys move as they are
     int32_t rot_chunks, chunks;        // of a key row, V pairs or V components each
+    int32_t rows;                      // of a tile
     unsigned int *err;
 };
 
-// grid (kv-head, 2, sequence)
-template <int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactParams p) {
+__device__ __forceinline__ void copy_async(uint4 *to, const uint16_t *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// What is being found out about one row, one step of the chain after another.
+struct RowLookup {
+    int32_t from = -1, to = 0;         // from -1: no such row, or a bad one
+    int32_t src_block = -1, dst_block = -1;
+};
+
+// grid (CTAs of one unit, 2 x kv-head, sequence); CLUSTER: they are a cluster
+// and write in order, else each goes its own way (one CTA, or out of place).
+// STAGES tiles are in shared memory or on their way there.
+template <int V, bool INTERLEAVED, int THREADS, int STAGES, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 8) compact_kernel(const CompactParams p) {
     using Vec = typename BfVec<V>::type;
-    extern __shared__ __align__(16) uint16_t tile[];         // [kTileRows][d]
-    __shared__ int64_t src_row[kTileRows], dst_row[kTileRows];   // element offsets; -1: the row stays
-    __shared__ int32_t shift[kTileRows];
+    constexpr int kRings = STAGES + 2;                     // tiles whose rows' places are known
+    extern __shared__ __align__(16) uint4 ring[];          // [STAGES][rows][row_vecs], then the rows' places
+    const int row_vecs = p.d / 8, tile_vecs = p.rows * row_vecs;
+    int64_t *src_rows = reinterpret_cast<int64_t *>(ring + STAGES * tile_vecs);   // [kRings][rows]; -1: stays
+    int64_t *dst_rows = src_rows + kRings * p.rows;
+    int32_t *shifts = reinterpret_cast<int32_t *>(dst_rows + kRings * p.rows);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int h = blockIdx.x, kv = blockIdx.y, s = blockIdx.z;
-    const int tid = threadIdx.x;
+    const int kv = blockIdx.y & 1, h = blockIdx.y >> 1, s = blockIdx.z, tid = threadIdx.x;
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
     const int64_t len = __ldg(p.seq_lens + s), n = __ldg(p.keep_lens + s);
     const int64_t start = p.starts ? __ldg(p.starts + s) : 0;
+    const bool reports = h == 0 && kv == 0;
     if (len < 0 || len > cap || n < 0 || n > p.max_keep || start < 0) {
-        if (tid == 0 && h == 0 && kv == 0) raise_error(p.err, PA_DEVERR_SEQ_LEN);
+        if (tid == 0 && reports && blockIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_LEN);
         return;
     }
     const int32_t *keep = p.keep + (int64_t)s * p.max_keep;
@@ -55,73 +91,194 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
     const int32_t *dst_table = p.dst_tables + (int64_t)s * p.max_blocks;
     const int64_t base = kv * p.kv_stride + (int64_t)h * p.block_size * p.d;
     const bool turn = p.turns != nullptr && kv == 0;
-    const int row_vecs = p.d / 8;
-    for (int64_t i0 = 0; i0 < n; i0 += kTileRows) {
-        const int rows = (int)(n - i0 < kTileRows ? n - i0 : kTileRows);
-        if (tid < rows) {
-            const int64_t i = i0 + tid, to = start + i;
-            const int64_t from = __ldg(keep + i);
-            const int64_t before = i > 0 ? __ldg(keep + i - 1) : -1;
-            int64_t src = -1, dst = -1;
-            if (from <= before || from < to || from >= len) {
-                if (h == 0 && kv == 0) raise_error(p.err, PA_DEVERR_KEEP);
-            } else {
-                const int sb = __ldg(src_table + from / p.block_size), db = __ldg(dst_table + to / p.block_size);
-                if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
-                    if (h == 0 && kv == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
-                } else if (from != to || sb != db) {
-                    src = sb * p.block_stride + base + (from % p.block_size) * p.d;
-                    dst = db * p.block_stride + base + (to % p.block_size) * p.d;
-                }
-            }
-            src_row[tid] = src;
-            dst_row[tid] = dst;
-            shift[tid] = (int32_t)(to - from);
+    const int32_t tiles = (int32_t)((n + p.rows - 1) / p.rows);
+    const int32_t steps = (tiles - (CLUSTER ? 0 : (int)blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
+    const bool looks = tid < p.rows;
+
+    // The chain behind a row's place: keep -> table entries -> offsets, one call
+    // (and one step of the loop below) each.  Threads 0 .. rows - 1 take a row.
+    int64_t next_row = (int64_t)blockIdx.x * p.rows + tid;   // of the next look_keep
+    auto look_keep = [&]() {
+        RowLookup r;
+        const int64_t i = next_row;
+        next_row += (int64_t)gridDim.x * p.rows;
+        if (!looks || i >= n) return r;
+        const int32_t before = i > 0 ? __ldg(keep + i - 1) : -1, from = __ldg(keep + i);
+        if (from <= before || from < start + i || from >= len) {
+            if (reports) raise_error(p.err, PA_DEVERR_KEEP);
+            return r;
         }
-        __syncthreads();
-        for (int e = tid; e < rows * row_vecs; e += kCompactThreads) {
-            const int r = e / row_vecs, c = e - r * row_vecs;
-            if (src_row[r] >= 0)
-                reinterpret_cast<uint4 *>(tile)[e] = *reinterpret_cast<const uint4 *>(p.pool + src_row[r] + c * 8);
+        r.from = from;
+        r.to = (int32_t)(start + i);                       // <= from
+        return r;
+    };
+    auto block_of = [&](int32_t t) {
+        return p.block_log >= 0 ? (uint32_t)t >> p.block_log : (uint32_t)t / (uint32_t)p.block_size;
+    };
+    auto look_blocks = [&](RowLookup r) {
+        if (r.from >= 0) {
+            r.src_block = __ldg(src_table + block_of(r.from));
+            r.dst_block = __ldg(dst_table + block_of(r.to));
         }
-        __syncthreads();
-        if (!turn) {
-            for (int e = tid; e < rows * row_vecs; e += kCompactThreads) {
-                const int r = e / row_vecs, c = e - r * row_vecs;
-                if (src_row[r] >= 0)
-                    *reinterpret_cast<uint4 *>(p.pool + dst_row[r] + c * 8) = reinterpret_cast<const uint4 *>(tile)[e];
+        return r;
+    };
+    auto put_row = [&](int slot, const RowLookup &r) {
+        if (!looks) return;
+        int64_t src = -1, dst = -1;
+        if (r.from >= 0) {
+            if (r.src_block < 0 || r.src_block >= p.num_blocks || r.dst_block < 0 || r.dst_block >= p.num_blocks) {
+                if (reports) raise_error(p.err, PA_DEVERR_BLOCK_ID);
+            } else if (r.from != r.to || r.src_block != r.dst_block) {
+                src = r.src_block * p.block_stride + base + (r.from - (int)block_of(r.from) * p.block_size) * p.d;
+                dst = r.dst_block * p.block_stride + base + (r.to - (int)block_of(r.to) * p.block_size) * p.d;
             }
-        } else {
-            const int half = p.rot_chunks * V;
-            for (int e = tid; e < rows * p.chunks; e += kCompactThreads) {
-                const int r = e / p.chunks, c = e - r * p.chunks;
-                if (src_row[r] < 0) continue;
-                const uint16_t *from = tile + r * p.d;
-                uint16_t *to = p.pool + dst_row[r];
-                if (c >= p.rot_chunks) {
-                    const int at = 2 * half + (c - p.rot_chunks) * V;
-                    *reinterpret_cast<Vec *>(to + at) = *reinterpret_cast<const Vec *>(from + at);
-                    continue;
-                }
-                const int at0 = INTERLEAVED ? 2 * c * V : c * V, at1 = INTERLEAVED ? at0 + V : half + at0;
-                Vec lo = *reinterpret_cast<const Vec *>(from + at0), hi = *reinterpret_cast<const Vec *>(from + at1);
-                float2 cs[V];
+        }
+        const int at = slot * p.rows + tid;
+        src_rows[at] = src;
+        dst_rows[at] = dst;
+        shifts[at] = r.to - r.from;
+    };
+
+    // this thread's vectors of a tile: (row, vector of the row), the same in all
+    int row_of[kLoads], vec_of[kLoads];
 #pragma unroll
-                for (int i = 0; i < V; ++i) cs[i] = rotary_cos_sin(shift[r], __ldg(p.turns + c * V + i), 1.f);
-                rotate_pairs<V, INTERLEAVED>(lo, hi, cs);
+    for (int u = 0; u < kLoads; ++u) {
+        row_of[u] = (tid + u * THREADS) / row_vecs;
+        vec_of[u] = (tid + u * THREADS) - row_of[u] * row_vecs;
+    }
+    auto begin_copies = [&](int32_t k, int stage, int slot) {
+        if (k < steps) {
+            const int64_t *src = src_rows + slot * p.rows;
+            uint4 *tile = ring + stage * tile_vecs + tid;
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u)
+                if (row_of[u] < p.rows && src[row_of[u]] >= 0)
+                    copy_async(tile + u * THREADS, p.pool + src[row_of[u]] + vec_of[u] * 8);
+        }
+        copy_commit();                                     // (an empty group where nothing is left)
+    };
+    auto next = [](int i, int count) { return i + 1 == count ? 0 : i + 1; };
+
+    // this thread's chunk of the rows it turns: every `apart`-th row from `row0` on
+    const int apart = turn ? THREADS / p.chunks : 1, row0 = turn ? tid / p.chunks : 0, c = turn ? tid - row0 * p.chunks : 0;
+    const bool turning = turn && row0 < apart && c < p.rot_chunks, passing = turn && row0 < apart && !turning;
+    float2 cs[V];
+    int32_t turned = 0;                                    // the shift that cs belongs to
+    const int half = p.rot_chunks * V;
+    const int at0 = !turning ? 2 * half + (c - p.rot_chunks) * V : INTERLEAVED ? 2 * c * V : c * V;
+    const int at1 = INTERLEAVED ? at0 + V : half + at0;
+
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) put_row(k, look_blocks(look_keep()));
+    RowLookup blocks = look_blocks(look_keep()), kept = look_keep();   // of tiles STAGES and STAGES + 1
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) begin_copies(k, k, k);
+    if (steps <= 0) return;                                // (the same for a whole cluster; nothing is under way)
+    copy_wait<STAGES - 2>();                               // tile 0 has landed
+    if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    int stage = 0, ahead = STAGES - 1;                     // tile k's place, and tile k + STAGES - 1's
+    int slot = 0, slot_ahead = STAGES - 1, slot_put = STAGES;
+    for (int32_t k = 0; k < steps; ++k) {
+        if (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // tile k has landed everywhere
+        __syncthreads();
+        begin_copies(k + STAGES - 1, ahead, slot_ahead);   // into the place of tile k - 1, written before the barrier
+        copy_wait<STAGES - 2>();                           // tile k + 1 has landed: said while tile k is written
+        if (CLUSTER && k + 1 < steps) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+        put_row(slot_put, blocks);                         // of tile k + STAGES
+        blocks = look_blocks(kept);
+        kept = look_keep();
+        const int64_t *src = src_rows + slot * p.rows, *dst = dst_rows + slot * p.rows;
+        const int32_t *shift_of = shifts + slot * p.rows;
+        const uint4 *tile = ring + stage * tile_vecs;
+        stage = next(stage, STAGES);
+        ahead = next(ahead, STAGES);
+        slot = next(slot, kRings);
+        slot_ahead = next(slot_ahead, kRings);
+        slot_put = next(slot_put, kRings);
+        if (!turn) {
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u)
+                if (row_of[u] < p.rows && src[row_of[u]] >= 0)
+                    *reinterpret_cast<uint4 *>(p.pool + dst[row_of[u]] + vec_of[u] * 8) = tile[tid + u * THREADS];
+            continue;
+        }
+        for (int r = row0; r < p.rows; r += apart) {
+            if (src[r] < 0) continue;
+            const uint16_t *from = reinterpret_cast<const uint16_t *>(tile) + r * p.d;
+            uint16_t *to = p.pool + dst[r];
+            if (turning) {
+                Vec lo = *reinterpret_cast<const Vec *>(from + at0), hi = *reinterpret_cast<const Vec *>(from + at1);
+                const int32_t shift = shift_of[r];
+                if (shift != 0) {                          // (0: into another block at its old position)
+                    if (shift != turned) {                 // a window slides by one distance: once for all its rows
+#pragma unroll
+                        for (int i = 0; i < V; ++i) cs[i] = rotary_cos_sin(shift, __ldg(p.turns + c * V + i), 1.f);
+                        turned = shift;
+                    }
+                    rotate_pairs<V, INTERLEAVED>(lo, hi, cs);
+                }
                 *reinterpret_cast<Vec *>(to + at0) = lo;
                 *reinterpret_cast<Vec *>(to + at1) = hi;
+            } else if (passing) {
+                *reinterpret_cast<Vec *>(to + at0) = *reinterpret_cast<const Vec *>(from + at0);
             }
         }
-        __syncthreads();
     }
+    copy_wait<0>();
+}
+
+template <int V, bool INTERLEAVED, int THREADS, int STAGES, bool CLUSTER>
+cudaError_t launch_compact_as(const CompactParams &p, int x, int32_t num_kv_heads, int32_t num_seqs,
+                              cudaStream_t stream) {
+    const auto kernel = compact_kernel<V, INTERLEAVED, THREADS, STAGES, CLUSTER>;
+    const size_t smem = (size_t)STAGES * p.rows * (p.d / 8) * sizeof(uint4) +
+                        (size_t)(STAGES + 2) * p.rows * (2 * sizeof(int64_t) + sizeof(int32_t));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(x, 2 * num_kv_heads, num_seqs);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = x;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    if (CLUSTER && x > 8) {                                // 16 CTAs a cluster is an opt-in
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int V, bool INTERLEAVED>
 cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num_seqs, cudaStream_t stream) {
-    const size_t smem = (size_t)kTileRows * p.d * 2;       // 32 KB at the widest head
-    return launch_pdl(compact_kernel<V, INTERLEAVED>, dim3(num_kv_heads, 2, num_seqs), dim3(kCompactThreads), stream,
-                      smem, p);
+    const int row_vecs = p.d / 8;
+    if (p.max_keep <= 32 && p.max_keep * row_vecs <= 32 * kLoads && p.chunks <= 32) {
+        // a few rows a sequence (accepted drafts): one warp has them in one tile,
+        // and all units are on the SMs at once
+        p.rows = p.max_keep;
+        return launch_compact_as<V, INTERLEAVED, 32, 2, false>(p, 1, num_kv_heads, num_seqs, stream);
+    }
+    p.rows = std::min({256 * kLoads / row_vecs, kMaxRows, p.max_keep});
+    // CTAs a unit, no more than there are tiles: out of place enough to give every
+    // SM four; in place the largest cluster that leaves every SM about two to four
+    const int64_t units = 2ll * num_kv_heads * num_seqs, tiles = ((int64_t)p.max_keep + p.rows - 1) / p.rows;
+    const int sms = device_sm_count();
+    if (p.src_tables != p.dst_tables) {
+        const int x = (int)std::min<int64_t>(tiles, (4 * sms + units - 1) / units);
+        return launch_compact_as<V, INTERLEAVED, 256, 3, false>(p, x, num_kv_heads, num_seqs, stream);
+    }
+    int x = 1;
+    while (x < 16 && x < tiles && units * x < 2 * sms) x *= 2;
+    return x == 1 ? launch_compact_as<V, INTERLEAVED, 256, 3, false>(p, x, num_kv_heads, num_seqs, stream)
+                  : launch_compact_as<V, INTERLEAVED, 256, 3, true>(p, x, num_kv_heads, num_seqs, stream);
 }
 
 }  // namespace
@@ -136,6 +293,9 @@ cudaError_t launch_compact(const PoolView &pool, const int32_t *src_tables, cons
     p.block_stride = pool.block_stride;
     p.kv_stride = pool.kv_stride;
     p.block_size = pool.block_size;
+    p.block_log = -1;
+    for (int i = 0; i < 31; ++i)
+        if (pool.block_size == 1 << i) p.block_log = i;
     p.d = pool.head_dim;
     p.src_tables = src_tables;
     p.dst_tables = dst_tables;
