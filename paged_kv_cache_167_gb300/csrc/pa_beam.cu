@@ -14,9 +14,10 @@
 //    it came from.  The n-th largest of the maxima of 4 n groups of threads is a
 //    lower bound of the slice's n-th largest element (and close to it: some 9
 //    elements reach it at n = 8), so only the few threads whose maximum reaches it
-//    can hold a candidate: their elements (and no others) are read again, from
-//    cache, and those at or above the bound are ranked.  Keys are (value, lower
-//    index first), so they are unique and ties need no further rule.
+//    can hold a candidate: their four vectors of that chunk (and the others only
+//    if the second best chunk reaches it too) are read again, from cache, and the
+//    elements at or above the bound are ranked.  Keys are (value, lower index
+//    first), so they are unique and ties need no further rule.
 // 2. merge: one CTA per group adds up each row's partial sums, turns the
 //    slices' lists (each sorted) into fp64 scores and picks the n best by the
 //    same bound, taken over the lists' heads.
@@ -296,8 +297,9 @@ __device__ __forceinline__ float2 chunk_sum(const uint4 (&v)[kUnroll], float top
 
 struct ScanShared {
     __align__(16) uint64_t keys[kCap];              // the groups' bounds first, then the candidates
-    int32_t holders[kThreads];
-    int num_holders, num_found;
+    int32_t holders[kThreads];                      // of candidates in one chunk: chunk * kThreads + thread
+    int32_t rich[kThreads];                         // in more than one: the thread
+    int num_holders, num_rich, num_found;
     uint64_t bound;
     float warp_max[kWarps];
 };
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const B
         }
         copy_commit();                              // (an empty group where nothing is left)
     };
-    float m = -INFINITY;
+    float m = -INFINITY, second = -INFINITY;        // the largest of the chunks' maxima, and of the others'
     int32_t best = first;
     float2 *sums = p.sums + ((int64_t)row * p.row_chunks + first) * kWarps + warp;
 #pragma unroll
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const B
         __syncwarp();                               // every lane has read what its neighbours copied
         start(k + kStages);
         const float top = E::maximum(v);
+        second = fmaxf(second, fminf(m, top));
         if (top > m) {
             m = top;
             best = k;
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const B
     if ((tid & ((1 << group_log) - 1)) == 0) sh.keys[tid >> group_log] = group;
     if (tid == 0) {
         sh.bound = kLeastKey;
-        sh.num_holders = sh.num_found = 0;
+        sh.num_holders = sh.num_rich = sh.num_found = 0;
     }
     __syncthreads();
     if (tid < groups) {                             // the n-th largest of the groups' bounds
@@ -417,21 +420,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const B
     int found;
     while (true) {
         const uint64_t limit = sh.bound;
-        if (most >= limit) sh.holders[atomicAdd(&sh.num_holders, 1)] = tid;
+        if (most >= limit) {
+            if (second > -INFINITY && order_of(second) >= (uint32_t)(limit >> 32))
+                sh.rich[atomicAdd(&sh.num_rich, 1)] = tid;
+            else
+                sh.holders[atomicAdd(&sh.num_holders, 1)] = best * kThreads + tid;
+        }
         __syncthreads();
-        for (int h = warp; h < sh.num_holders; h += kWarps)
-            for (int32_t j = first * kChunk + sh.holders[h] + lane * kThreads; j < end; j += 32 * kThreads) {
-                float e[VN];
-                E::unpack(x.load(j), e);
+        auto collect = [&](int32_t j) {
+            float e[VN];
+            E::unpack(x.load(j), e);
 #pragma unroll
-                for (int i = 0; i < VN; ++i) {
-                    const uint64_t key = key_of(order_of(e[i]), (uint32_t)j * VN + i);
-                    if (e[i] > -INFINITY && key >= limit) {
-                        const int at = atomicAdd(&sh.num_found, 1);
-                        if (at < kCap) sh.keys[at] = key;
-                    }
+            for (int i = 0; i < VN; ++i) {
+                const uint64_t key = key_of(order_of(e[i]), (uint32_t)j * VN + i);
+                if (e[i] > -INFINITY && key >= limit) {
+                    const int to = atomicAdd(&sh.num_found, 1);
+                    if (to < kCap) sh.keys[to] = key;
                 }
             }
+        };
+        for (int i = tid; i < sh.num_holders * kUnroll; i += kThreads) {
+            const int32_t h = sh.holders[i / kUnroll];
+            const int32_t j = h / kThreads * kChunk + i % kUnroll * kThreads + h % kThreads;
+            if (j < end) collect(j);
+        }
+        for (int h = warp; h < sh.num_rich; h += kWarps)
+            for (int32_t j = first * kChunk + sh.rich[h] + lane * kThreads; j < end; j += 32 * kThreads) collect(j);
         __syncthreads();
         found = sh.num_found;
         if (found <= kCap) break;
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const B
             if (rank == n - 1) sh.bound = mine;
         }
         __syncthreads();
-        if (tid == 0) sh.num_holders = sh.num_found = 0;
+        if (tid == 0) sh.num_holders = sh.num_rich = sh.num_found = 0;
         __syncthreads();
     }
     for (int k = tid; k < found; k += kThreads) {
@@ -506,6 +520,18 @@ struct Beam {
     int32_t flat;                    // j * vocab
 };
 
+// The number of items in [0, count) better than `mine`, which is item `of`, by
+// the `per` neighbouring threads that share it (a power of two; all get it).
+__device__ __forceinline__ int rank_of(const Candidate *items, int count, const Candidate &mine, int per) {
+    int rank = 0;
+#pragma unroll 4
+    for (int t = threadIdx.x & (per - 1); t < count; t += per) rank += better(items[t], mine);
+    for (int o = 1; o < per; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    return rank;
+}
+// Threads an item can have so that one round takes all of them.
+__device__ __forceinline__ int share_of(int count) { return count <= 32 ? 8 : count <= 64 ? 4 : count <= 128 ? 2 : 1; }
+
 // Dynamic shared memory: the lists' fronts (their first `depth` candidates)
 // [lists * depth], the candidates to rank [kCap], beams [num_beams], counts
 // [lists].
@@ -517,10 +543,10 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, n = p.num_out;
-    const int lists = p.num_beams * p.slices, row0 = g * p.num_beams, depth = p.depth;
+    const int lists = p.num_beams * p.slices, row0 = g * p.num_beams, depth = p.depth, fronts = lists * depth;
     const int64_t entry0 = (int64_t)row0 * p.slices;
     Candidate *front = reinterpret_cast<Candidate *>(dyn);
-    Candidate *found = front + lists * depth;
+    Candidate *found = front + fronts;
     Beam *beams = reinterpret_cast<Beam *>(found + kCap);
     int32_t *counts = reinterpret_cast<int32_t *>(beams + p.num_beams);
     if (tid == 0) {
@@ -529,31 +555,35 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
         bound.index = INT32_MAX;
     }
     // the fronts, raw, and every list's count: loads that depend on nothing
-    for (int e = tid; e < lists * depth; e += kThreads) {
+    for (int e = tid; e < fronts; e += kThreads) {
         const int l = e / depth, i = e - l * depth;
         const int64_t at = (entry0 + l) * n + i;
         front[e].score = (int64_t)__float_as_uint(__ldcg(p.values + at));
         front[e].index = __ldcg(p.indices + at);
     }
     for (int l = tid; l < lists; l += kThreads) counts[l] = __ldcg(p.counts + entry0 + l);
-    // a warp per row: its maximum, and its sum relative to that
+    // a warp per row: its maximum, and its sum relative to that.  (A row that
+    // does not run has left its records as they were: read, and not used.)
     for (int j = warp; j < p.num_beams; j += kWarps) {
+        const float2 *part = p.sums + (int64_t)(row0 + j) * p.row_chunks * kWarps;
+        const int parts = p.row_chunks * kWarps;
+        float2 head[4];                                    // (most rows have no more a lane)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            head[u] = lane + 32 * u < parts ? __ldcg(part + lane + 32 * u) : make_float2(0.f, 0.f);
         const float score = __ldg(p.beam_scores + row0 + j);
         const bool done = p.finished && __ldg(p.finished + row0 + j);
+        float top = -INFINITY;
+        for (int i = lane; i < p.slices; i += 32) top = fmaxf(top, __ldcg(p.maxima + entry0 + j * p.slices + i));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         int kind = score > -INFINITY && score < INFINITY ? (done ? 2 : 1) : 0;
         bool bad = !(score < INFINITY);
-        float top = -INFINITY;
         unsigned long long total = 0;
         if (kind == 1) {
-            for (int i = lane; i < p.slices; i += 32)
-                top = fmaxf(top, __ldcg(p.maxima + entry0 + j * p.slices + i));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const bool far = is_far(top);
             const float reference = reference_of(top);
-            const float2 *part = p.sums + (int64_t)(row0 + j) * p.row_chunks * kWarps;
-            for (int k = lane; k < p.row_chunks * kWarps; k += 32) {
-                const float2 s = __ldcg(part + k);
+            auto add = [&](const float2 &s) {
                 bad |= !(fabsf(s.y) < INFINITY);
                 if (!far && s.y >= 0.f) {
                     const float down = reference - s.x;
@@ -564,7 +594,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
                                                : __fmaf_rn(s.x, kLog2e, -reference);
                     total += __float2ull_rn(fabsf(s.y) * fast_exp2(up) * 4294967296.f);
                 }
-            }
+            };
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (lane + 32 * u < parts) add(head[u]);
+            for (int k = lane + 128; k < parts; k += 32) add(__ldcg(part + k));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
             bad = __any_sync(0xffffffffu, bad);
@@ -593,7 +627,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
         c.index = b.flat + (b.kind == 2 ? p.end_token : token);
         return c;
     };
-    for (int e = tid; e < lists * depth; e += kThreads) {
+    for (int e = tid; e < fronts; e += kThreads) {
         const int l = e / depth, i = e - l * depth, j = l / p.slices;
         const Beam &b = beams[j];
         // an ended beam's one candidate is in its first list
@@ -603,21 +637,24 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
         front[e] = c;
     }
     __syncthreads();
-    // the n-th largest of the maxima of 4 n groups of the fronts: a lower bound of
-    // the n-th largest candidate
-    const int groups = n <= 8 ? 32 : n <= 16 ? 64 : n <= 32 ? 128 : 256;
-    if (tid < groups) {
+    // The n-th largest of the fronts (or, where they are many, of the maxima of
+    // 256 groups of them) is a lower bound of the n-th largest candidate.
+    const Candidate *items = front;
+    int num_items = fronts;
+    if (fronts > kThreads) {
         Candidate c = {INT64_MIN, INT32_MAX};
-        for (int e = tid; e < lists * depth; e += groups)
+        for (int e = tid; e < fronts; e += kThreads)
             if (better(front[e], c)) c = front[e];
         best[tid] = c;
+        items = best;
+        num_items = kThreads;
+        __syncthreads();
     }
-    __syncthreads();
-    if (tid < groups) {
-        const Candidate mine = best[tid];
-        int rank = 0;
-        for (int t = 0; t < groups; ++t) rank += better(best[t], mine);
-        if (rank == n - 1 && mine.score != INT64_MIN) bound = mine;
+    {
+        const int per = share_of(num_items), of = tid / per;
+        const Candidate mine = items[min(of, num_items - 1)];
+        const int rank = rank_of(items, num_items, mine, per);
+        if (of < num_items && rank == n - 1 && mine.score != INT64_MIN) bound = mine;
     }
     __syncthreads();
     int total;
@@ -652,11 +689,12 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
         __syncthreads();
     }
     const int listed = total < n ? total : n;
-    for (int k = tid; k < total; k += kThreads) {
-        const Candidate mine = found[k];
-        int rank = 0;
-        for (int t = 0; t < total; ++t) rank += better(found[t], mine);
-        if (rank >= n) continue;
+    const int per = share_of(total);
+    for (int k0 = 0; k0 < total; k0 += kThreads / per) {
+        const int k = k0 + tid / per;
+        const Candidate mine = found[min(k, total - 1)];
+        const int rank = rank_of(found, total, mine, per);
+        if (k >= total || rank >= n || (tid & (per - 1)) != 0) continue;
         const int64_t o = (int64_t)g * n + rank;
         p.scores_out[o] = (float)score_of(mine.score);
         p.parents_out[o] = mine.index / p.vocab;
@@ -682,10 +720,11 @@ int32_t chunks_of(int32_t vocab, int32_t vec) {
     return (int32_t)(((int64_t)vocab + (int64_t)vec * kChunk - 1) / ((int64_t)vec * kChunk));
 }
 
-// Slices of a row: about four CTAs for each of the GB300's 152 SMs (the
-// workspace is sized without a device at hand), no slice without a chunk.
+// Slices of a row: as many as still run side by side, four CTAs on each of the
+// GB300's 152 SMs (the workspace is sized without a device at hand), no slice
+// without a chunk.
 int32_t slices_of(int64_t rows, int32_t row_chunks) {
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(row_chunks, (kCtasPerSm * 152 + rows - 1) / rows));
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(row_chunks, kCtasPerSm * 152 / rows));
 }
 
 // Front entries of each list: together 4 n or more, or the whole lists.
