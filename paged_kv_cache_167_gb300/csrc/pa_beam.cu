@@ -4,34 +4,32 @@
 // score(j, v) = beam_scores[j] + x - log sum exp x.  Two kernels, one pass over
 // the logits:
 //
-// 1. scan: a row is cut into chunks of 1024 vectors of 16 bytes, four for each
-//    thread of a CTA.  A warp's part of a chunk is summed by itself (32 lanes'
-//    local maxima and sums of exponentials, joined by shuffles: no running
-//    maximum, no divergence) and written as one (reference, sum) pair; which
-//    elements meet in which sum goes by their index in the row alone.  CTA
-//    (slice, row) takes an equal share of the row's chunks and reads them once;
-//    each of its threads keeps the maximum over them and the chunk
-//    it came from.  The n-th largest of the maxima of 4 n groups of threads is a
-//    lower bound of the slice's n-th largest element (and close to it: some 9
-//    elements reach it at n = 8), so only the few threads whose maximum reaches it
-//    can hold a candidate: their four vectors of that chunk (and the others only
-//    if the second best chunk reaches it too) are read again, from cache, and the
-//    elements at or above the bound are ranked.  Keys are (value, lower index
-//    first), so they are unique and ties need no further rule.
-// 2. merge: one CTA per group adds up each row's partial sums, turns the
-//    slices' lists (each sorted) into fp64 scores and picks the n best by the
-//    same bound, taken over the lists' heads.
+// 1. scan: CTA (slice, row) reads an equal share of the row's chunks (1024
+//    vectors of 16 bytes, four for each thread) once, three chunks on their way
+//    into shared memory at a time.  Each thread keeps the maximum, the chunk it
+//    came from and the sum of exponentials; which elements a thread has goes by
+//    their index in the row.  The n-th largest of the maxima of 4 n groups of
+//    threads is a lower bound of the slice's n-th largest element (and close to
+//    it: some 9 elements reach it at n = 8), so only the few threads whose maximum
+//    reaches it can hold a candidate: their four vectors of that chunk (and the
+//    others only if the second best chunk reaches it too) are read again, from
+//    cache, and the elements at or above the bound are ranked.  Keys are (value,
+//    lower index first), so they are unique and ties need no further rule.
+// 2. merge: one CTA per group adds up each row's slices, turns the slices' lists
+//    (each sorted) into fp64 scores and picks the n best by the same bound, taken
+//    over the lists' fronts.
 //
-// The exponentials: 2^(x L - c) with L = log2(e) rounded to fp32 and c = m L
-// rounded to an integer: one fused multiply-add (x L is not rounded by itself)
-// and one hardware 2^x.  The sum is then relative to c / L, which fp64 holds, so
-// c's rounding biases nothing, L's own (2^-26) acts on the distance to the
-// maximum only, and sums of different references join by exact shifts: above the
-// warp they are integers in units of 2^-32, and equal rows have equal sums
-// wherever they lie and however the grid cuts them.  A warp that meets a value
-// beyond 2^22 in size, where c would have no fraction left to lose (a row of the
-// type's lowest value, say), sums differences to its maximum instead.
+// The exponentials: 2^(x L - c) with L = log2(e) rounded to fp32 and c the running
+// maximum's m L rounded to an integer: one fused multiply-add (x L is not rounded
+// by itself) and one hardware 2^x.  The sum is then relative to c / L, which fp64
+// holds, so c's rounding biases nothing; L's own (2^-26) acts on the distance to
+// the maximum only; and a rising c scales the sum by a power of two, exactly, with
+// no branch.  Above the warp sums are integers in units of 2^-32.  So equal rows
+// have equal sums wherever they begin.  A slice whose maximum is beyond 2^22 in
+// size, where c would have no fraction left to lose (a row of the type's lowest
+// value, say), is summed again from its differences to that maximum.
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -92,6 +90,11 @@ __device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t pair_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -116,10 +119,9 @@ struct BeamParams {
     int32_t row_chunks;              // ceil(row_vectors / kChunk)
     int32_t slices;                  // of a row
     int32_t depth;                   // of the lists' fronts in the merge
-    // workspace
-    float2 *sums;                    // [rows][row_chunks][kWarps]: (reference, sum), or (maximum, -sum)
-    // and for each (row, slice):
-    float *maxima;
+    // workspace, one entry for each (row, slice)
+    unsigned long long *sums;        // of 2^(x L - reference_of(maximum)), or of e^(x - maximum) if that is far; 2^-32
+    float *maxima;                   // +inf: a NaN or +inf was met
     int32_t *counts;
     float *values;                   // [..][num_out], descending
     int32_t *indices;
@@ -251,57 +253,13 @@ __device__ __forceinline__ bool beam_runs(const BeamParams &p, int row) {
     return score > -INFINITY && score < INFINITY;
 }
 
-// A warp's part of a chunk: top is the maximum of each lane's vectors.  Returns
-// (reference, sum of 2^(x L - reference)), or (maximum, -sum of e^(x - maximum))
-// where a value is far.  A NaN or +inf makes the sum NaN or inf.
-template <typename E>
-__device__ __forceinline__ float2 chunk_sum(const uint4 (&v)[kUnroll], float top) {
-    if (__any_sync(0xffffffffu, is_far(top))) {
-        float most = top;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        float sum = 0.f;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float e[E::kVec];
-            E::unpack(v[u], e);
-#pragma unroll
-            for (int i = 0; i < E::kVec; ++i) sum += fast_exp2((e[i] - most) * kLog2e);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        return make_float2(most, -sum);
-    }
-    const float c = reference_of(top);
-    const uint64_t minus_c = pair(-c, -c), scale = pair(kLog2e, kLog2e);
-    uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        float e[E::kVec];
-        E::unpack(v[u], e);
-#pragma unroll
-        for (int i = 0; i < E::kVec; i += 4) {
-            const float2 s = unpair(pair_fma(pair(e[i], e[i + 1]), scale, minus_c));
-            const float2 t = unpair(pair_fma(pair(e[i + 2], e[i + 3]), scale, minus_c));
-            sum0 = pair_add(sum0, pair(fast_exp2(s.x), fast_exp2(s.y)));
-            sum1 = pair_add(sum1, pair(fast_exp2(t.x), fast_exp2(t.y)));
-        }
-    }
-    const float2 s = unpair(pair_add(sum0, sum1));
-    const int reference = __reduce_max_sync(0xffffffffu, (int)c);
-    float sum = (s.x + s.y) * fast_exp2((float)((int)c - reference));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return make_float2((float)reference, sum);
-}
-
 struct ScanShared {
     __align__(16) uint64_t keys[kCap];              // the groups' bounds first, then the candidates
     int32_t holders[kThreads];                      // of candidates in one chunk: chunk * kThreads + thread
     int32_t rich[kThreads];                         // in more than one: the thread
     int num_holders, num_rich, num_found;
     uint64_t bound;
-    float warp_max[kWarps];
+    float warp_max[kWarps], warp_sum[kWarps];
 };
 static_assert(sizeof(ScanShared) <= kScanSmem, "the selection reuses the copies' shared memory");
 
@@ -327,56 +285,100 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const B
     const Row<T> x(static_cast<const T *>(p.logits) + (int64_t)row * p.row_stride, p.vocab);
     const int32_t whole = x.whole(), vectors = p.row_vectors;
     const uint32_t none = E::minus_inf_word();
-    // A thread copies its own vectors; those of a warp are neighbours, and a row
-    // that does not begin on 16 bytes needs the one behind them too.
-    const uint4 *at = x.aligned();
-    const int32_t available = x.skew == 0 ? whole : whole + 1;
-    auto part = [&](int32_t chunk, int u) {
-        return parts + ((((chunk - first) % kStages) * kWarps + warp) * kUnroll + u) * kPart + lane;
-    };
-    auto start = [&](int32_t chunk) {
-        if (chunk < last) {
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int32_t j = chunk * kChunk + u * kThreads + tid;
-                if (j < available) copy_async(part(chunk, u), at + j);
-                if (x.skew != 0 && lane == 31 && j + 1 < available) copy_async(part(chunk, u) + 1, at + j + 1);
-            }
-        }
-        copy_commit();                              // (an empty group where nothing is left)
-    };
     float m = -INFINITY, second = -INFINITY;        // the largest of the chunks' maxima, and of the others'
     int32_t best = first;
-    float2 *sums = p.sums + ((int64_t)row * p.row_chunks + first) * kWarps + warp;
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) start(first + s);
-    for (int32_t k = first; k < last; ++k) {
-        copy_wait<kStages - 1>();                   // chunk k has landed; the later ones may be under way
-        __syncwarp();
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int32_t j = k * kChunk + u * kThreads + tid;
-            v[u] = make_uint4(none, none, none, none);
-            if (j < whole) {
-                const uint4 *a = part(k, u);
-                v[u] = x.skew == 0 ? a[0] : x.shifted(a[0], a[1]);
-            } else if (j < vectors) {
-                v[u] = x.load(j);                   // the row's last one or two
-            }
-        }
-        __syncwarp();                               // every lane has read what its neighbours copied
-        start(k + kStages);
+    float c = reference_of(m);
+    uint64_t sum0 = 0, sum1 = 0;                    // pairs
+    auto take = [&](const uint4 (&v)[kUnroll], int32_t k) {
         const float top = E::maximum(v);
         second = fmaxf(second, fminf(m, top));
         if (top > m) {
             m = top;
             best = k;
         }
-        const float2 s = chunk_sum<E>(v, top);
-        if (lane == 0) *sums = s;
-        sums += kWarps;
-    }
+        const float next = fmaxf(c, reference_of(top)), down = fast_exp2(c - next);
+        c = next;
+        sum0 = pair_mul(sum0, pair(down, down));
+        sum1 = pair_mul(sum1, pair(down, down));
+        const uint64_t minus_c = pair(-c, -c), scale = pair(kLog2e, kLog2e);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float e[VN];
+            E::unpack(v[u], e);
+#pragma unroll
+            for (int i = 0; i < VN; i += 4) {       // NaN and +inf end up in the sum as NaN or inf
+                const float2 s = unpair(pair_fma(pair(e[i], e[i + 1]), scale, minus_c));
+                const float2 t = unpair(pair_fma(pair(e[i + 2], e[i + 3]), scale, minus_c));
+                sum0 = pair_add(sum0, pair(fast_exp2(s.x), fast_exp2(s.y)));
+                sum1 = pair_add(sum1, pair(fast_exp2(t.x), fast_exp2(t.y)));
+            }
+        }
+    };
+    // A thread copies its own vectors and reads its own copies; those of a warp are
+    // neighbours, and a row that does not begin on 16 bytes (SKEW) needs the one
+    // behind them too.
+    auto stream = [&](auto skewed) {
+        constexpr bool SKEW = decltype(skewed)::value;
+        const int32_t available = SKEW ? whole + 1 : whole;
+        const uint4 *from = x.aligned() + (int64_t)first * kChunk + tid;   // of the next chunk to start
+        uint4 *const mine = parts + warp * (kUnroll * kPart) + lane;
+        constexpr int kStage = kWarps * kUnroll * kPart;
+        auto start = [&](int32_t chunk, uint4 *to) {
+            if (chunk < last) {
+                if ((chunk + 1) * kChunk < available) {    // (all of it, and one more)
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u) copy_async(to + u * kPart, from + u * kThreads);
+                    if (SKEW && lane == 31) {
+#pragma unroll
+                        for (int u = 0; u < kUnroll; ++u) copy_async(to + u * kPart + 1, from + u * kThreads + 1);
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u) {
+                        const int32_t j = chunk * kChunk + u * kThreads + tid;
+                        if (j < available) copy_async(to + u * kPart, from + u * kThreads);
+                        if (SKEW && lane == 31 && j + 1 < available)
+                            copy_async(to + u * kPart + 1, from + u * kThreads + 1);
+                    }
+                }
+            }
+            from += kChunk;
+            copy_commit();                          // (an empty group where nothing is left)
+        };
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) start(first + s, mine + s * kStage);
+        uint4 *at = mine;
+        for (int32_t k = first; k < last; ++k) {
+            copy_wait<kStages - 1>();               // chunk k has landed; the later ones may be under way
+            if (SKEW) __syncwarp();
+            uint4 v[kUnroll];
+            if ((k + 1) * kChunk <= whole) {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+                    v[u] = SKEW ? x.shifted(at[u * kPart], at[u * kPart + 1]) : at[u * kPart];
+            } else {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int32_t j = k * kChunk + u * kThreads + tid;
+                    v[u] = make_uint4(none, none, none, none);
+                    if (j < whole)
+                        v[u] = SKEW ? x.shifted(at[u * kPart], at[u * kPart + 1]) : at[u * kPart];
+                    else if (j < vectors)
+                        v[u] = x.load(j);           // the row's last one or two
+                }
+            }
+            if (SKEW) __syncwarp();                 // every lane has read what its neighbours copied
+            start(k + kStages, at);
+            at = at == mine + (kStages - 1) * kStage ? mine : at + kStage;
+            take(v, k);
+        }
+    };
+    if (x.skew == 0)
+        stream(std::false_type());
+    else
+        stream(std::true_type());
+    const float2 s0 = unpair(sum0), s1 = unpair(sum1);
+    const float sum = (s0.x + s0.y) + (s1.x + s1.y);
     copy_wait<0>();
     __syncthreads();                                // the copies' shared memory is free
 
@@ -401,6 +403,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const B
         sh.num_holders = sh.num_rich = sh.num_found = 0;
     }
     __syncthreads();
+    const int32_t end = min(last * kChunk, vectors);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.warp_max[i]);
+    float part = 0.f;
+    if (is_far(top)) {
+        for (int32_t j = first * kChunk + tid; j < end; j += kThreads) {
+            float e[VN];
+            E::unpack(x.load(j), e);
+#pragma unroll
+            for (int i = 0; i < VN; ++i) part += fast_exp2((e[i] - top) * kLog2e);
+        }
+    } else {
+        part = sum * fast_exp2(c - reference_of(top));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0) sh.warp_sum[warp] = part;
     if (tid < groups) {                             // the n-th largest of the groups' bounds
         const uint64_t mine = sh.keys[tid];
         int above = 0;
@@ -410,13 +429,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const B
         }
         if (mine != 0 && above == n - 1) sh.bound = mine;
     }
-    if (tid == 0) {
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.warp_max[i]);
-        p.maxima[entry] = top;
-    }
     __syncthreads();
-    const int32_t end = min(last * kChunk, vectors);
+    if (tid == 0) {
+        unsigned long long total = 0;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            bad |= !(fabsf(sh.warp_sum[i]) < INFINITY);
+            total += __float2ull_rn(sh.warp_sum[i] * 4294967296.f);
+        }
+        p.sums[entry] = total;
+        p.maxima[entry] = bad ? INFINITY : top;
+    }
     int found;
     while (true) {
         const uint64_t limit = sh.bound;
@@ -533,13 +557,13 @@ __device__ __forceinline__ int rank_of(const Candidate *items, int count, const 
 __device__ __forceinline__ int share_of(int count) { return count <= 32 ? 8 : count <= 64 ? 4 : count <= 128 ? 2 : 1; }
 
 // Dynamic shared memory: the lists' fronts (their first `depth` candidates)
-// [lists * depth], the candidates to rank [kCap], beams [num_beams], counts
-// [lists].
+// [lists * depth], the candidates to rank [kCap], beams [num_beams], counts and
+// the lists to look further into [lists] each.
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Candidate best[kThreads];
     __shared__ Candidate bound;
-    __shared__ int num_found;
+    __shared__ int num_found, num_deep;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, n = p.num_out;
@@ -548,9 +572,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     Candidate *front = reinterpret_cast<Candidate *>(dyn);
     Candidate *found = front + fronts;
     Beam *beams = reinterpret_cast<Beam *>(found + kCap);
-    int32_t *counts = reinterpret_cast<int32_t *>(beams + p.num_beams);
+    int32_t *counts = reinterpret_cast<int32_t *>(beams + p.num_beams), *deep = counts + lists;
     if (tid == 0) {
-        num_found = 0;
+        num_found = num_deep = 0;
         bound.score = INT64_MIN;
         bound.index = INT32_MAX;
     }
@@ -565,45 +589,39 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     // a warp per row: its maximum, and its sum relative to that.  (A row that
     // does not run has left its records as they were: read, and not used.)
     for (int j = warp; j < p.num_beams; j += kWarps) {
-        const float2 *part = p.sums + (int64_t)(row0 + j) * p.row_chunks * kWarps;
-        const int parts = p.row_chunks * kWarps;
-        float2 head[4];                                    // (most rows have no more a lane)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            head[u] = lane + 32 * u < parts ? __ldcg(part + lane + 32 * u) : make_float2(0.f, 0.f);
+        const int64_t e0 = entry0 + j * p.slices;
+        const float first = lane < p.slices ? __ldcg(p.maxima + e0 + lane) : -INFINITY;
+        const unsigned long long first_sum = lane < p.slices ? __ldcg(p.sums + e0 + lane) : 0;
         const float score = __ldg(p.beam_scores + row0 + j);
         const bool done = p.finished && __ldg(p.finished + row0 + j);
-        float top = -INFINITY;
-        for (int i = lane; i < p.slices; i += 32) top = fmaxf(top, __ldcg(p.maxima + entry0 + j * p.slices + i));
+        int kind = score > -INFINITY && score < INFINITY ? (done ? 2 : 1) : 0;
+        float top = first;
+        for (int i = lane + 32; i < p.slices; i += 32) top = fmaxf(top, __ldcg(p.maxima + e0 + i));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        int kind = score > -INFINITY && score < INFINITY ? (done ? 2 : 1) : 0;
-        bool bad = !(score < INFINITY);
+        const bool bad = !(score < INFINITY) || (kind == 1 && top == INFINITY);
+        const bool far = is_far(top);
+        const float reference = reference_of(top);
         unsigned long long total = 0;
-        if (kind == 1) {
-            const bool far = is_far(top);
-            const float reference = reference_of(top);
-            auto add = [&](const float2 &s) {
-                bad |= !(fabsf(s.y) < INFINITY);
-                if (!far && s.y >= 0.f) {
-                    const float down = reference - s.x;
-                    if (down < 64.f) total += __float2ull_rn(s.y * 4294967296.f) >> (int)down;
-                } else if (s.y != 0.f) {            // the sum's reference above the row's, in powers of two
-                    const float up = s.y > 0.f ? __fmaf_rn(-top, kLog2e, s.x)
-                                     : far     ? (s.x - top) * kLog2e
-                                               : __fmaf_rn(s.x, kLog2e, -reference);
-                    total += __float2ull_rn(fabsf(s.y) * fast_exp2(up) * 4294967296.f);
-                }
-            };
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (lane + 32 * u < parts) add(head[u]);
-            for (int k = lane + 128; k < parts; k += 32) add(__ldcg(part + k));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            bad = __any_sync(0xffffffffu, bad);
-            if (bad || top == -INFINITY) kind = 0;
+        auto add = [&](float maximum, unsigned long long sum) {
+            if (maximum == -INFINITY) return;
+            if (!far && !is_far(maximum)) {
+                const float down = reference - reference_of(maximum);
+                if (down < 64.f) total += sum >> (int)down;
+            } else {                                // the slice's reference above the row's, in powers of two
+                const float up = !far            ? __fmaf_rn(maximum, kLog2e, -reference)
+                                 : is_far(maximum) ? (maximum - top) * kLog2e
+                                                   : __fmaf_rn(-top, kLog2e, reference_of(maximum));
+                total += __float2ull_rn((float)sum * fast_exp2(up));
+            }
+        };
+        if (kind == 1 && !bad) {
+            add(first, first_sum);
+            for (int i = lane + 32; i < p.slices; i += 32) add(__ldcg(p.maxima + e0 + i), __ldcg(p.sums + e0 + i));
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (bad || (kind == 1 && top == -INFINITY)) kind = 0;
         if (lane == 0) {
             if (bad) raise_error(p.err, PA_DEVERR_VALUE);
             beams[j].offset = score;
@@ -659,21 +677,28 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     __syncthreads();
     int total;
     while (true) {
-        // the candidates at or above the bound (hardly more than n: the groups are many)
+        // The candidates at or above the bound, hardly more than n: those in the
+        // fronts, then what lies behind a front that is all above it.
         const Candidate limit = bound;
-        for (int e = tid; e < lists * n; e += kThreads) {
-            const int l = e / n, i = e - l * n;
-            Candidate c = front[l * depth + min(i, depth - 1)];
-            if (c.score == INT64_MIN || better(limit, c)) continue;
-            if (i >= depth) {                              // behind a front that is all above the bound
-                const Beam &b = beams[l / p.slices];
-                if (b.kind != 1 || i >= counts[l]) continue;
-                const int64_t at = (entry0 + l) * n + i;
-                c = candidate(b, __ldcg(p.values + at), __ldcg(p.indices + at));
-                if (better(limit, c)) continue;
-            }
+        auto take = [&](const Candidate &c) {
+            if (c.score == INT64_MIN || better(limit, c)) return;
             const int at = atomicAdd(&num_found, 1);
             if (at < kCap) found[at] = c;
+        };
+        for (int e = tid; e < fronts; e += kThreads) {
+            const Candidate c = front[e];
+            take(c);
+            const int l = e / depth;
+            if (e - l * depth == depth - 1 && c.score != INT64_MIN && !better(limit, c) &&
+                beams[l / p.slices].kind == 1 && counts[l] > depth)
+                deep[atomicAdd(&num_deep, 1)] = l;
+        }
+        __syncthreads();
+        for (int d = tid; d < num_deep * (n - depth); d += kThreads) {
+            const int l = deep[d / (n - depth)], i = depth + d % (n - depth);
+            if (i >= counts[l]) continue;
+            const int64_t at = (entry0 + l) * n + i;
+            take(candidate(beams[l / p.slices], __ldcg(p.values + at), __ldcg(p.indices + at)));
         }
         __syncthreads();
         total = num_found;
@@ -685,7 +710,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
             if (rank == n - 1) bound = mine;
         }
         __syncthreads();
-        if (tid == 0) num_found = 0;
+        if (tid == 0) num_found = num_deep = 0;
         __syncthreads();
     }
     const int listed = total < n ? total : n;
@@ -733,16 +758,15 @@ int32_t depth_of(int32_t lists, int32_t n) { return std::min(n, (4 * n + lists -
 size_t merge_smem(int32_t beams, int32_t slices, int32_t n) {
     const int lists = beams * slices;
     return ((size_t)lists * depth_of(lists, n) + kCap) * sizeof(Candidate) + beams * sizeof(Beam) +
-           lists * sizeof(int32_t);
+           2 * (size_t)lists * sizeof(int32_t);
 }
 
 }  // namespace
 
 // For either type: fp32's vectors, the shorter ones, make the more chunks.
 size_t beam_workspace(int64_t rows, int32_t vocab, int32_t num_out) {
-    const int32_t chunks = chunks_of(vocab, 4);
-    const size_t entries = (size_t)rows * slices_of(rows, chunks);
-    return round_up((size_t)rows * chunks * kWarps * sizeof(float2)) + 2 * round_up(entries * 4) + 2 * round_up(entries * num_out * 4);
+    const size_t entries = (size_t)rows * slices_of(rows, chunks_of(vocab, 4));
+    return round_up(entries * 8) + 2 * round_up(entries * 4) + 2 * round_up(entries * num_out * 4);
 }
 
 cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
@@ -762,8 +786,8 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     p.slices = slices_of(rows, p.row_chunks);
     const size_t entries = (size_t)rows * p.slices;
     char *w = static_cast<char *>(a.workspace);
-    p.sums = reinterpret_cast<float2 *>(w);
-    w += round_up((size_t)rows * p.row_chunks * kWarps * sizeof(float2));
+    p.sums = reinterpret_cast<unsigned long long *>(w);
+    w += round_up(entries * 8);
     p.maxima = reinterpret_cast<float *>(w);
     w += round_up(entries * 4);
     p.counts = reinterpret_cast<int32_t *>(w);
@@ -783,7 +807,7 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScanSmem);
     if (e == cudaSuccess) e = launch_pdl(scan, grid, dim3(kThreads), stream, kScanSmem, p);
     if (e != cudaSuccess) return e;
-    // (at most 36 KB: 640 lists, 256 front entries beyond them)
+    // (at most 39 KB: 640 lists, 256 front entries beyond them)
     const size_t smem = merge_smem(a.num_beams, p.slices, a.num_out);
     return launch_pdl(beam_merge_kernel, dim3(a.num_groups), dim3(kThreads), stream, smem, p);
 }
