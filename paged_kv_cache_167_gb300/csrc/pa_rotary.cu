@@ -112,14 +112,25 @@ cudaError_t launch_rotate_v(RotateParams &p, int64_t tokens, cudaStream_t stream
     int y = kRotateThreads / x;
     if (y > heads) y = heads;
     const unsigned gz = (unsigned)((p.chunks + x - 1) / x);
-    // Four heads a thread once that still fills every SM; one otherwise, for a
-    // short call's latency.
-    const int64_t wide = tokens * ((heads + 4 * y - 1) / (4 * y)) * gz;
-    const bool four = wide >= 4ll * device_sm_count();
-    const int per = four ? 4 * y : y;
-    const dim3 grid((unsigned)tokens, (unsigned)((heads + per - 1) / per), gz), block(x, y);
-    return four ? launch_pdl(rotate_kernel<V, INTERLEAVED, 4, CACHE>, grid, block, stream, 0, p)
-                : launch_pdl(rotate_kernel<V, INTERLEAVED, 1, CACHE>, grid, block, stream, 0, p);
+    // Several heads a thread (up to six, the number that wastes least) once that
+    // still fills every SM; one otherwise, for a short call's latency.
+    const int rows = (heads + y - 1) / y, groups = (rows + 5) / 6, most = (rows + groups - 1) / groups;
+    const bool wide = tokens * groups * gz >= 4ll * device_sm_count();
+    const int u = wide ? (V == 8 ? most : most > 2 ? 4 : most) : 1;
+    const dim3 grid((unsigned)tokens, (unsigned)((heads + y * u - 1) / (y * u)), gz), block(x, y);
+    if constexpr (V == 8) {
+        switch (u) {
+            case 2: return launch_pdl(rotate_kernel<V, INTERLEAVED, 2, CACHE>, grid, block, stream, 0, p);
+            case 3: return launch_pdl(rotate_kernel<V, INTERLEAVED, 3, CACHE>, grid, block, stream, 0, p);
+            case 4: return launch_pdl(rotate_kernel<V, INTERLEAVED, 4, CACHE>, grid, block, stream, 0, p);
+            case 5: return launch_pdl(rotate_kernel<V, INTERLEAVED, 5, CACHE>, grid, block, stream, 0, p);
+            case 6: return launch_pdl(rotate_kernel<V, INTERLEAVED, 6, CACHE>, grid, block, stream, 0, p);
+            default: return launch_pdl(rotate_kernel<V, INTERLEAVED, 1, CACHE>, grid, block, stream, 0, p);
+        }
+    }
+    return u == 4   ? launch_pdl(rotate_kernel<V, INTERLEAVED, 4, CACHE>, grid, block, stream, 0, p)
+           : u == 2 ? launch_pdl(rotate_kernel<V, INTERLEAVED, 2, CACHE>, grid, block, stream, 0, p)
+                    : launch_pdl(rotate_kernel<V, INTERLEAVED, 1, CACHE>, grid, block, stream, 0, p);
 }
 
 template <bool CACHE>
