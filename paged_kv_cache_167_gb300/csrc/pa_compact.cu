@@ -1,7 +1,8 @@
 // pa_compact.cu -- compaction of a sequence's kept tokens to consecutive
 // positions, in place or into other blocks, keys re-rotated on the way.
 //
-// The rows of one (sequence, K or V, kv-head) are taken in tiles of up to 16 KB.
+// A unit is one sequence's K or V rows of one or several kv-heads (several share
+// the rows' places and, for keys, their angles); it is taken in tiles of up to 16 KB.
 // A tile is gathered into shared memory by asynchronous 16-byte copies, two tiles
 // ahead of the one being written; the positions and table entries that say where
 // its rows lie are fetched further ahead still, so that no step waits for that
@@ -10,14 +11,16 @@
 // In place, row i is written at start + i <= keep[i] < keep[i + 1]: what a tile
 // writes lies before everything that later tiles read, so it is enough that a
 // tile is written only when it and all earlier ones have been read.  One CTA has
-// that from a barrier per tile.  Where there are too few (sequence, K or V,
-// head) for the SMs, a cluster of up to 16 CTAs takes the tiles in turn, and the
-// barrier is the cluster's (arrived at for one tile while the one before is
-// written); out of place the tiles are free of one another and any number of CTAs
-// share them.  The cluster's barrier is a relaxed one: what it
-// orders are reads that have ended (their bytes are in shared memory) before
-// writes that have not begun; nobody reads what was written, so no store has to
-// be waited for.
+// that from a barrier per tile.  Where there are too few units for the SMs, a
+// cluster of up to 16 CTAs takes a unit's tiles in turn: each CTA writes into
+// the shared memory of all others how many of its tiles have landed, and writes
+// its own tile of a step to the pool when all have landed theirs.  That is said
+// one step ahead, so the way from SM to SM is not waited for (the cluster's own
+// barrier cost 1.6 us a step).  The counts are relaxed stores, one word for each
+// sender: what they order are reads that have ended (their bytes are in shared
+// memory) before writes that have not begun; nobody reads what was written, so no
+// store has to be waited for.  Out of place the tiles are free of one another and
+// any number of CTAs share them.
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -45,6 +48,7 @@ struct CompactParams {
     const uint64_t *turns;             // null: keys move as they are
     int32_t rot_chunks, chunks;        // of a key row, V pairs or V components each
     int32_t rows;                      // of a tile
+    int32_t heads;                     // of a unit
     unsigned int *err;
 };
 
@@ -57,34 +61,61 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
+// Stores value at this address in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_there(int32_t *at, uint32_t rank, int32_t value) {
+    asm volatile(
+        "{\n\t.reg .b32 there;\n\t"
+        "mapa.shared::cluster.u32 there, %0, %1;\n\t"
+        "st.relaxed.cluster.shared::cluster.s32 [there], %2;\n\t}" ::"r"(smem_addr(at)),
+        "r"(rank), "r"(value)
+        : "memory");
+}
+__device__ __forceinline__ int32_t load_here(const int32_t *at) {
+    int32_t v;
+    asm volatile("ld.relaxed.cluster.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_addr(at)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // What is being found out about one row, one step of the chain after another.
 struct RowLookup {
-    int32_t from = -1, to = 0;         // from -1: no such row, or a bad one
-    int32_t src_block = -1, dst_block = -1;
+    int32_t from = 0, before = 0;      // keep[i] and keep[i - 1]
+    int32_t to = 0;                    // start + i
+    int32_t src_block = 0, dst_block = 0;
+    bool row = false;                  // false: no such row, or a bad one
 };
 
-// grid (CTAs of one unit, 2 x kv-head, sequence); CLUSTER: they are a cluster
+// grid (CTAs of one unit, 2 x head groups, sequence); CLUSTER: they are a cluster
 // and write in order, else each goes its own way (one CTA, or out of place).
 // STAGES tiles are in shared memory or on their way there.
 template <int V, bool INTERLEAVED, int THREADS, int STAGES, bool CLUSTER>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 8) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 && CLUSTER ? 3 : 4) compact_kernel(const CompactParams p) {
     using Vec = typename BfVec<V>::type;
     constexpr int kRings = STAGES + 2;                     // tiles whose rows' places are known
-    extern __shared__ __align__(16) uint4 ring[];          // [STAGES][rows][row_vecs], then the rows' places
-    const int row_vecs = p.d / 8, tile_vecs = p.rows * row_vecs;
+    extern __shared__ __align__(16) uint4 ring[];          // [STAGES][rows][heads][d / 8], then the rows' places
+    const int row_vecs = p.heads * (p.d / 8), tile_vecs = p.rows * row_vecs;
     int64_t *src_rows = reinterpret_cast<int64_t *>(ring + STAGES * tile_vecs);   // [kRings][rows]; -1: stays
     int64_t *dst_rows = src_rows + kRings * p.rows;
-    int32_t *shifts = reinterpret_cast<int32_t *>(dst_rows + kRings * p.rows);
+    uint64_t *turns = reinterpret_cast<uint64_t *>(dst_rows + kRings * p.rows);    // [V][rot_chunks]
+    int32_t *shifts = reinterpret_cast<int32_t *>(turns + p.rot_chunks * V);
+    __shared__ int32_t landed[16];                         // CLUSTER: tiles that have landed in each of its CTAs
+    if (CLUSTER) {
+        if (threadIdx.x < 16) landed[threadIdx.x] = 0;
+        cluster_sync();
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int kv = blockIdx.y & 1, h = blockIdx.y >> 1, s = blockIdx.z, tid = threadIdx.x;
+    const int kv = blockIdx.y & 1, h = (blockIdx.y >> 1) * p.heads, s = blockIdx.z, tid = threadIdx.x;
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
     const int64_t len = __ldg(p.seq_lens + s), n = __ldg(p.keep_lens + s);
     const int64_t start = p.starts ? __ldg(p.starts + s) : 0;
     const bool reports = h == 0 && kv == 0;
     if (len < 0 || len > cap || n < 0 || n > p.max_keep || start < 0) {
         if (tid == 0 && reports && blockIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_LEN);
-        return;
+        return;                                            // (a whole cluster does, before any count)
     }
     const int32_t *keep = p.keep + (int64_t)s * p.max_keep;
     const int32_t *src_table = p.src_tables + (int64_t)s * p.max_blocks;
@@ -96,27 +127,29 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 8) compact_kerne
     const bool looks = tid < p.rows;
 
     // The chain behind a row's place: keep -> table entries -> offsets, one call
-    // (and one step of the loop below) each.  Threads 0 .. rows - 1 take a row.
+    // (and one step of the loop below) each, so that no call uses what it has just
+    // asked for.  Threads 0 .. rows - 1 take a row.
     int64_t next_row = (int64_t)blockIdx.x * p.rows + tid;   // of the next look_keep
     auto look_keep = [&]() {
         RowLookup r;
         const int64_t i = next_row;
         next_row += (int64_t)gridDim.x * p.rows;
         if (!looks || i >= n) return r;
-        const int32_t before = i > 0 ? __ldg(keep + i - 1) : -1, from = __ldg(keep + i);
-        if (from <= before || from < start + i || from >= len) {
-            if (reports) raise_error(p.err, PA_DEVERR_KEEP);
-            return r;
-        }
-        r.from = from;
-        r.to = (int32_t)(start + i);                       // <= from
+        r.before = i > 0 ? __ldg(keep + i - 1) : -1;
+        r.from = __ldg(keep + i);
+        r.to = (int32_t)min(start + i, (int64_t)INT32_MAX);   // (beyond every length: refused)
+        r.row = true;
         return r;
     };
     auto block_of = [&](int32_t t) {
         return p.block_log >= 0 ? (uint32_t)t >> p.block_log : (uint32_t)t / (uint32_t)p.block_size;
     };
     auto look_blocks = [&](RowLookup r) {
-        if (r.from >= 0) {
+        if (r.row && (r.from <= r.before || r.from < r.to || r.from >= len)) {
+            if (reports) raise_error(p.err, PA_DEVERR_KEEP);
+            r.row = false;
+        }
+        if (r.row) {
             r.src_block = __ldg(src_table + block_of(r.from));
             r.dst_block = __ldg(dst_table + block_of(r.to));
         }
@@ -125,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 8) compact_kerne
     auto put_row = [&](int slot, const RowLookup &r) {
         if (!looks) return;
         int64_t src = -1, dst = -1;
-        if (r.from >= 0) {
+        if (r.row) {
             if (r.src_block < 0 || r.src_block >= p.num_blocks || r.dst_block < 0 || r.dst_block >= p.num_blocks) {
                 if (reports) raise_error(p.err, PA_DEVERR_BLOCK_ID);
             } else if (r.from != r.to || r.src_block != r.dst_block) {
@@ -139,12 +172,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 8) compact_kerne
         shifts[at] = r.to - r.from;
     };
 
-    // this thread's vectors of a tile: (row, vector of the row), the same in all
-    int row_of[kLoads], vec_of[kLoads];
+    // this thread's vectors of a tile: (row, elements from the row's place), the
+    // same in all tiles
+    const int head_stride = p.block_size * p.d;
+    int row_of[kLoads], off_of[kLoads];
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
         row_of[u] = (tid + u * THREADS) / row_vecs;
-        vec_of[u] = (tid + u * THREADS) - row_of[u] * row_vecs;
+        const int vec = (tid + u * THREADS) - row_of[u] * row_vecs, head = vec / (p.d / 8);
+        off_of[u] = head * head_stride + (vec - head * (p.d / 8)) * 8;
     }
     auto begin_copies = [&](int32_t k, int stage, int slot) {
         if (k < steps) {
@@ -153,18 +189,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 8) compact_kerne
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
                 if (row_of[u] < p.rows && src[row_of[u]] >= 0)
-                    copy_async(tile + u * THREADS, p.pool + src[row_of[u]] + vec_of[u] * 8);
+                    copy_async(tile + u * THREADS, p.pool + src[row_of[u]] + off_of[u]);
         }
         copy_commit();                                     // (an empty group where nothing is left)
     };
     auto next = [](int i, int count) { return i + 1 == count ? 0 : i + 1; };
 
     // this thread's chunk of the rows it turns: every `apart`-th row from `row0` on
-    const int apart = turn ? THREADS / p.chunks : 1, row0 = turn ? tid / p.chunks : 0, c = turn ? tid - row0 * p.chunks : 0;
+    const int apart = turn ? max(THREADS / p.chunks, 1) : 1, row0 = turn ? tid / p.chunks : 0, c = turn ? tid - row0 * p.chunks : 0;
     const bool turning = turn && row0 < apart && c < p.rot_chunks, passing = turn && row0 < apart && !turning;
     float2 cs[V];
     int32_t turned = 0;                                    // the shift that cs belongs to
     const int half = p.rot_chunks * V;
+    if (turn)
+        for (int i = tid; i < half; i += THREADS) turns[i % V * p.rot_chunks + i / V] = __ldg(p.turns + i);
     const int at0 = !turning ? 2 * half + (c - p.rot_chunks) * V : INTERLEAVED ? 2 * c * V : c * V;
     const int at1 = INTERLEAVED ? at0 + V : half + at0;
 
@@ -174,20 +212,47 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 8) compact_kerne
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) begin_copies(k, k, k);
-    if (steps <= 0) return;                                // (the same for a whole cluster; nothing is under way)
-    copy_wait<STAGES - 2>();                               // tile 0 has landed
-    if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    auto say_landed = [&](int32_t count) {
+        if (CLUSTER && tid < (int)gridDim.x) store_there(&landed[blockIdx.x], tid, count);
+    };
+    // Whether the first `count` tiles have landed in all CTAs of the cluster; gives
+    // up, as every wait of the library does, after kWaitLimitNs.
+    auto all_landed = [&](int32_t count) {
+        const int lane = tid & 31;
+        uint64_t since = 0;
+        for (int tries = 0;; ++tries) {
+            const bool there = lane >= (int)gridDim.x || load_here(&landed[lane]) >= count;
+            if (__all_sync(0xffffffffu, there)) return true;
+            if ((tries & 255) == 255) {
+                const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+                if (since == 0) since = now;
+                if (now - since > kWaitLimitNs) {
+                    if (lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
+                    return false;
+                }
+            }
+        }
+    };
+    constexpr int kPending = CLUSTER ? (STAGES > 2 ? STAGES - 3 : 0) : STAGES - 2;
+    if (CLUSTER && steps > 0) {
+        copy_wait<STAGES - 2>();                           // tile 0
+        __syncthreads();
+        say_landed(1);
+    }
     int stage = 0, ahead = STAGES - 1;                     // tile k's place, and tile k + STAGES - 1's
     int slot = 0, slot_ahead = STAGES - 1, slot_put = STAGES;
+    bool writing = true;
     for (int32_t k = 0; k < steps; ++k) {
-        if (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // tile k has landed everywhere
-        __syncthreads();
+        copy_wait<kPending>();                             // tile k has landed; in a cluster, tile k + 1
+        __syncthreads();                                   // in all threads, and tile k - 1 is written
+        say_landed(k + 2);
         begin_copies(k + STAGES - 1, ahead, slot_ahead);   // into the place of tile k - 1, written before the barrier
-        copy_wait<STAGES - 2>();                           // tile k + 1 has landed: said while tile k is written
-        if (CLUSTER && k + 1 < steps) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
         put_row(slot_put, blocks);                         // of tile k + STAGES
         blocks = look_blocks(kept);
         kept = look_keep();
+        // (a wait that gives up leaves the warp's remaining rows unwritten; the CTA
+        // goes on counting, so that the others end)
+        if (CLUSTER && writing) writing = all_landed(k + 1);
         const int64_t *src = src_rows + slot * p.rows, *dst = dst_rows + slot * p.rows;
         const int32_t *shift_of = shifts + slot * p.rows;
         const uint4 *tile = ring + stage * tile_vecs;
@@ -196,48 +261,52 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 8) compact_kerne
         slot = next(slot, kRings);
         slot_ahead = next(slot_ahead, kRings);
         slot_put = next(slot_put, kRings);
+        if (!writing) continue;
         if (!turn) {
 #pragma unroll
             for (int u = 0; u < kLoads; ++u)
                 if (row_of[u] < p.rows && src[row_of[u]] >= 0)
-                    *reinterpret_cast<uint4 *>(p.pool + dst[row_of[u]] + vec_of[u] * 8) = tile[tid + u * THREADS];
+                    *reinterpret_cast<uint4 *>(p.pool + dst[row_of[u]] + off_of[u]) = tile[tid + u * THREADS];
             continue;
         }
         for (int r = row0; r < p.rows; r += apart) {
             if (src[r] < 0) continue;
-            const uint16_t *from = reinterpret_cast<const uint16_t *>(tile) + r * p.d;
+            const uint16_t *from = reinterpret_cast<const uint16_t *>(tile) + r * p.heads * p.d;
             uint16_t *to = p.pool + dst[r];
-            if (turning) {
-                Vec lo = *reinterpret_cast<const Vec *>(from + at0), hi = *reinterpret_cast<const Vec *>(from + at1);
-                const int32_t shift = shift_of[r];
-                if (shift != 0) {                          // (0: into another block at its old position)
-                    if (shift != turned) {                 // a window slides by one distance: once for all its rows
+            const int32_t shift = shift_of[r];
+            if (turning && shift != turned && shift != 0) {   // a window slides by one distance: once for all its rows
 #pragma unroll
-                        for (int i = 0; i < V; ++i) cs[i] = rotary_cos_sin(shift, __ldg(p.turns + c * V + i), 1.f);
-                        turned = shift;
-                    }
-                    rotate_pairs<V, INTERLEAVED>(lo, hi, cs);
+                for (int i = 0; i < V; ++i) cs[i] = rotary_cos_sin(shift, turns[i * p.rot_chunks + c]);
+                turned = shift;
+            }
+            for (int i = 0; i < p.heads; ++i, from += p.d, to += head_stride) {
+                if (turning) {
+                    Vec lo = *reinterpret_cast<const Vec *>(from + at0), hi = *reinterpret_cast<const Vec *>(from + at1);
+                    // (shift 0: into another block at its old position)
+                    if (shift != 0) rotate_pairs<V, INTERLEAVED>(lo, hi, cs);
+                    *reinterpret_cast<Vec *>(to + at0) = lo;
+                    *reinterpret_cast<Vec *>(to + at1) = hi;
+                } else if (passing) {
+                    *reinterpret_cast<Vec *>(to + at0) = *reinterpret_cast<const Vec *>(from + at0);
                 }
-                *reinterpret_cast<Vec *>(to + at0) = lo;
-                *reinterpret_cast<Vec *>(to + at1) = hi;
-            } else if (passing) {
-                *reinterpret_cast<Vec *>(to + at0) = *reinterpret_cast<const Vec *>(from + at0);
             }
         }
     }
     copy_wait<0>();
+    if (CLUSTER) cluster_sync();                           // nobody leaves while others may still store here
 }
 
 template <int V, bool INTERLEAVED, int THREADS, int STAGES, bool CLUSTER>
 cudaError_t launch_compact_as(const CompactParams &p, int x, int32_t num_kv_heads, int32_t num_seqs,
                               cudaStream_t stream) {
     const auto kernel = compact_kernel<V, INTERLEAVED, THREADS, STAGES, CLUSTER>;
-    const size_t smem = (size_t)STAGES * p.rows * (p.d / 8) * sizeof(uint4) +
-                        (size_t)(STAGES + 2) * p.rows * (2 * sizeof(int64_t) + sizeof(int32_t));
+    const size_t smem = (size_t)STAGES * p.rows * p.heads * (p.d / 8) * sizeof(uint4) +
+                        (size_t)(STAGES + 2) * p.rows * (2 * sizeof(int64_t) + sizeof(int32_t)) +
+                        (size_t)p.rot_chunks * V * sizeof(uint64_t);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(x, 2 * num_kv_heads, num_seqs);
+    cfg.gridDim = dim3(x, 2 * (num_kv_heads / p.heads), num_seqs);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -260,25 +329,39 @@ cudaError_t launch_compact_as(const CompactParams &p, int x, int32_t num_kv_head
 template <int V, bool INTERLEAVED>
 cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num_seqs, cudaStream_t stream) {
     const int row_vecs = p.d / 8;
+    p.heads = 1;
     if (p.max_keep <= 32 && p.max_keep * row_vecs <= 32 * kLoads && p.chunks <= 32) {
         // a few rows a sequence (accepted drafts): one warp has them in one tile,
         // and all units are on the SMs at once
         p.rows = p.max_keep;
         return launch_compact_as<V, INTERLEAVED, 32, 2, false>(p, 1, num_kv_heads, num_seqs, stream);
     }
-    p.rows = std::min({256 * kLoads / row_vecs, kMaxRows, p.max_keep});
-    // CTAs a unit, no more than there are tiles: out of place enough to give every
-    // SM four; in place the largest cluster that leaves every SM about two to four
-    const int64_t units = 2ll * num_kv_heads * num_seqs, tiles = ((int64_t)p.max_keep + p.rows - 1) / p.rows;
-    const int sms = device_sm_count();
-    if (p.src_tables != p.dst_tables) {
-        const int x = (int)std::min<int64_t>(tiles, (4 * sms + units - 1) / units);
+    // Two heads share a unit, and the angles, where keys turn and units are many
+    // (in place a cluster of 16 has to be enough to give every SM two CTAs).
+    const bool ordered = p.src_tables == p.dst_tables;
+    const int sms = device_sm_count(), most = 256 * kLoads / row_vecs;
+    const int64_t pairs = (int64_t)num_kv_heads * num_seqs;
+    if (p.turns && num_kv_heads % 2 == 0 && (!ordered || pairs * 16 >= 2 * sms)) p.heads = 2;
+    p.rows = std::min({most / p.heads, kMaxRows, p.max_keep});
+    const int64_t units = 2ll * (num_kv_heads / p.heads) * num_seqs, tiles = ((int64_t)p.max_keep + p.rows - 1) / p.rows;
+    // Then CTAs share a unit, no more than there are tiles: out of place enough to
+    // give every SM four, in place the smallest cluster that gives it two.
+    if (!ordered) {
+        const int x = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, 4 * sms / units));
         return launch_compact_as<V, INTERLEAVED, 256, 3, false>(p, x, num_kv_heads, num_seqs, stream);
     }
     int x = 1;
     while (x < 16 && x < tiles && units * x < 2 * sms) x *= 2;
-    return x == 1 ? launch_compact_as<V, INTERLEAVED, 256, 3, false>(p, x, num_kv_heads, num_seqs, stream)
-                  : launch_compact_as<V, INTERLEAVED, 256, 3, true>(p, x, num_kv_heads, num_seqs, stream);
+    if (x == 1) return launch_compact_as<V, INTERLEAVED, 256, 3, false>(p, x, num_kv_heads, num_seqs, stream);
+    // Four tiles ahead: of 16 KB for clusters of 16, whose CTAs are few (131,072
+    // tokens, half of them kept: 112 us, against 133 with tiles of 12 KB); of 12 KB
+    // otherwise, so that four CTAs fit an SM and all clusters run at once (a window
+    // over 8 x 8,192 tokens: 52 us, against 72).  A chunk needs a thread (V = 1: up
+    // to 255 chunks).
+    if (x == 16 || p.chunks > 192)
+        return launch_compact_as<V, INTERLEAVED, 256, 4, true>(p, x, num_kv_heads, num_seqs, stream);
+    p.rows = std::min({192 * kLoads / (row_vecs * p.heads), kMaxRows, p.max_keep});
+    return launch_compact_as<V, INTERLEAVED, 192, 4, true>(p, x, num_kv_heads, num_seqs, stream);
 }
 
 }  // namespace

@@ -16,13 +16,24 @@ namespace pa {
 // of the true values (PTX's bound), 2^-11 of a bf16 rounding step of the result's
 // length, which the one rounding to bf16 hides; the library's accurate functions
 // would cost some twenty instructions more a pair.
-__device__ __forceinline__ float2 rotary_cos_sin(int64_t offset, uint64_t turns, float m) {
-    const uint64_t phase = (uint64_t)offset * turns;
-    const float angle = (float)(int32_t)(phase >> 32) * 1.46291807926715968105e-9f;   // 2 pi / 2^32
+__device__ __forceinline__ float2 phase_cos_sin(uint32_t phase) {
+    const float angle = (float)(int32_t)phase * 1.46291807926715968105e-9f;   // 2 pi / 2^32
     float s, c;
     asm("sin.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(angle));
     asm("cos.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(angle));
-    return make_float2(c * m, s * m);
+    return make_float2(c, s);
+}
+__device__ __forceinline__ float2 rotary_cos_sin(int64_t offset, uint64_t turns, float m) {
+    const float2 cs = phase_cos_sin((uint32_t)(((uint64_t)offset * turns) >> 32));
+    return make_float2(cs.x * m, cs.y * m);
+}
+// The same phase of a 32-bit offset in three instructions: its upper word is
+// offset * upper + the upper word of offset * lower, less lower for a negative offset
+// (whose unsigned form is 2^32 too large).
+__device__ __forceinline__ float2 rotary_cos_sin(int32_t offset, uint64_t turns) {
+    const uint32_t lower = (uint32_t)turns;
+    return phase_cos_sin((uint32_t)offset * (uint32_t)(turns >> 32) + __umulhi((uint32_t)offset, lower) -
+                         (offset < 0 ? lower : 0u));
 }
 
 // V bf16 values (V = 8, 4, 2 or 1) moved as one access.
