@@ -567,7 +567,10 @@ pa_status pa_rotate_and_cache(const pa_kv_pool *pool, void *q_out, const void *q
  * draft, a sliding window behind its first tokens, any subset.
  *   src_tables, dst_tables  device, [num_seqs][max_blocks_per_seq] int32.  The
  *              same pointer: in place.  Different: the blocks written must not
- *              be read by any row of this call (a compacted fork)
+ *              be read by any row of this call (a compacted fork); a row that
+ *              would move into the block src_tables has at that place raises
+ *              PA_DEVERR_BLOCK_ID and is skipped.  (Unmoved rows may keep their
+ *              blocks: equal entries for a common beginning are fine)
  *   seq_lens   device, [num_seqs] int32: tokens cached
  *   keep       device, [num_seqs][max_keep] int32: positions, strictly
  *              ascending, starts[s] + i <= keep[s][i] < seq_lens[s].  (In place
@@ -622,7 +625,8 @@ pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, c
  * in fp32 over the elements a warp holds together and exactly beyond; rows of
  * equal logits have equal sums.
  *   workspace    device, 256-byte aligned, pa_beam_select_workspace_size bytes;
- *                overwritten
+ *                overwritten (calls that may run at the same time, on two streams
+ *                or from two graphs, need one each)
  * Supported: 1 <= num_beams <= 64; 1 <= num_out <= 64 and <= num_beams * vocab;
  * 0 <= end_token < vocab where finished is given; num_groups * num_beams at
  * most 65,535; num_beams * vocab at most 2^31 - 1.

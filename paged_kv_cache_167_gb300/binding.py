@@ -506,7 +506,7 @@ def _refuse(t, dtype, name: str, device: int):
 
 def _at(t: torch.Tensor, dtype, name: str, device: int) -> int:
     """Address of a dense tensor on the current device (where the library launches)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
         _refuse(t, dtype, name, device)
     return t.data_ptr()
 

@@ -85,6 +85,7 @@ struct RowLookup {
     int32_t from = 0, before = 0;      // keep[i] and keep[i - 1]
     int32_t to = 0;                    // start + i
     int32_t src_block = 0, dst_block = 0;
+    int32_t own_block = -1;            // out of place: what src_tables has where dst_block is
     bool row = false;                  // false: no such row, or a bad one
 };
 
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
         if (r.row) {
             r.src_block = __ldg(src_table + block_of(r.from));
             r.dst_block = __ldg(dst_table + block_of(r.to));
+            if (src_table != dst_table) r.own_block = __ldg(src_table + block_of(r.to));
         }
         return r;
     };
@@ -162,6 +164,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
             if (r.src_block < 0 || r.src_block >= p.num_blocks || r.dst_block < 0 || r.dst_block >= p.num_blocks) {
                 if (reports) raise_error(p.err, PA_DEVERR_BLOCK_ID);
             } else if (r.from != r.to || r.src_block != r.dst_block) {
+                // out of place nothing orders the tiles: a block that the sequence
+                // still reads is not written
+                if (r.dst_block == r.own_block) {
+                    if (reports) raise_error(p.err, PA_DEVERR_BLOCK_ID);
+                    src_rows[slot * p.rows + tid] = -1;
+                    return;
+                }
                 src = r.src_block * p.block_stride + base + (r.from - (int)block_of(r.from) * p.block_size) * p.d;
                 dst = r.dst_block * p.block_stride + base + (r.to - (int)block_of(r.to) * p.block_size) * p.d;
             }

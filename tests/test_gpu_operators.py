@@ -632,6 +632,160 @@ def test_captured_and_replayed(pa):
     assert pa.get_device_error() == 0
 
 
+@pytest.mark.parametrize("hkv,rot", [(8, None), (2, 64), (1, 10), (3, None)])
+def test_compact_clusters_captured_and_beside_other_work(pa, hkv, rot):
+    """Long in-place compactions that clusters of CTAs share, captured and
+    replayed, while another stream copies memory: the same bits as an eager run
+    of the out-of-place form into fresh blocks."""
+    b, d, L = 16, 64, 20000
+    rng = np.random.default_rng(hkv)
+    keep = _scattered(rng, L, 12000)
+    width = -(-L // b)
+    ids = rng.permutation(2 * width).astype(np.int32)
+    src, fresh = cuda(ids[None, :width].copy()), cuda(ids[None, width:].copy())
+    start = normal((2 * width, 2, hkv, b, d), 5)
+    lens, counts = cuda(np.asarray([L], np.int32)), cuda(np.asarray([len(keep)], np.int32))
+    keep_t = cuda(keep.astype(np.int32)[None])
+    freqs = cuda(pa.rotary_frequencies(rot)) if rot else None
+    other = start.clone()
+    pa.compact_tokens(other, src, fresh, lens, keep_t, counts, freqs=freqs)
+    order = torch.as_tensor(ids.astype(np.int64), device="cuda")
+    at = torch.arange(len(keep), device="cuda")
+    want = other[order[width:][at // b], :, :, at % b]
+    pool = start.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.compact_tokens(pool, src, src, lens, keep_t, counts, freqs=freqs)
+    side, junk = torch.cuda.Stream(), torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    target = torch.empty_like(junk)
+    for _ in range(6):
+        pool.copy_(start)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            target.copy_(junk)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = pool[order[:width][at // b], :, :, at % b]
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        # rows behind the last one, and blocks of nobody, as they were
+        rest = torch.arange(len(keep), L, device="cuda")
+        assert torch.equal(pool[order[:width][rest // b], :, :, rest % b],
+                           start[order[:width][rest // b], :, :, rest % b])
+        assert torch.equal(pool[order[width:]], start[order[width:]])
+    assert pa.get_device_error() == 0
+
+
+def test_compact_fork_keeps_a_common_beginning_and_refuses_its_own_blocks(pa):
+    """Equal table entries for unmoved rows are fine out of place; a row that
+    would move into a block the sequence still reads is refused."""
+    b, d, hkv, L = 16, 64, 2, 160
+    rng = np.random.default_rng(8)
+    ids = rng.permutation(24).astype(np.int32)
+    src = ids[None, :10].copy()
+    dst = np.concatenate([ids[:3], ids[10:17]])[None].copy()      # three shared blocks, then fresh ones
+    keep = np.concatenate([np.arange(48), 48 + _scattered(rng, 112, 60)])
+    pool = normal((24, 2, hkv, b, d), 9)
+    want, size = ref.compact(f64(pool), src, dst, keep[None], [len(keep)], None, ref.angular_frequencies(64), False)
+    args = (cuda(np.asarray([L], np.int32)), cuda(keep.astype(np.int32)[None]), cuda(np.asarray([len(keep)], np.int32)))
+    pa.compact_tokens(pool, cuda(src), cuda(dst), *args, freqs=cuda(pa.rotary_frequencies(64)))
+    assert pa.get_device_error() == 0
+    check_rotated(pool, want, size, "common beginning")
+    clone = pool.clone()
+    pa.compact_tokens(pool, cuda(src), cuda(src.copy()), *args)      # another tensor of the same blocks
+    assert pa.get_device_error() == 0x1
+    moved = keep != np.arange(len(keep))
+    assert moved.any() and torch.equal(pool, clone)
+
+
+def test_offsets_beyond_32_bits(pa):
+    """Slots and rows behind 2^32 bytes of one pool."""
+    nb, hkv, b, d = 70000, 8, 16, 128                               # 4.6 GB
+    pool = torch.zeros((nb, 2, hkv, b, d), dtype=torch.bfloat16, device="cuda")
+    high = np.asarray([69999, 65537, 66000, 3], np.int32)
+    n = 64
+    k, v = normal((n, hkv, d), 1), normal((n, hkv, d), 2)
+    slots = (high.astype(np.int64)[:, None] * b + np.arange(b)).ravel()
+    w, freqs = ref.angular_frequencies(d), cuda(pa.rotary_frequencies(d))
+    pa.rotate_and_cache(pool, None, None, k, v, cuda(np.arange(n)), cuda(slots), freqs)
+    rows, sizes = rotated(f64(k), np.arange(n), w, False)
+    at = torch.as_tensor(high.astype(np.int64), device="cuda")
+    got = pool[at]                                                   # [4][2][Hkv][b][d]
+    check_rotated(got[:, 0].transpose(1, 2).reshape(n, hkv, d), rows, sizes, "slots")
+    assert torch.equal(got[:, 1].transpose(1, 2).reshape(n, hkv, d), v)
+    keep = np.arange(1, 64, 2)
+    table = cuda(high[None].copy())
+    pa.compact_tokens(pool, table, table, cuda(np.asarray([n], np.int32)), cuda(keep.astype(np.int32)[None]),
+                      cuda(np.asarray([len(keep)], np.int32)))
+    after = pool[at]
+    flat, old = after.transpose(2, 3).reshape(4, 2, b, hkv, d), got.transpose(2, 3).reshape(4, 2, b, hkv, d)
+    for i, p in enumerate(keep):
+        assert torch.equal(flat[i // b, :, i % b], old[p // b, :, p % b])
+    assert pa.get_device_error() == 0
+    pool[at] = 0
+    assert int(torch.count_nonzero(pool.view(torch.int64).view(-1))) == 0   # nothing else was touched
+
+
+def test_beam_select_offsets_beyond_32_bits(pa):
+    """More than 2^31 logits: one spike a row, the last rows read right."""
+    rows, V = 300, 7_500_001
+    x = torch.zeros((rows, 1, V), dtype=torch.bfloat16, device="cuda")
+    spike = (torch.arange(rows, device="cuda") * 24593 + 12345) % V
+    x[torch.arange(rows, device="cuda"), 0, spike] = 20.0
+    s = torch.zeros((rows, 1), device="cuda")
+    scores, parents, tokens = _select(pa, x, s, 2)
+    assert torch.equal(tokens[:, 0].long(), spike) and not parents.any()
+    assert torch.equal(tokens[:, 1].long(), torch.where(spike == 0, 1, 0))
+    want = -math.log1p((V - 1) * math.exp(-20.0))
+    # the sum of equal small terms: 2^-22 each (the hardware's 2^x), and a thread's
+    # additions, at most V / 256 of them, one half step each
+    tol = 2.0 ** -22 + (V / 256 + 64) * 2.0 ** -24
+    assert float((scores[:, 0] - want).abs().max()) <= tol
+    assert float((scores[:, 1] - (want - 20.0)).abs().max()) <= tol + 2.0 ** -19
+    assert pa.get_device_error() == 0
+
+
+def test_two_streams_at_once(pa):
+    """The same calls on two streams at the same time, each with its own buffers."""
+    x, s = _random_beams(16, 4, 40000, seed=12, dtype=torch.bfloat16)
+    pool0 = normal((300, 2, 4, 16, 64), 1)
+    q, k, v = normal((512, 8, 64), 2), normal((512, 4, 64), 3), normal((512, 4, 64), 4)
+    pos, slots = cuda(np.arange(512)), cuda(np.arange(512) + 7)
+    freqs = cuda(pa.rotary_frequencies(64))
+    table = cuda(np.arange(300, dtype=np.int32)[None])
+    keep = cuda(np.arange(1000, 4000, dtype=np.int32)[None])
+    lens, counts = cuda(np.asarray([4500], np.int32)), cuda(np.asarray([3000], np.int32))
+    nbytes = pa.beam_select_workspace_size(16, 4, 40000, 8)
+
+    def buffers():
+        return (pool0.clone(), torch.empty_like(q), torch.empty(nbytes, dtype=torch.uint8, device="cuda"),
+                (torch.empty((16, 8), device="cuda"), torch.empty((16, 8), dtype=torch.int32, device="cuda"),
+                 torch.empty((16, 8), dtype=torch.int32, device="cuda")))
+
+    def run(held, stream):
+        pool, q_out, ws, out = held
+        pa.rotate_and_cache(pool, q_out, q, k, v, pos, slots, freqs, stream=stream)
+        pa.compact_tokens(pool, table, table, lens, keep, counts, freqs=freqs, stream=stream)
+        pa.beam_select(*out, x, s, workspace=ws, stream=stream)
+
+    alone = buffers()
+    run(alone, None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    held = [buffers() for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (pool, *_rest), stream in zip(held, streams):
+            with torch.cuda.stream(stream):
+                pool.copy_(pool0)
+        for h, stream in zip(held, streams):
+            run(h, stream)
+    torch.cuda.synchronize()
+    for pool, q_out, _, out in held:
+        assert torch.equal(pool, alone[0]) and torch.equal(q_out, alone[1])
+        assert all(torch.equal(a, b) for a, b in zip(out, alone[3]))
+    assert pa.get_device_error() == 0
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
