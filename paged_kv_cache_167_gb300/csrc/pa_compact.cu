@@ -4,9 +4,9 @@
 // A unit is one sequence's K or V rows of one or several kv-heads (several share
 // the rows' places and, for keys, their angles); it is taken in tiles of up to 16 KB.
 // A tile is gathered into shared memory by asynchronous 16-byte copies, two tiles
-// ahead of the one being written; the positions and table entries that say where
-// its rows lie are fetched further ahead still, so that no step waits for that
-// chain of loads.
+// (in a cluster three) ahead of the one being written; the positions and table
+// entries that say where its rows lie are fetched further ahead still, so that no
+// step waits for that chain of loads.
 //
 // In place, row i is written at start + i <= keep[i] < keep[i + 1]: what a tile
 // writes lies before everything that later tiles read, so it is enough that a
@@ -21,6 +21,15 @@
 // memory) before writes that have not begun; nobody reads what was written, so no
 // store has to be waited for.  Out of place the tiles are free of one another and
 // any number of CTAs share them.
+//
+// What bounds it: every moved row is read and written once, so DRAM where there are
+// enough units.  GB300, of the measured copy bandwidth: 64 x 3,000 tokens, half of
+// them kept, 91 us (0.85), the keys turned, each by its own distance, 114 us (0.68:
+// 64 registers a thread for four CTAs an SM, and the angles); a window over 8 x 8,192
+// tokens, all keys turned by one distance, 50 us (0.79); 131,072 tokens of one
+// sequence in place 105 us (0.75: 256 CTAs, a step of all of them takes 1.6 us), out
+// of place 93 us (0.85); 64 sequences with one to six accepted rows each 3.1 us, a
+// chain of four dependent loads behind a launch.
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -31,6 +40,12 @@ namespace {
 
 constexpr int kLoads = 4;                                  // 16-byte copies a thread has in a tile
 constexpr int kMaxRows = 96;
+
+// What is done to the components of a key: nothing, all of them turned, or some of
+// them.  A kernel each, since registers decide how many CTAs an SM holds: with one
+// for all, 131,072 tokens that do not turn took 112 us instead of 105, and a window
+// 52 instead of 50.
+enum { kAsTheyAre = 0, kWhole = 1, kParts = 2 };
 
 struct CompactParams {
     uint16_t *pool;
@@ -92,8 +107,9 @@ struct RowLookup {
 // grid (CTAs of one unit, 2 x head groups, sequence); CLUSTER: they are a cluster
 // and write in order, else each goes its own way (one CTA, or out of place).
 // STAGES tiles are in shared memory or on their way there.
-template <int V, bool INTERLEAVED, int THREADS, int STAGES, bool CLUSTER>
-__global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 && CLUSTER ? 3 : 4) compact_kernel(const CompactParams p) {
+template <int V, bool INTERLEAVED, int TURNS, int THREADS, int STAGES, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 && CLUSTER ? 3 : 4)
+    compact_kernel(const CompactParams p) {
     using Vec = typename BfVec<V>::type;
     constexpr int kRings = STAGES + 2;                     // tiles whose rows' places are known
     extern __shared__ __align__(16) uint4 ring[];          // [STAGES][rows][heads][d / 8], then the rows' places
@@ -111,8 +127,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
     asm volatile("griddepcontrol.launch_dependents;");
     const int kv = blockIdx.y & 1, h = (blockIdx.y >> 1) * p.heads, s = blockIdx.z, tid = threadIdx.x;
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
-    const int64_t len = __ldg(p.seq_lens + s), n = __ldg(p.keep_lens + s);
-    const int64_t start = p.starts ? __ldg(p.starts + s) : 0;
+    const int32_t len = __ldg(p.seq_lens + s), n = __ldg(p.keep_lens + s);
+    const int32_t start = p.starts ? __ldg(p.starts + s) : 0;
     const bool reports = h == 0 && kv == 0;
     if (len < 0 || len > cap || n < 0 || n > p.max_keep || start < 0) {
         if (tid == 0 && reports && blockIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_LEN);
@@ -122,23 +138,23 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
     const int32_t *src_table = p.src_tables + (int64_t)s * p.max_blocks;
     const int32_t *dst_table = p.dst_tables + (int64_t)s * p.max_blocks;
     const int64_t base = kv * p.kv_stride + (int64_t)h * p.block_size * p.d;
-    const bool turn = p.turns != nullptr && kv == 0;
-    const int32_t tiles = (int32_t)((n + p.rows - 1) / p.rows);
+    const bool turn = TURNS != kAsTheyAre && kv == 0;
+    const int32_t tiles = (int32_t)(((uint32_t)n + p.rows - 1) / p.rows);
     const int32_t steps = (tiles - (CLUSTER ? 0 : (int)blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
     const bool looks = tid < p.rows;
 
     // The chain behind a row's place: keep -> table entries -> offsets, one call
     // (and one step of the loop below) each, so that no call uses what it has just
     // asked for.  Threads 0 .. rows - 1 take a row.
-    int64_t next_row = (int64_t)blockIdx.x * p.rows + tid;   // of the next look_keep
+    uint32_t next_row = blockIdx.x * p.rows + tid;         // of the next look_keep (past 2^31 by a few tiles at most)
     auto look_keep = [&]() {
         RowLookup r;
-        const int64_t i = next_row;
-        next_row += (int64_t)gridDim.x * p.rows;
-        if (!looks || i >= n) return r;
+        const uint32_t i = next_row;
+        next_row += gridDim.x * p.rows;
+        if (!looks || i >= (uint32_t)n) return r;
         r.before = i > 0 ? __ldg(keep + i - 1) : -1;
         r.from = __ldg(keep + i);
-        r.to = (int32_t)min(start + i, (int64_t)INT32_MAX);   // (beyond every length: refused)
+        r.to = (int32_t)min((uint32_t)start + i, (uint32_t)INT32_MAX);   // (beyond every length: refused)
         r.row = true;
         return r;
     };
@@ -181,38 +197,42 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
         shifts[at] = r.to - r.from;
     };
 
-    // this thread's vectors of a tile: (row, elements from the row's place), the
-    // same in all tiles
+    // A tile's vectors are taken `at_once` whole rows at a time; this thread's are one
+    // vector of rows my_row, my_row + at_once, ..., my_off elements from the row's place.
     const int head_stride = p.block_size * p.d;
-    int row_of[kLoads], off_of[kLoads];
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-        row_of[u] = (tid + u * THREADS) / row_vecs;
-        const int vec = (tid + u * THREADS) - row_of[u] * row_vecs, head = vec / (p.d / 8);
-        off_of[u] = head * head_stride + (vec - head * (p.d / 8)) * 8;
-    }
+    const int at_once = THREADS / row_vecs;
+    int my_row = tid / row_vecs, my_off = tid - my_row * row_vecs;
+    my_off = my_off / (p.d / 8) * head_stride + my_off % (p.d / 8) * 8;
+    if (my_row >= at_once) my_row = p.rows;                // (no whole row is left for it)
     auto begin_copies = [&](int32_t k, int stage, int slot) {
         if (k < steps) {
             const int64_t *src = src_rows + slot * p.rows;
             uint4 *tile = ring + stage * tile_vecs + tid;
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u)
-                if (row_of[u] < p.rows && src[row_of[u]] >= 0)
-                    copy_async(tile + u * THREADS, p.pool + src[row_of[u]] + off_of[u]);
+            for (int u = 0; u < kLoads; ++u) {
+                const int r = my_row + u * at_once;
+                if (r < p.rows && src[r] >= 0) copy_async(tile + u * at_once * row_vecs, p.pool + src[r] + my_off);
+            }
         }
         copy_commit();                                     // (an empty group where nothing is left)
     };
     auto next = [](int i, int count) { return i + 1 == count ? 0 : i + 1; };
 
-    // this thread's chunk of the rows it turns: every `apart`-th row from `row0` on
-    const int apart = turn ? max(THREADS / p.chunks, 1) : 1, row0 = turn ? tid / p.chunks : 0, c = turn ? tid - row0 * p.chunks : 0;
-    const bool turning = turn && row0 < apart && c < p.rot_chunks, passing = turn && row0 < apart && !turning;
+    // This thread's chunk of the rows it turns, every `apart`-th row from `row0` on,
+    // and its chunk of the components that pass, in a loop of their own: neighbouring
+    // threads do the same, where a row's chunks side by side would have each warp go
+    // both ways (33 x 3,000 tokens of 64 components, 32 of them turned: 26 us, now 22).
+    const int half = TURNS == kWhole ? p.d / 2 : p.rot_chunks * V;
+    const int pass_chunks = TURNS == kParts ? p.chunks - p.rot_chunks : 0;
+    const int apart = turn ? THREADS / p.rot_chunks : 1;
+    int row0 = turn ? tid / p.rot_chunks : 0;
+    const int c = turn ? tid - row0 * p.rot_chunks : 0;
+    if (row0 >= apart) row0 = p.rows;                      // (no whole row is left for it)
     float2 cs[V];
     int32_t turned = 0;                                    // the shift that cs belongs to
-    const int half = p.rot_chunks * V;
     if (turn)
         for (int i = tid; i < half; i += THREADS) turns[i % V * p.rot_chunks + i / V] = __ldg(p.turns + i);
-    const int at0 = !turning ? 2 * half + (c - p.rot_chunks) * V : INTERLEAVED ? 2 * c * V : c * V;
+    const int at0 = INTERLEAVED ? 2 * c * V : c * V;
     const int at1 = INTERLEAVED ? at0 + V : half + at0;
 
 #pragma unroll
@@ -273,42 +293,49 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
         if (!writing) continue;
         if (!turn) {
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u)
-                if (row_of[u] < p.rows && src[row_of[u]] >= 0)
-                    *reinterpret_cast<uint4 *>(p.pool + dst[row_of[u]] + off_of[u]) = tile[tid + u * THREADS];
+            for (int u = 0; u < kLoads; ++u) {
+                const int r = my_row + u * at_once;
+                if (r < p.rows && src[r] >= 0)
+                    *reinterpret_cast<uint4 *>(p.pool + dst[r] + my_off) = tile[tid + u * at_once * row_vecs];
+            }
             continue;
         }
+        const uint16_t *rows = reinterpret_cast<const uint16_t *>(tile);
         for (int r = row0; r < p.rows; r += apart) {
             if (src[r] < 0) continue;
-            const uint16_t *from = reinterpret_cast<const uint16_t *>(tile) + r * p.heads * p.d;
+            const uint16_t *from = rows + r * p.heads * p.d;
             uint16_t *to = p.pool + dst[r];
             const int32_t shift = shift_of[r];
-            if (turning && shift != turned && shift != 0) {   // a window slides by one distance: once for all its rows
+            if (shift != turned && shift != 0) {           // a window slides by one distance: once for all its rows
 #pragma unroll
                 for (int i = 0; i < V; ++i) cs[i] = rotary_cos_sin(shift, turns[i * p.rot_chunks + c]);
                 turned = shift;
             }
             for (int i = 0; i < p.heads; ++i, from += p.d, to += head_stride) {
-                if (turning) {
-                    Vec lo = *reinterpret_cast<const Vec *>(from + at0), hi = *reinterpret_cast<const Vec *>(from + at1);
-                    // (shift 0: into another block at its old position)
-                    if (shift != 0) rotate_pairs<V, INTERLEAVED>(lo, hi, cs);
-                    *reinterpret_cast<Vec *>(to + at0) = lo;
-                    *reinterpret_cast<Vec *>(to + at1) = hi;
-                } else if (passing) {
-                    *reinterpret_cast<Vec *>(to + at0) = *reinterpret_cast<const Vec *>(from + at0);
-                }
+                Vec lo = *reinterpret_cast<const Vec *>(from + at0), hi = *reinterpret_cast<const Vec *>(from + at1);
+                // (shift 0: into another block at its old position)
+                if (shift != 0) rotate_pairs<V, INTERLEAVED>(lo, hi, cs);
+                *reinterpret_cast<Vec *>(to + at0) = lo;
+                *reinterpret_cast<Vec *>(to + at1) = hi;
             }
+        }
+        for (int j = tid; j < p.rows * pass_chunks; j += THREADS) {
+            const int r = (uint32_t)j / (uint32_t)pass_chunks, at = 2 * half + (j - r * pass_chunks) * V;
+            if (src[r] < 0) continue;
+            const uint16_t *from = rows + r * p.heads * p.d + at;
+            uint16_t *to = p.pool + dst[r] + at;
+            for (int i = 0; i < p.heads; ++i, from += p.d, to += head_stride)
+                *reinterpret_cast<Vec *>(to) = *reinterpret_cast<const Vec *>(from);
         }
     }
     copy_wait<0>();
     if (CLUSTER) cluster_sync();                           // nobody leaves while others may still store here
 }
 
-template <int V, bool INTERLEAVED, int THREADS, int STAGES, bool CLUSTER>
+template <int V, bool INTERLEAVED, int TURNS, int THREADS, int STAGES, bool CLUSTER>
 cudaError_t launch_compact_as(const CompactParams &p, int x, int32_t num_kv_heads, int32_t num_seqs,
                               cudaStream_t stream) {
-    const auto kernel = compact_kernel<V, INTERLEAVED, THREADS, STAGES, CLUSTER>;
+    const auto kernel = compact_kernel<V, INTERLEAVED, TURNS, THREADS, STAGES, CLUSTER>;
     const size_t smem = (size_t)STAGES * p.rows * p.heads * (p.d / 8) * sizeof(uint4) +
                         (size_t)(STAGES + 2) * p.rows * (2 * sizeof(int64_t) + sizeof(int32_t)) +
                         (size_t)p.rot_chunks * V * sizeof(uint64_t);
@@ -335,42 +362,52 @@ cudaError_t launch_compact_as(const CompactParams &p, int x, int32_t num_kv_head
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int V, bool INTERLEAVED>
+template <int V, bool INTERLEAVED, int TURNS>
 cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num_seqs, cudaStream_t stream) {
+    // threads of a CTA that is not in a cluster: two loops need more registers than
+    // four CTAs of 256 have (330 x 3,000 tokens, half turned: 160 us, now 143)
+    constexpr int kAlone = TURNS == kParts ? 192 : 256;
     const int row_vecs = p.d / 8;
     p.heads = 1;
-    if (p.max_keep <= 32 && p.max_keep * row_vecs <= 32 * kLoads && p.chunks <= 32) {
+    if (p.max_keep <= 32 && p.max_keep <= kLoads * (32 / row_vecs) && p.rot_chunks <= 32) {
         // a few rows a sequence (accepted drafts): one warp has them in one tile,
-        // and all units are on the SMs at once
+        // and all units are on the SMs at once (64 sequences: 3.1 us, 6.7 with 256
+        // threads)
         p.rows = p.max_keep;
-        return launch_compact_as<V, INTERLEAVED, 32, 2, false>(p, 1, num_kv_heads, num_seqs, stream);
+        return launch_compact_as<V, INTERLEAVED, TURNS, 32, 2, false>(p, 1, num_kv_heads, num_seqs, stream);
     }
     // Two heads share a unit, and the angles, where keys turn and units are many
-    // (in place a cluster of 16 has to be enough to give every SM two CTAs).
+    // (in place a cluster of 16 has to be enough to give every SM two CTAs): of
+    // 64 x 3,000 tokens 127 us became 120, of a window 53 became 50.
     const bool ordered = p.src_tables == p.dst_tables;
-    const int sms = device_sm_count(), most = 256 * kLoads / row_vecs;
+    const int sms = device_sm_count();
     const int64_t pairs = (int64_t)num_kv_heads * num_seqs;
-    if (p.turns && num_kv_heads % 2 == 0 && (!ordered || pairs * 16 >= 2 * sms)) p.heads = 2;
-    p.rows = std::min({most / p.heads, kMaxRows, p.max_keep});
-    const int64_t units = 2ll * (num_kv_heads / p.heads) * num_seqs, tiles = ((int64_t)p.max_keep + p.rows - 1) / p.rows;
+    if (TURNS != kAsTheyAre && num_kv_heads % 2 == 0 && (!ordered || pairs * 16 >= 2 * sms)) p.heads = 2;
+    p.rows = std::min({kLoads * (kAlone / (row_vecs * p.heads)), kMaxRows, p.max_keep});
+    const int64_t units = 2ll * (num_kv_heads / p.heads) * num_seqs;
+    const int64_t tiles = ((int64_t)p.max_keep + p.rows - 1) / p.rows;
     // Then CTAs share a unit, no more than there are tiles: out of place enough to
-    // give every SM four, in place the smallest cluster that gives it two.
+    // give every SM four (33 x 3,000 tokens of 128 components: 28.7 us, with six 30.9;
+    // half turned of 64: 22.2, with two 35), in place the smallest cluster that gives
+    // it two.
     if (!ordered) {
         const int x = (int)std::min<int64_t>(tiles, std::max<int64_t>(1, 4 * sms / units));
-        return launch_compact_as<V, INTERLEAVED, 256, 3, false>(p, x, num_kv_heads, num_seqs, stream);
+        return launch_compact_as<V, INTERLEAVED, TURNS, kAlone, 3, false>(p, x, num_kv_heads, num_seqs, stream);
     }
     int x = 1;
     while (x < 16 && x < tiles && units * x < 2 * sms) x *= 2;
-    if (x == 1) return launch_compact_as<V, INTERLEAVED, 256, 3, false>(p, x, num_kv_heads, num_seqs, stream);
-    // Four tiles ahead: of 16 KB for clusters of 16, whose CTAs are few (131,072
-    // tokens, half of them kept: 112 us, against 133 with tiles of 12 KB); of 12 KB
-    // otherwise, so that four CTAs fit an SM and all clusters run at once (a window
-    // over 8 x 8,192 tokens: 52 us, against 72).  A chunk needs a thread (V = 1: up
-    // to 255 chunks).
-    if (x == 16 || p.chunks > 192)
-        return launch_compact_as<V, INTERLEAVED, 256, 4, true>(p, x, num_kv_heads, num_seqs, stream);
-    p.rows = std::min({192 * kLoads / (row_vecs * p.heads), kMaxRows, p.max_keep});
-    return launch_compact_as<V, INTERLEAVED, 192, 4, true>(p, x, num_kv_heads, num_seqs, stream);
+    if (x == 1) return launch_compact_as<V, INTERLEAVED, TURNS, kAlone, 3, false>(p, x, num_kv_heads, num_seqs, stream);
+    // Four stages: of 16 KB for clusters of 16, whose CTAs are few (131,072 tokens,
+    // half of them kept: 105 us; 112 against 133 when tiles of 12 KB were tried; five
+    // stages: 183, since no longer all clusters are on the SMs at once); of 12 KB
+    // otherwise, so that four CTAs fit an SM (a window over 8 x 8,192 tokens: 50 us,
+    // with 16 KB 72).
+    if (x == 16) {
+        p.rows = std::min({kLoads * (256 / (row_vecs * p.heads)), kMaxRows, p.max_keep});
+        return launch_compact_as<V, INTERLEAVED, TURNS, 256, 4, true>(p, x, num_kv_heads, num_seqs, stream);
+    }
+    p.rows = std::min({kLoads * (192 / (row_vecs * p.heads)), kMaxRows, p.max_keep});
+    return launch_compact_as<V, INTERLEAVED, TURNS, 192, 4, true>(p, x, num_kv_heads, num_seqs, stream);
 }
 
 }  // namespace
@@ -399,26 +436,29 @@ cudaError_t launch_compact(const PoolView &pool, const int32_t *src_tables, cons
     p.starts = starts;
     p.err = device_error_word();
     if (!p.err) return cudaErrorUnknown;
-    if (!rotary) return launch_compact_v<8, false>(p, pool.num_kv_heads, num_seqs, stream);
+    if (!rotary) return launch_compact_v<8, false, kAsTheyAre>(p, pool.num_kv_heads, num_seqs, stream);
     const int v = rotary_vec(rotary->rot_dim);
     const bool interleaved = (rotary->flags & PA_ROTARY_INTERLEAVED) != 0;
     p.turns = rotary->turns;
     p.rot_chunks = rotary->rot_dim / 2 / v;
     p.chunks = p.rot_chunks + (p.d - rotary->rot_dim) / v;
     const int hkv = pool.num_kv_heads;
+    if (v == 8 && rotary->rot_dim == p.d)
+        return interleaved ? launch_compact_v<8, true, kWhole>(p, hkv, num_seqs, stream)
+                           : launch_compact_v<8, false, kWhole>(p, hkv, num_seqs, stream);
     switch (v) {
         case 8:
-            return interleaved ? launch_compact_v<8, true>(p, hkv, num_seqs, stream)
-                               : launch_compact_v<8, false>(p, hkv, num_seqs, stream);
+            return interleaved ? launch_compact_v<8, true, kParts>(p, hkv, num_seqs, stream)
+                               : launch_compact_v<8, false, kParts>(p, hkv, num_seqs, stream);
         case 4:
-            return interleaved ? launch_compact_v<4, true>(p, hkv, num_seqs, stream)
-                               : launch_compact_v<4, false>(p, hkv, num_seqs, stream);
+            return interleaved ? launch_compact_v<4, true, kParts>(p, hkv, num_seqs, stream)
+                               : launch_compact_v<4, false, kParts>(p, hkv, num_seqs, stream);
         case 2:
-            return interleaved ? launch_compact_v<2, true>(p, hkv, num_seqs, stream)
-                               : launch_compact_v<2, false>(p, hkv, num_seqs, stream);
+            return interleaved ? launch_compact_v<2, true, kParts>(p, hkv, num_seqs, stream)
+                               : launch_compact_v<2, false, kParts>(p, hkv, num_seqs, stream);
         default:
-            return interleaved ? launch_compact_v<1, true>(p, hkv, num_seqs, stream)
-                               : launch_compact_v<1, false>(p, hkv, num_seqs, stream);
+            return interleaved ? launch_compact_v<1, true, kParts>(p, hkv, num_seqs, stream)
+                               : launch_compact_v<1, false, kParts>(p, hkv, num_seqs, stream);
     }
 }
 

@@ -324,6 +324,23 @@ def test_compact_accepted_drafts(pa):
     _run_compaction(pa, lens, [np.asarray(k) for k in keeps], 2, 128, 16, 128, starts=starts, seed=3, fork=True)
 
 
+@pytest.mark.parametrize("d,rot,interleaved", [(80, 16, False), (24, 24, True), (200, 48, True), (256, 256, False),
+                                               (8, 2, False), (256, 2, True), (40, 20, False), (72, 24, True),
+                                               (256, 48, False)])
+def test_compact_head_sizes_in_every_split(pa, d, rot, interleaved):
+    """Head sizes whose vectors do not divide a CTA's threads, keys turned whole,
+    in part or not, in each way the work is split: a warp a sequence, one CTA, the
+    clusters of an ordered pass, and CTAs that share out-of-place tiles."""
+    rng = np.random.default_rng(d + rot)
+    splits = [([40, 9, 17, 64], [2, 0, 1, 2], 2), ([50 + i for i in range(90)], [25 + i // 3 for i in range(90)], 2),
+              ([700, 333, 512], [350, 333, 200], 4), ([2600], [1300], 1), ([900] * 12, [450] * 12, 2)]
+    for k, (lens, kept, hkv) in enumerate(splits):
+        keeps = [_scattered(rng, L, n) for L, n in zip(lens, kept)]
+        for r in (rot, None):
+            for fork in (False, True):
+                _run_compaction(pa, lens, keeps, hkv, d, 16, r, interleaved, fork, seed=d + k)
+
+
 def test_compact_layer_of_a_layered_pool(pa):
     rng = np.random.default_rng(6)
     _run_compaction(pa, [100, 37], [_scattered(rng, 100, 50), _scattered(rng, 37, 20)], 2, 64, 16, 64, layers=3,
