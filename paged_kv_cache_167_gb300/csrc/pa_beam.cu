@@ -28,6 +28,13 @@
 // have equal sums wherever they begin.  A slice whose maximum is beyond 2^22 in
 // size, where c would have no fraction left to lose (a row of the type's lowest
 // value, say), is summed again from its differences to that maximum.
+//
+// What bounds it: the logits are read once (plus the candidates' vectors from
+// cache).  GB300, of the measured copy bandwidth: 64 x 8 rows of 128,256 fp32 logits
+// 56 us (0.69; the 512 CTAs of the scan are three on some SMs and four on others, and
+// the merge takes 5 us).  Below that a chain of latencies: 32 x 4 rows of 128,256
+// bf16 logits 15.6 us (about 5 to stream, 3 for the slice's end, 5 to merge), 4 rows
+// of 32,000 9.9 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -747,7 +754,8 @@ int32_t chunks_of(int32_t vocab, int32_t vec) {
 
 // Slices of a row: as many as still run side by side, four CTAs on each of the
 // GB300's 152 SMs (the workspace is sized without a device at hand), no slice
-// without a chunk.
+// without a chunk.  (64 x 8 rows of 128,256: with two slices a row, so in
+// two waves, 80 us when one wave took 66; it takes 56 now.)
 int32_t slices_of(int64_t rows, int32_t row_chunks) {
     return (int32_t)std::max<int64_t>(1, std::min<int64_t>(row_chunks, kCtasPerSm * 152 / rows));
 }

@@ -7,6 +7,11 @@
 // token: thread (x, y) owns chunk x of heads y, y + Y, ..., so the V angles of a
 // thread are computed once and kept in registers for all of its heads, and all
 // of its loads are issued before the angles they wait for.
+//
+// What bounds it: every component is read and written once (two operations a
+// byte), so DRAM, and the host's call where tokens are few.  GB300, of the measured
+// copy bandwidth: 8,192 tokens of 64 query and 8 key heads of 128 components 52 us
+// (0.96), 32,000 tokens of a fused projection 191 us (1.01); 64 tokens 2.3 us.
 #include "pa_internal.h"
 #include "pa_rotary.cuh"
 
@@ -113,7 +118,9 @@ cudaError_t launch_rotate_v(RotateParams &p, int64_t tokens, cudaStream_t stream
     if (y > heads) y = heads;
     const unsigned gz = (unsigned)((p.chunks + x - 1) / x);
     // Several heads a thread (up to six, the number that wastes least) once that
-    // still fills every SM; one otherwise, for a short call's latency.
+    // still fills every SM: 8,192 tokens 52 us, with one head a thread 61, with four
+    // and a rest of one 60.  One otherwise, for a short call's latency: 64 tokens 2.3
+    // us, with several 2.8.
     const int rows = (heads + y - 1) / y, groups = (rows + 5) / 6, most = (rows + groups - 1) / groups;
     const bool wide = tokens * groups * gz >= 4ll * device_sm_count();
     const int u = wide ? (V == 8 ? most : most > 2 ? 4 : most) : 1;
