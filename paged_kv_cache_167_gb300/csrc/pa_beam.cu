@@ -1,8 +1,8 @@
 // pa_beam.cu -- beam search's selection: the best continuations of a group's
 // beams over the whole vocabulary.
 //
-// score(j, v) = beam_scores[j] + x - log sum exp x.  Two kernels, one pass over
-// the logits:
+// score(j, v) = beam_scores[j] + x - log sum exp x.  Two steps, one pass over the
+// logits; two kernels, or one where a group's CTAs are a cluster:
 //
 // 1. scan: CTA (slice, row) reads an equal share of the row's chunks (1024
 //    vectors of 16 bytes, four for each thread) once, three chunks on their way
@@ -15,9 +15,9 @@
 //    others only if the second best chunk reaches it too) are read again, from
 //    cache, and the elements at or above the bound are ranked.  Keys are (value,
 //    lower index first), so they are unique and ties need no further rule.
-// 2. merge: one CTA per group adds up each row's slices, turns the slices' lists
-//    (each sorted) into fp64 scores and picks the n best by the same bound, taken
-//    over the lists' fronts.
+// 2. merge: one CTA per group (of a cluster, the first) adds up each row's slices,
+//    turns the slices' lists (each sorted) into fp64 scores and picks the n best by
+//    the same bound, taken over the lists' fronts.
 //
 // The exponentials: 2^(x L - c) with L = log2(e) rounded to fp32 and c the running
 // maximum's m L rounded to an integer: one fused multiply-add (x L is not rounded
@@ -34,7 +34,7 @@
 // 56 us (0.69; the 512 CTAs of the scan are three on some SMs and four on others, and
 // the merge takes 5 us).  Below that a chain of latencies: 32 x 4 rows of 128,256
 // bf16 logits 15.6 us (about 5 to stream, 3 for the slice's end, 5 to merge), 4 rows
-// of 32,000 9.9 us.
+// of 32,000 in one cluster 9.1 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -52,6 +52,8 @@ constexpr int kStages = 3;            // chunks in flight or at work
 constexpr int kPart = 33;             // a warp's 32 neighbouring vectors and the one behind them
 constexpr size_t kScanSmem = (size_t)kStages * kWarps * kUnroll * kPart * sizeof(uint4);
 constexpr int kCtasPerSm = 4;
+constexpr int kMaxCluster = 16;
+constexpr int kFewCtas = 76;          // half as many as a GB300 has SMs
 constexpr int kCap = 1024;            // candidates ranked at once
 constexpr float kLog2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
 constexpr float kFar = 4194304.f;                      // 2^22
@@ -270,15 +272,14 @@ struct ScanShared {
 };
 static_assert(sizeof(ScanShared) <= kScanSmem, "the selection reuses the copies' shared memory");
 
+// One slice of a row: its sum, maximum and list.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const BeamParams p) {
+__device__ __forceinline__ void scan_slice(const BeamParams &p) {
+    extern __shared__ __align__(16) unsigned char dyn[];
     using E = Elements<T>;
     constexpr int VN = E::kVec;
-    extern __shared__ __align__(16) unsigned char dyn[];
     uint4 *parts = reinterpret_cast<uint4 *>(dyn);  // [stage][warp][load][kPart] while the slice streams by
     ScanShared &sh = *reinterpret_cast<ScanShared *>(dyn);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.y, n = p.num_out;
     const int64_t entry = (int64_t)row * p.slices + blockIdx.x;
@@ -563,17 +564,15 @@ __device__ __forceinline__ int rank_of(const Candidate *items, int count, const 
 // Threads an item can have so that one round takes all of them.
 __device__ __forceinline__ int share_of(int count) { return count <= 32 ? 8 : count <= 64 ? 4 : count <= 128 ? 2 : 1; }
 
-// Dynamic shared memory: the lists' fronts (their first `depth` candidates)
-// [lists * depth], the candidates to rank [kCap], beams [num_beams], counts and
-// the lists to look further into [lists] each.
-__global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
+// One group's selection out of its rows' lists.  Dynamic shared memory: the lists'
+// fronts (their first `depth` candidates) [lists * depth], the candidates to rank
+// [kCap], beams [num_beams], counts and the lists to look further into [lists] each.
+__device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Candidate best[kThreads];
     __shared__ Candidate bound;
     __shared__ int num_found, num_deep;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, n = p.num_out;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.num_out;
     const int lists = p.num_beams * p.slices, row0 = g * p.num_beams, depth = p.depth, fronts = lists * depth;
     const int64_t entry0 = (int64_t)row0 * p.slices;
     Candidate *front = reinterpret_cast<Candidate *>(dyn);
@@ -746,6 +745,27 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p
     }
 }
 
+// grid (slices, rows).  CLUSTER: a group's CTAs are a cluster, and its first one
+// merges when all have written their records.
+template <typename T, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(const BeamParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    scan_slice<T>(p);
+    if (!CLUSTER) return;
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    const int g = blockIdx.y / p.num_beams;
+    if (blockIdx.x == 0 && (int)blockIdx.y == g * p.num_beams) merge_group(p, g);
+}
+
+// grid (groups): where a group has more CTAs than a cluster.
+__global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    merge_group(p, blockIdx.x);
+}
+
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 int32_t chunks_of(int32_t vocab, int32_t vec) {
@@ -765,8 +785,8 @@ int32_t depth_of(int32_t lists, int32_t n) { return std::min(n, (4 * n + lists -
 
 size_t merge_smem(int32_t beams, int32_t slices, int32_t n) {
     const int lists = beams * slices;
-    return ((size_t)lists * depth_of(lists, n) + kCap) * sizeof(Candidate) + beams * sizeof(Beam) +
-           2 * (size_t)lists * sizeof(int32_t);
+    return ((size_t)lists * depth_of(lists, n) + kCap) * sizeof(Candidate) +
+           beams * sizeof(Beam) + 2 * (size_t)lists * sizeof(int32_t);
 }
 
 }  // namespace
@@ -791,7 +811,17 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     p.num_out = a.num_out;
     p.row_vectors = (int32_t)(((int64_t)a.vocab + vec - 1) / vec);
     p.row_chunks = chunks_of(a.vocab, vec);
-    p.slices = slices_of(rows, p.row_chunks);
+    // No more than 16 slices a group, unless one then had more than 16 chunks: each is
+    // a list to merge (16 x 16 rows of 50,257 fp32 logits 25.5 us, with all the slices
+    // that fit 28; 1 x 64 of 128,256 bf16 39.5 and 53; 1 x 1 of 128,256 9.8 and 9.0).
+    p.slices = std::min(slices_of(rows, p.row_chunks),
+                        std::max(kMaxCluster / a.num_beams, (p.row_chunks + kMaxCluster - 1) / kMaxCluster));
+    // Where few CTAs have all the work, a group's are one cluster and need no second
+    // launch (1 x 4 rows of 32,000 bf16 logits 9.1 us, in two kernels 9.8, and 2 us
+    // less on the host).  Where they are many, clusters pack the SMs worse than single
+    // CTAs do (32 x 4 rows of 128,256 bf16 logits: 19.1 us, in two kernels 15.6; 256 x
+    // 4 of 32,000: 27.4 and 24.7).
+    const bool cluster = a.num_beams * p.slices <= kMaxCluster && rows * p.slices <= kFewCtas;
     const size_t entries = (size_t)rows * p.slices;
     char *w = static_cast<char *>(a.workspace);
     p.sums = reinterpret_cast<unsigned long long *>(w);
@@ -809,15 +839,36 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     p.err = device_error_word();
     if (!p.err) return cudaErrorUnknown;
     p.depth = depth_of(a.num_beams * p.slices, a.num_out);
-    const dim3 grid(p.slices, (unsigned)rows);
-    const auto scan = a.bf16 ? beam_scan_kernel<uint16_t> : beam_scan_kernel<float>;
+    const auto scan = a.bf16 ? (cluster ? beam_scan_kernel<uint16_t, true> : beam_scan_kernel<uint16_t, false>)
+                             : (cluster ? beam_scan_kernel<float, true> : beam_scan_kernel<float, false>);
+    const size_t smem = merge_smem(a.num_beams, p.slices, a.num_out);   // (at most 39 KB)
     // more than the 48 KB a kernel may take unasked: a setting of the loaded kernel
     cudaError_t e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScanSmem);
-    if (e == cudaSuccess) e = launch_pdl(scan, grid, dim3(kThreads), stream, kScanSmem, p);
     if (e != cudaSuccess) return e;
-    // (at most 39 KB: 640 lists, 256 front entries beyond them)
-    const size_t smem = merge_smem(a.num_beams, p.slices, a.num_out);
-    return launch_pdl(beam_merge_kernel, dim3(a.num_groups), dim3(kThreads), stream, smem, p);
+    if (!cluster) {
+        e = launch_pdl(scan, dim3(p.slices, (unsigned)rows), dim3(kThreads), stream, kScanSmem, p);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(beam_merge_kernel, dim3(a.num_groups), dim3(kThreads), stream, smem, p);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.slices, (unsigned)rows);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kScanSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.slices;
+    attr[1].val.clusterDim.y = a.num_beams;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (a.num_beams * p.slices > 8) {                      // an opt-in
+        e = cudaFuncSetAttribute(scan, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, scan, p);
 }
 
 }  // namespace pa

@@ -540,6 +540,29 @@ def test_beam_select_extreme_values(pa, dtype):
     assert pa.get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("J,V,n", [(3, 20001, 12), (4, 32000, 8), (16, 5000, 64), (1, 70000, 1), (5, 4096, 33),
+                                   (20, 70001, 24)])
+def test_beam_select_few_groups_and_many(pa, J, V, n, dtype):
+    """Few groups take one launch and many take two, with other slices: both are
+    right, on rows of all kinds, and a group's place among the others is nothing
+    to it."""
+    x, s = _random_beams(4, J, V, seed=V, dtype=dtype)
+    done = torch.zeros((4, J), dtype=torch.bool, device="cuda")
+    x[1] = x[1].masked_fill(torch.arange(V, device="cuda") % 11 != 0, -math.inf)
+    x[2, 0] = torch.finfo(dtype).min
+    done[2, J - 1] = J > 1
+    x[3, :, V // 2:] = x[3, :, :1]
+    few = _select(pa, x, s, n, done, V - 1)
+    _check_selection(few, x, s, n, done, V - 1, f"few {J}x{V}")
+    many = _select(pa, x.repeat(30, 1, 1), s.repeat(30, 1), n, done.repeat(30, 1), V - 1)
+    for a in many:
+        assert torch.equal(a.view(30, 4, n), a.view(30, 4, n)[:1].expand(30, 4, n))
+    _check_selection(tuple(a[:4] for a in many), x, s, n, done, V - 1, f"many {J}x{V}")
+    assert torch.equal(few[1], many[1][:4]) and torch.equal(few[2], many[2][:4])
+    assert pa.get_device_error() == 0
+
+
 def test_beam_select_equal_rows_at_any_alignment(pa):
     """Twin beams have equal sums, and so equal scores, wherever their rows
     begin: their candidates alternate, the lower beam first."""
