@@ -24,12 +24,12 @@
 //
 // What bounds it: every moved row is read and written once, so DRAM where there are
 // enough units.  GB300, of the measured copy bandwidth: 64 x 3,000 tokens, half of
-// them kept, 91 us (0.85), the keys turned, each by its own distance, 114 us (0.68:
+// them kept, 89 us (0.86), the keys turned, each by its own distance, 113 us (0.68:
 // 64 registers a thread for four CTAs an SM, and the angles); a window over 8 x 8,192
-// tokens, all keys turned by one distance, 50 us (0.79); 131,072 tokens of one
-// sequence in place 105 us (0.75: 256 CTAs, a step of all of them takes 1.6 us), out
-// of place 93 us (0.85); 64 sequences with one to six accepted rows each 3.1 us, a
-// chain of four dependent loads behind a launch.
+// tokens, all keys turned by one distance, 49 us (0.81); 131,072 tokens of one
+// sequence in place 104 us (0.76: 256 CTAs, a step of all of them takes 1.6 us), out
+// of place 91 us (0.87); 64 sequences with one to six accepted rows each 2.9 us, a
+// chain of three dependent loads behind a launch.
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -42,9 +42,8 @@ constexpr int kLoads = 4;                                  // 16-byte copies a t
 constexpr int kMaxRows = 96;
 
 // What is done to the components of a key: nothing, all of them turned, or some of
-// them.  A kernel each, since registers decide how many CTAs an SM holds: with one
-// for all, 131,072 tokens that do not turn took 112 us instead of 105, and a window
-// 52 instead of 50.
+// them.  A kernel each, since registers decide how many CTAs an SM holds: 131,072
+// tokens that do not turn went from 112 to 105 us, and a window from 52 to 50.
 enum { kAsTheyAre = 0, kWhole = 1, kParts = 2 };
 
 struct CompactParams {
@@ -98,7 +97,7 @@ __device__ __forceinline__ void cluster_sync() {
 // What is being found out about one row, one step of the chain after another.
 struct RowLookup {
     int32_t from = 0, before = 0;      // keep[i] and keep[i - 1]
-    int32_t to = 0;                    // start + i
+    int32_t to = 0;                    // i, then start + i
     int32_t src_block = 0, dst_block = 0;
     int32_t own_block = -1;            // out of place: what src_tables has where dst_block is
     bool row = false;                  // false: no such row, or a bad one
@@ -127,6 +126,30 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
     asm volatile("griddepcontrol.launch_dependents;");
     const int kv = blockIdx.y & 1, h = (blockIdx.y >> 1) * p.heads, s = blockIdx.z, tid = threadIdx.x;
     const int64_t cap = (int64_t)p.max_blocks * p.block_size;
+    const int32_t *keep = p.keep + (int64_t)s * p.max_keep;
+    const bool looks = tid < p.rows;
+
+    // The chain behind a row's place: keep -> table entries -> offsets, one call
+    // (and one step of the loop below) each, so that no call uses what it has just
+    // asked for.  Threads 0 .. rows - 1 take a row.  The first tiles' positions are
+    // asked for together with the lengths (any of max_keep may be read), each kind of
+    // load for all of them at once: 1.0 to 1.8 us less a call than one tile after the
+    // other behind the lengths.
+    uint32_t next_row = blockIdx.x * p.rows + tid;         // of the next look_keep (past 2^31 by a few tiles at most)
+    auto look_keep = [&]() {
+        RowLookup r;
+        const uint32_t i = next_row;
+        next_row += gridDim.x * p.rows;
+        r.row = looks && i < (uint32_t)p.max_keep;
+        if (!r.row) return r;
+        r.before = i > 0 ? __ldg(keep + i - 1) : -1;
+        r.from = __ldg(keep + i);
+        r.to = (int32_t)i;
+        return r;
+    };
+    RowLookup first[STAGES + 2];
+#pragma unroll
+    for (int k = 0; k < STAGES + 2; ++k) first[k] = look_keep();
     const int32_t len = __ldg(p.seq_lens + s), n = __ldg(p.keep_lens + s);
     const int32_t start = p.starts ? __ldg(p.starts + s) : 0;
     const bool reports = h == 0 && kv == 0;
@@ -134,34 +157,18 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
         if (tid == 0 && reports && blockIdx.x == 0) raise_error(p.err, PA_DEVERR_SEQ_LEN);
         return;                                            // (a whole cluster does, before any count)
     }
-    const int32_t *keep = p.keep + (int64_t)s * p.max_keep;
     const int32_t *src_table = p.src_tables + (int64_t)s * p.max_blocks;
     const int32_t *dst_table = p.dst_tables + (int64_t)s * p.max_blocks;
     const int64_t base = kv * p.kv_stride + (int64_t)h * p.block_size * p.d;
     const bool turn = TURNS != kAsTheyAre && kv == 0;
     const int32_t tiles = (int32_t)(((uint32_t)n + p.rows - 1) / p.rows);
     const int32_t steps = (tiles - (CLUSTER ? 0 : (int)blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
-    const bool looks = tid < p.rows;
-
-    // The chain behind a row's place: keep -> table entries -> offsets, one call
-    // (and one step of the loop below) each, so that no call uses what it has just
-    // asked for.  Threads 0 .. rows - 1 take a row.
-    uint32_t next_row = blockIdx.x * p.rows + tid;         // of the next look_keep (past 2^31 by a few tiles at most)
-    auto look_keep = [&]() {
-        RowLookup r;
-        const uint32_t i = next_row;
-        next_row += gridDim.x * p.rows;
-        if (!looks || i >= (uint32_t)n) return r;
-        r.before = i > 0 ? __ldg(keep + i - 1) : -1;
-        r.from = __ldg(keep + i);
-        r.to = (int32_t)min((uint32_t)start + i, (uint32_t)INT32_MAX);   // (beyond every length: refused)
-        r.row = true;
-        return r;
-    };
     auto block_of = [&](int32_t t) {
         return p.block_log >= 0 ? (uint32_t)t >> p.block_log : (uint32_t)t / (uint32_t)p.block_size;
     };
     auto look_blocks = [&](RowLookup r) {
+        r.row = r.row && r.to < n;
+        r.to = (int32_t)min((uint32_t)start + (uint32_t)r.to, (uint32_t)INT32_MAX);   // (beyond every length: refused)
         if (r.row && (r.from <= r.before || r.from < r.to || r.from >= len)) {
             if (reports) raise_error(p.err, PA_DEVERR_KEEP);
             r.row = false;
@@ -230,14 +237,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 &&
     if (row0 >= apart) row0 = p.rows;                      // (no whole row is left for it)
     float2 cs[V];
     int32_t turned = 0;                                    // the shift that cs belongs to
-    if (turn)
-        for (int i = tid; i < half; i += THREADS) turns[i % V * p.rot_chunks + i / V] = __ldg(p.turns + i);
     const int at0 = INTERLEAVED ? 2 * c * V : c * V;
     const int at1 = INTERLEAVED ? at0 + V : half + at0;
 
 #pragma unroll
-    for (int k = 0; k < STAGES; ++k) put_row(k, look_blocks(look_keep()));
-    RowLookup blocks = look_blocks(look_keep()), kept = look_keep();   // of tiles STAGES and STAGES + 1
+    for (int k = 0; k <= STAGES; ++k) first[k] = look_blocks(first[k]);
+    if (turn)
+        for (int i = tid; i < half; i += THREADS) turns[i % V * p.rot_chunks + i / V] = __ldg(p.turns + i);
+#pragma unroll
+    for (int k = 0; k < STAGES; ++k) put_row(k, first[k]);
+    RowLookup blocks = first[STAGES], kept = first[STAGES + 1];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) begin_copies(k, k, k);
@@ -371,7 +380,7 @@ cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num
     p.heads = 1;
     if (p.max_keep <= 32 && p.max_keep <= kLoads * (32 / row_vecs) && p.rot_chunks <= 32) {
         // a few rows a sequence (accepted drafts): one warp has them in one tile,
-        // and all units are on the SMs at once (64 sequences: 3.1 us, 6.7 with 256
+        // and all units are on the SMs at once (64 sequences: 2.9 us, 6.7 with 256
         // threads)
         p.rows = p.max_keep;
         return launch_compact_as<V, INTERLEAVED, TURNS, 32, 2, false>(p, 1, num_kv_heads, num_seqs, stream);
