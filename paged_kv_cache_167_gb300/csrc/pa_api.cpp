@@ -515,7 +515,7 @@ pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, c
 size_t pa_beam_select_workspace_size(int32_t num_groups, int32_t num_beams, int32_t vocab, int32_t num_out) {
     if (!beam_shape_ok(num_groups, num_beams, vocab, num_out) || num_beams > kMaxBeams || num_out > kMaxBeamOut)
         return 0;
-    return num_groups ? beam_workspace((int64_t)num_groups * num_beams, vocab, num_out) : 0;
+    return num_groups ? beam_workspace(num_groups, num_beams, vocab, num_out) : 0;
 }
 
 pa_status pa_beam_select(float *scores_out, int32_t *parents_out, int32_t *tokens_out, const void *logits,
@@ -530,7 +530,7 @@ pa_status pa_beam_select(float *scores_out, int32_t *parents_out, int32_t *token
     if (num_groups == 0) return PA_OK;
     if (!scores_out || !parents_out || !tokens_out || !logits || !aligned16(logits) || !beam_scores)
         return PA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < beam_workspace((int64_t)num_groups * num_beams, vocab, num_out) ||
+    if (!workspace || workspace_bytes < beam_workspace(num_groups, num_beams, vocab, num_out) ||
         reinterpret_cast<uintptr_t>(workspace) % kWsAlign != 0)
         return PA_ERR_WORKSPACE;
     BeamArgs a;

@@ -31,10 +31,9 @@
 //
 // What bounds it: the logits are read once (plus the candidates' vectors from
 // cache).  GB300, of the measured copy bandwidth: 64 x 8 rows of 128,256 fp32 logits
-// 56 us (0.69; the 512 CTAs of the scan are three on some SMs and four on others, and
-// the merge takes 5 us).  Below that a chain of latencies: 32 x 4 rows of 128,256
-// bf16 logits 15.6 us (about 5 to stream, 3 for the slice's end, 5 to merge), 4 rows
-// of 32,000 in one cluster 9.1 us.
+// 55 us (0.70; the merge takes 5 us, and the SMs' last slices end at different times).
+// Below that a chain of latencies: 32 x 4 rows of 128,256 bf16 logits 14.7 us (about 5
+// to stream, 3 for the slice's end, 4 to merge), 4 rows of 32,000 in one cluster 9.1.
 #include <algorithm>
 #include <type_traits>
 
@@ -54,6 +53,7 @@ constexpr size_t kScanSmem = (size_t)kStages * kWarps * kUnroll * kPart * sizeof
 constexpr int kCtasPerSm = 4;
 constexpr int kMaxCluster = 16;
 constexpr int kFewCtas = 76;          // half as many as a GB300 has SMs
+constexpr int kFewLists = 64, kMaxLists = 640;   // of a group
 constexpr int kCap = 1024;            // candidates ranked at once
 constexpr float kLog2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
 constexpr float kFar = 4194304.f;                      // 2^22
@@ -287,7 +287,7 @@ __device__ __forceinline__ void scan_slice(const BeamParams &p) {
         if (tid == 0) p.counts[entry] = 0;
         return;
     }
-    // (at most 2^19 chunks and 608 slices: the products fit)
+    // (at most 2^19 chunks and 640 slices: the products fit)
     const int32_t first = (int32_t)((uint32_t)p.row_chunks * blockIdx.x / (uint32_t)p.slices);
     const int32_t last = (int32_t)((uint32_t)p.row_chunks * (blockIdx.x + 1) / (uint32_t)p.slices);
     const Row<T> x(static_cast<const T *>(p.logits) + (int64_t)row * p.row_stride, p.vocab);
@@ -772,12 +772,18 @@ int32_t chunks_of(int32_t vocab, int32_t vec) {
     return (int32_t)(((int64_t)vocab + (int64_t)vec * kChunk - 1) / ((int64_t)vec * kChunk));
 }
 
-// Slices of a row: as many as still run side by side, four CTAs on each of the
-// GB300's 152 SMs (the workspace is sized without a device at hand), no slice
-// without a chunk.  (64 x 8 rows of 128,256: with two slices a row, so in
-// two waves, 80 us when one wave took 66; it takes 56 now.)
-int32_t slices_of(int64_t rows, int32_t row_chunks) {
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>(row_chunks, kCtasPerSm * 152 / rows));
+// Slices of a row (the workspace is sized by it, without a device at hand).  Each is
+// a list to merge, and its end costs some 3 us, so where there are rows enough a
+// slice has up to 16 chunks: 64 x 8 rows of 128,256 fp32 logits take 54 us in 2 slices
+// a row, 55 in one and 61 in 8; 32 x 4 of 128,256 bf16 14.7 in one, 15.6 in 4.  Where
+// rows are few a slice has 4 chunks, or a group at least 16 slices, but no more than
+// 64: 1 x 8 rows of 128,256 bf16 logits 11.8 us in 4 slices a row, 15.1 in one; 1 x 1
+// of 32,000 9.2 in 4 and 10.4 in one; 1 x 64 of 128,256 38.7 in one and 53.6 in 8.
+int32_t slices_of(int64_t rows, int32_t beams, int32_t row_chunks) {
+    int32_t slices = (row_chunks + 15) / 16;
+    if (rows < 128)
+        slices = std::max({slices, kMaxCluster / beams, std::min((row_chunks + 3) / 4, kFewLists / beams)});
+    return std::min({slices, std::max(kMaxLists / beams, 1), row_chunks});
 }
 
 // Front entries of each list: together 4 n or more, or the whole lists.
@@ -792,8 +798,9 @@ size_t merge_smem(int32_t beams, int32_t slices, int32_t n) {
 }  // namespace
 
 // For either type: fp32's vectors, the shorter ones, make the more chunks.
-size_t beam_workspace(int64_t rows, int32_t vocab, int32_t num_out) {
-    const size_t entries = (size_t)rows * slices_of(rows, chunks_of(vocab, 4));
+size_t beam_workspace(int32_t groups, int32_t beams, int32_t vocab, int32_t num_out) {
+    const int64_t rows = (int64_t)groups * beams;
+    const size_t entries = (size_t)rows * slices_of(rows, beams, chunks_of(vocab, 4));
     return round_up(entries * 8) + 2 * round_up(entries * 4) + 2 * round_up(entries * num_out * 4);
 }
 
@@ -811,16 +818,12 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     p.num_out = a.num_out;
     p.row_vectors = (int32_t)(((int64_t)a.vocab + vec - 1) / vec);
     p.row_chunks = chunks_of(a.vocab, vec);
-    // No more than 16 slices a group, unless one then had more than 16 chunks: each is
-    // a list to merge (16 x 16 rows of 50,257 fp32 logits 25.5 us, with all the slices
-    // that fit 28; 1 x 64 of 128,256 bf16 39.5 and 53; 1 x 1 of 128,256 9.8 and 9.0).
-    p.slices = std::min(slices_of(rows, p.row_chunks),
-                        std::max(kMaxCluster / a.num_beams, (p.row_chunks + kMaxCluster - 1) / kMaxCluster));
+    p.slices = slices_of(rows, a.num_beams, p.row_chunks);
     // Where few CTAs have all the work, a group's are one cluster and need no second
     // launch (1 x 4 rows of 32,000 bf16 logits 9.1 us, in two kernels 9.8, and 2 us
     // less on the host).  Where they are many, clusters pack the SMs worse than single
-    // CTAs do (32 x 4 rows of 128,256 bf16 logits: 19.1 us, in two kernels 15.6; 256 x
-    // 4 of 32,000: 27.4 and 24.7).
+    // CTAs do (32 x 4 rows of 128,256 bf16 logits in 4 slices: 19.1 us, in two kernels
+    // 15.6; 256 x 4 of 32,000: 27.4 and 24.7).
     const bool cluster = a.num_beams * p.slices <= kMaxCluster && rows * p.slices <= kFewCtas;
     const size_t entries = (size_t)rows * p.slices;
     char *w = static_cast<char *>(a.workspace);
@@ -841,7 +844,7 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     p.depth = depth_of(a.num_beams * p.slices, a.num_out);
     const auto scan = a.bf16 ? (cluster ? beam_scan_kernel<uint16_t, true> : beam_scan_kernel<uint16_t, false>)
                              : (cluster ? beam_scan_kernel<float, true> : beam_scan_kernel<float, false>);
-    const size_t smem = merge_smem(a.num_beams, p.slices, a.num_out);   // (at most 39 KB)
+    const size_t smem = merge_smem(a.num_beams, p.slices, a.num_out);   // (at most 34 KB: 640 lists)
     // more than the 48 KB a kernel may take unasked: a setting of the loaded kernel
     cudaError_t e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScanSmem);
     if (e != cudaSuccess) return e;

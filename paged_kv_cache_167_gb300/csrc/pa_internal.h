@@ -81,7 +81,7 @@ struct BeamArgs {
     int32_t num_groups, num_beams, vocab, num_out;
     void *workspace;           // beam_workspace bytes, 256-byte aligned
 };
-size_t beam_workspace(int64_t rows, int32_t vocab, int32_t num_out);
+size_t beam_workspace(int32_t groups, int32_t beams, int32_t vocab, int32_t num_out);
 cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream);
 
 // ---- decode (pa_decode_*.cu) -----------------------------------------------
