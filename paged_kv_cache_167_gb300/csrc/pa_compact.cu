@@ -107,7 +107,7 @@ struct RowLookup {
 // and write in order, else each goes its own way (one CTA, or out of place).
 // STAGES tiles are in shared memory or on their way there.
 template <int V, bool INTERLEAVED, int TURNS, int THREADS, int STAGES, bool CLUSTER>
-__global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 256 && CLUSTER ? 3 : 4)
+__global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 512 ? 1 : THREADS == 256 && CLUSTER ? 3 : 4)
     compact_kernel(const CompactParams p) {
     using Vec = typename BfVec<V>::type;
     constexpr int kRings = STAGES + 2;                     // tiles whose rows' places are known
@@ -406,11 +406,17 @@ cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num
     int x = 1;
     while (x < 16 && x < tiles && units * x < 2 * sms) x *= 2;
     if (x == 1) return launch_compact_as<V, INTERLEAVED, TURNS, kAlone, 3, false>(p, x, num_kv_heads, num_seqs, stream);
-    // Four stages: of 16 KB for clusters of 16, whose CTAs are few (131,072 tokens,
-    // half of them kept: 105 us; 112 against 133 when tiles of 12 KB were tried; five
-    // stages: 183, since no longer all clusters are on the SMs at once); of 12 KB
-    // otherwise, so that four CTAs fit an SM (a window over 8 x 8,192 tokens: 50 us,
-    // with 16 KB 72).
+    // Four stages.  Of 32 KB for up to six clusters of 16, one CTA on an SM (65,536
+    // tokens of one sequence and two heads, half of them kept: 26 us, with 16 KB 41;
+    // eight such clusters do not always fit at once: 52 against 44).  Of 16 KB for more
+    // clusters of 16 (131,072 tokens, eight heads: 104 us; 112 against 133 when tiles
+    // of 12 KB were tried; a fifth stage: 183, since no longer all clusters are on the
+    // SMs at once).  Of 12 KB otherwise, so that four CTAs fit an SM (a window over
+    // 8 x 8,192 tokens: 49 us, with 16 KB 72).
+    if (x == 16 && units <= 6) {
+        p.rows = std::min({kLoads * (512 / (row_vecs * p.heads)), 256, p.max_keep});
+        return launch_compact_as<V, INTERLEAVED, TURNS, 512, 4, true>(p, x, num_kv_heads, num_seqs, stream);
+    }
     if (x == 16) {
         p.rows = std::min({kLoads * (256 / (row_vecs * p.heads)), kMaxRows, p.max_keep});
         return launch_compact_as<V, INTERLEAVED, TURNS, 256, 4, true>(p, x, num_kv_heads, num_seqs, stream);
