@@ -2,7 +2,7 @@
 // positions, in place or into other blocks, keys re-rotated on the way.
 //
 // A unit is one sequence's K or V rows of one or several kv-heads (several share
-// the rows' places and, for keys, their angles); it is taken in tiles of up to 16 KB.
+// the rows' places and, for keys, their angles); it is taken in tiles of up to 32 KB.
 // A tile is gathered into shared memory by asynchronous 16-byte copies, two tiles
 // (in a cluster three) ahead of the one being written; the positions and table
 // entries that say where its rows lie are fetched further ahead still, so that no
