@@ -622,8 +622,10 @@ pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, c
  * +inf, raises PA_DEVERR_VALUE and counts as such a row.
  * Within a row candidates are ordered by their logits, across rows by scores
  * compared in fp64 and rounded once to fp32.  The exponentials are fp32, summed
- * in fp32 over the elements a warp holds together and exactly beyond; rows of
- * equal logits have equal sums.
+ * in fp32 over the elements a warp holds together and exactly beyond, so a row's
+ * log sum is off by some 3e-8 (at most 2.5e-7 was seen): candidates of different
+ * rows that lie nearer than that may come in either order.  Rows of equal logits
+ * have equal sums.
  *   workspace    device, 256-byte aligned, pa_beam_select_workspace_size bytes;
  *                overwritten (calls that may run at the same time, on two streams
  *                or from two graphs, need one each)

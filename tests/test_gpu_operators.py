@@ -563,6 +563,28 @@ def test_beam_select_few_groups_and_many(pa, J, V, n, dtype):
     assert pa.get_device_error() == 0
 
 
+@pytest.mark.parametrize("G,J,V,n", [(2, 4, 9000, 8), (50, 4, 9000, 8)])
+def test_beam_select_captured_in_either_form(pa, G, J, V, n):
+    """One launch or two, replayed on new logits in the same buffers."""
+    x, s = _random_beams(G, J, V, seed=G, dtype=torch.bfloat16)
+    ws = torch.empty(pa.beam_select_workspace_size(G, J, V, n), dtype=torch.uint8, device="cuda")
+    out = tuple(torch.empty((G, n), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32))
+    pa.beam_select(*out, x, s, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.beam_select(*out, x, s, workspace=ws)
+        pa.beam_select(*out, x, s, workspace=ws)         # the second overtakes nothing of the first
+    for seed in range(3):
+        y, _ = _random_beams(G, J, V, seed=100 + seed, dtype=torch.bfloat16)
+        x.copy_(y)
+        graph.replay()
+        want = _select(pa, y, s, n)
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    _check_selection(out, x, s, n, what=f"replayed {G}x{J}")
+    assert pa.get_device_error() == 0
+
+
 def test_beam_select_equal_rows_at_any_alignment(pa):
     """Twin beams have equal sums, and so equal scores, wherever their rows
     begin: their candidates alternate, the lower beam first."""
