@@ -39,7 +39,9 @@ namespace pa {
 namespace {
 
 constexpr int kLoads = 4;                                  // 16-byte copies a thread has in a tile
-constexpr int kMaxRows = 96;
+constexpr int kMaxHead = 256;                              // components
+// Rows of a tile at most.
+constexpr int max_rows(int threads) { return threads == 32 ? 32 : threads == 512 ? 256 : 96; }
 
 // What is done to the components of a key: nothing, all of them turned, or some of
 // them.  A kernel each, since registers decide how many CTAs an SM holds: 131,072
@@ -341,14 +343,24 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 512 ? 
     if (CLUSTER) cluster_sync();                           // nobody leaves while others may still store here
 }
 
+// Dynamic shared memory of a launch: the tiles, their rows' places, the frequencies.
+constexpr size_t compact_smem(int stages, size_t tile_vecs, size_t rows, size_t turns) {
+    return stages * tile_vecs * sizeof(uint4) + (stages + 2) * rows * (2 * sizeof(int64_t) + sizeof(int32_t)) +
+           turns * sizeof(uint64_t);
+}
+
 template <int V, bool INTERLEAVED, int TURNS, int THREADS, int STAGES, bool CLUSTER>
 cudaError_t launch_compact_as(const CompactParams &p, int x, int32_t num_kv_heads, int32_t num_seqs,
                               cudaStream_t stream) {
     const auto kernel = compact_kernel<V, INTERLEAVED, TURNS, THREADS, STAGES, CLUSTER>;
-    const size_t smem = (size_t)STAGES * p.rows * p.heads * (p.d / 8) * sizeof(uint4) +
-                        (size_t)(STAGES + 2) * p.rows * (2 * sizeof(int64_t) + sizeof(int32_t)) +
-                        (size_t)p.rot_chunks * V * sizeof(uint64_t);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = compact_smem(STAGES, (size_t)p.rows * p.heads * (p.d / 8), p.rows, p.rot_chunks * V);
+    // The limit belongs to the kernel, and other host threads may be about to launch
+    // it: it is the most that any call asks for, so that no call lowers it for another.
+    // (A tile has at most kLoads vectors a thread.)
+    constexpr size_t kLimit = compact_smem(STAGES, kLoads * THREADS, max_rows(THREADS), kMaxHead / 2);
+    static_assert(kLimit <= 227 * 1024, "what a CTA may have");
+    if (smem > kLimit) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLimit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(x, 2 * (num_kv_heads / p.heads), num_seqs);
@@ -392,7 +404,7 @@ cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num
     const int sms = device_sm_count();
     const int64_t pairs = (int64_t)num_kv_heads * num_seqs;
     if (TURNS != kAsTheyAre && num_kv_heads % 2 == 0 && (!ordered || pairs * 16 >= 2 * sms)) p.heads = 2;
-    p.rows = std::min({kLoads * (kAlone / (row_vecs * p.heads)), kMaxRows, p.max_keep});
+    p.rows = std::min({kLoads * (kAlone / (row_vecs * p.heads)), max_rows(kAlone), p.max_keep});
     const int64_t units = 2ll * (num_kv_heads / p.heads) * num_seqs;
     const int64_t tiles = ((int64_t)p.max_keep + p.rows - 1) / p.rows;
     // Then CTAs share a unit, no more than there are tiles: out of place enough to
@@ -414,14 +426,14 @@ cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num
     // SMs at once).  Of 12 KB otherwise, so that four CTAs fit an SM (a window over
     // 8 x 8,192 tokens: 49 us, with 16 KB 72).
     if (x == 16 && units <= 6) {
-        p.rows = std::min({kLoads * (512 / (row_vecs * p.heads)), 256, p.max_keep});
+        p.rows = std::min({kLoads * (512 / (row_vecs * p.heads)), max_rows(512), p.max_keep});
         return launch_compact_as<V, INTERLEAVED, TURNS, 512, 4, true>(p, x, num_kv_heads, num_seqs, stream);
     }
     if (x == 16) {
-        p.rows = std::min({kLoads * (256 / (row_vecs * p.heads)), kMaxRows, p.max_keep});
+        p.rows = std::min({kLoads * (256 / (row_vecs * p.heads)), max_rows(256), p.max_keep});
         return launch_compact_as<V, INTERLEAVED, TURNS, 256, 4, true>(p, x, num_kv_heads, num_seqs, stream);
     }
-    p.rows = std::min({kLoads * (192 / (row_vecs * p.heads)), kMaxRows, p.max_keep});
+    p.rows = std::min({kLoads * (192 / (row_vecs * p.heads)), max_rows(192), p.max_keep});
     return launch_compact_as<V, INTERLEAVED, TURNS, 192, 4, true>(p, x, num_kv_heads, num_seqs, stream);
 }
 
