@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 512 ? 
                     src_rows[slot * p.rows + tid] = -1;
                     return;
                 }
-                src = r.src_block * p.block_stride + base + (r.from - (int)block_of(r.from) * p.block_size) * p.d;
-                dst = r.dst_block * p.block_stride + base + (r.to - (int)block_of(r.to) * p.block_size) * p.d;
+                src = r.src_block * p.block_stride + base + (int64_t)(r.from - (int)block_of(r.from) * p.block_size) * p.d;
+                dst = r.dst_block * p.block_stride + base + (int64_t)(r.to - (int)block_of(r.to) * p.block_size) * p.d;
             }
         }
         const int at = slot * p.rows + tid;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 32 ? 8 : THREADS == 512 ? 
 
     // A tile's vectors are taken `at_once` whole rows at a time; this thread's are one
     // vector of rows my_row, my_row + at_once, ..., my_off elements from the row's place.
-    const int head_stride = p.block_size * p.d;
+    const int head_stride = p.heads > 1 ? p.block_size * p.d : 0;   // (two heads share a unit only where it fits)
     const int at_once = THREADS / row_vecs;
     int my_row = tid / row_vecs, my_off = tid - my_row * row_vecs;
     my_off = my_off / (p.d / 8) * head_stride + my_off % (p.d / 8) * 8;
@@ -399,11 +399,14 @@ cudaError_t launch_compact_v(CompactParams &p, int32_t num_kv_heads, int32_t num
     }
     // Two heads share a unit, and the angles, where keys turn and units are many
     // (in place a cluster of 16 has to be enough to give every SM two CTAs): of
-    // 64 x 3,000 tokens 127 us became 120, of a window 53 became 50.
+    // 64 x 3,000 tokens 127 us became 120, of a window 53 became 50.  (Not where a
+    // head's slab of a block is so large that the way to the next needs 64 bits: that
+    // would cost every kernel registers, and some of them spills.)
     const bool ordered = p.src_tables == p.dst_tables;
     const int sms = device_sm_count();
     const int64_t pairs = (int64_t)num_kv_heads * num_seqs;
-    if (TURNS != kAsTheyAre && num_kv_heads % 2 == 0 && (!ordered || pairs * 16 >= 2 * sms)) p.heads = 2;
+    const bool near = (int64_t)p.block_size * p.d <= 1 << 30;
+    if (TURNS != kAsTheyAre && near && num_kv_heads % 2 == 0 && (!ordered || pairs * 16 >= 2 * sms)) p.heads = 2;
     p.rows = std::min({kLoads * (kAlone / (row_vecs * p.heads)), max_rows(kAlone), p.max_keep});
     const int64_t units = 2ll * (num_kv_heads / p.heads) * num_seqs;
     const int64_t tiles = ((int64_t)p.max_keep + p.rows - 1) / p.rows;

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import operators as ref
 from tests import test_gpu_operators as ops
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +68,47 @@ def test_compaction_from_several_host_threads(pa):
     for (pool, *_rest), want in zip(plans, alone):
         assert torch.equal(pool.view(torch.int16), want.view(torch.int16))
     assert pa.get_device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# far offsets inside a block
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("hkv,rot,fork", [(1, None, False), (1, 128, False), (2, 128, True), (1, 32, True)])
+def test_compaction_in_blocks_of_more_than_2_31_elements(pa, hkv, rot, fork):
+    """Rows either side of 2^31 elements from the beginning of a head's slab in one
+    block: a warp's few, one CTA's and a cluster's."""
+    d, far = 128, 2 ** 24
+    B = far + 1000
+    pool = torch.zeros((2 if fork else 1, 2, hkv, B, d), dtype=torch.bfloat16, device="cuda")
+    before = normal((2, hkv, 2000, d), 3)
+    w, freqs = (ref.angular_frequencies(rot), cuda(pa.rotary_frequencies(rot))) if rot else (None, None)
+    src = cuda(np.zeros((1, 1), np.int32))
+    dst = cuda(np.ones((1, 1), np.int32)) if fork else src
+    rng = np.random.default_rng(4)
+    for count, start in ((6, far - 2), (15, far - 8), (900, far - 500)):
+        pool[0, :, :, far - 1000:] = before
+        keep = start + 1 + ops._scattered(rng, B - start - 1, count)
+        pa.compact_tokens(pool, src, dst, cuda(np.asarray([B], np.int32)), cuda(keep.astype(np.int32)[None]),
+                          cuda(np.asarray([count], np.int32)), starts=cuda(np.asarray([start], np.int32)), freqs=freqs)
+        assert pa.get_device_error() == 0
+        moved = before[:, :, torch.as_tensor(keep - (far - 1000), device="cuda")]
+        got = pool[-1, :, :, start:start + count]
+        assert torch.equal(got[1], moved[1])
+        if rot is None:
+            assert torch.equal(got[0], moved[0])
+        else:
+            rows = f64(moved[0]).transpose(1, 0, 2)
+            want, size = zip(*(ref.rotate(rows[i], start + i - int(keep[i]), w, False) for i in range(count)))
+            ops.check_rotated(got[0].transpose(0, 1), np.stack(want), np.stack(size), f"{count} rows")
+        # nothing else was touched
+        if fork:
+            assert torch.equal(pool[0, :, :, far - 1000:], before)
+        else:
+            at = far - 1000
+            assert torch.equal(pool[0, :, :, at:start], before[:, :, :start - at])
+            assert torch.equal(pool[0, :, :, start + count:], before[:, :, start + count - at:])
+        pool[:, :, :, far - 1000:] = 0
+        for block in pool:
+            for slab in block:
+                assert int(torch.count_nonzero(slab.view(torch.int64).view(-1))) == 0
