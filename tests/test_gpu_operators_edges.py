@@ -1,5 +1,6 @@
 """Rotation, compaction and beam selection where a call could go wrong beside
-others, at far offsets or in the last bits."""
+others, at far offsets or in the last bits, and with checks that an unwritten
+component fails."""
 import ctypes
 import threading
 
@@ -9,11 +10,56 @@ import torch
 
 from oracle import operators as ref
 from tests import test_gpu_operators as ops
+from tests.written import check_written
 
 pytestmark = pytest.mark.gpu
 
 pa = ops.pa
 cuda, normal, f64 = ops.cuda, ops.normal, ops.f64
+
+
+# ---------------------------------------------------------------------------
+# every component is written
+# ---------------------------------------------------------------------------
+
+@pytest.fixture()
+def written(monkeypatch):
+    """The checks of test_gpu_operators.py, with one that NaN fails."""
+    monkeypatch.setattr(ops, "check_rotated", lambda got, want, size, what: check_written(f64(got), want, size, what))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot,heads", [(128, 128, 8), (64, 32, 3), (80, 24, 2), (96, 20, 7), (72, 10, 1),
+                                         (1024, 1024, 1), (1024, 6, 2), (256, 64, 33)])
+def test_rotate_writes_every_component(pa, written, d, rot, heads, interleaved):
+    ops.test_rotate(pa, d, rot, heads, interleaved)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_inverse_and_far_rotations_write_every_component(pa, written, interleaved):
+    ops.test_rotate_inverse_is_the_gradient(pa, interleaved)
+    ops.test_rotate_positions_beyond_32_bits(pa)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("n,hq,hkv,d,b,rot", [(1, 4, 2, 64, 16, 64), (64, 64, 8, 128, 16, 128), (37, 28, 4, 64, 32, 32),
+                                              (130, 8, 1, 128, 8, 48), (9, 3, 3, 80, 5, 20), (5, 0, 2, 128, 64, 128),
+                                              (3, 71, 1, 64, 4, 6), (700, 6, 2, 64, 16, 64)])
+def test_rotate_and_cache_writes_every_component(pa, written, n, hq, hkv, d, b, rot, interleaved):
+    ops._cached(pa, n, hq, hkv, d, b, rot, interleaved, seed=n + d, mscale=1.0 if n % 2 else 0.875)
+
+
+@pytest.mark.parametrize("fork", [False, True])
+@pytest.mark.parametrize("d,b,rot,interleaved", [(128, 16, None, False), (128, 16, 128, False), (64, 32, 32, True),
+                                                 (80, 4, 24, True), (128, 64, 20, False), (256, 16, 10, False),
+                                                 (72, 5, 6, True)])
+def test_compaction_writes_every_component(pa, written, d, b, rot, interleaved, fork):
+    ops.test_compact_subsets(pa, d, b, rot, interleaved, fork)
+
+
+@pytest.mark.parametrize("rot", [None, 64])
+def test_compaction_in_clusters_writes_every_component(pa, written, rot):
+    ops.test_compact_long_in_place(pa, 8, rot)
 
 
 # ---------------------------------------------------------------------------
@@ -100,7 +146,7 @@ def test_compaction_in_blocks_of_more_than_2_31_elements(pa, hkv, rot, fork):
         else:
             rows = f64(moved[0]).transpose(1, 0, 2)
             want, size = zip(*(ref.rotate(rows[i], start + i - int(keep[i]), w, False) for i in range(count)))
-            ops.check_rotated(got[0].transpose(0, 1), np.stack(want), np.stack(size), f"{count} rows")
+            check_written(f64(got[0].transpose(0, 1)), np.stack(want), np.stack(size), f"{count} rows")
         # nothing else was touched
         if fork:
             assert torch.equal(pool[0, :, :, far - 1000:], before)
