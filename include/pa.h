@@ -621,11 +621,15 @@ pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, c
  * j * vocab + v first.  A row with a NaN or +inf logit, or a beam score of NaN or
  * +inf, raises PA_DEVERR_VALUE and counts as such a row.
  * Within a row candidates are ordered by their logits, across rows by scores
- * compared in fp64 and rounded once to fp32.  The exponentials are fp32, summed
- * in fp32 over the elements a warp holds together and exactly beyond, so a row's
- * log sum is off by some 3e-8 (at most 2.5e-7 was seen): candidates of different
- * rows that lie nearer than that may come in either order.  Rows of equal logits
- * have equal sums.
+ * compared in fp64 and rounded once to fp32.  A row's log sum is made of fp32
+ * exponentials: with D the distance of its elements below their maximum, weighted
+ * by probability (at most log(vocab)), it is off by at most 2^-24 (1.25 D + 12.4):
+ * 2^-22 of the hardware's 2^x, 2^-24 (D + 0.4) of its argument, 2^-26 D of log2(e),
+ * 6 * 2^-24 of a thread's additions and 2^-23 of what follows them, whatever the
+ * vocabulary (a row whose maximum is beyond 2^22 in size: 2^-24 (2.25 D + 18)).
+ * (Rows of normal logits were off by 1e-8 around a mean of -5e-8, and by 1.3e-7 at
+ * most.)  Candidates of different rows that lie nearer than their rows'
+ * errors may come in either order.  Rows of equal logits have equal sums.
  *   workspace    device, 256-byte aligned, pa_beam_select_workspace_size bytes;
  *                overwritten (calls that may run at the same time, on two streams
  *                or from two graphs, need one each)

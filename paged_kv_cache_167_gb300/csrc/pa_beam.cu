@@ -24,8 +24,12 @@
 // by itself) and one hardware 2^x.  The sum is then relative to c / L, which fp64
 // holds, so c's rounding biases nothing; L's own (2^-26) acts on the distance to
 // the maximum only; and a rising c scales the sum by a power of two, exactly, with
-// no branch.  Above the warp sums are integers in units of 2^-32.  So equal rows
-// have equal sums wherever they begin.  A slice whose maximum is beyond 2^22 in
+// no branch.  A thread adds the elements of a chunk by halves and the chunks in a
+// compensated sum, so its error does not grow with the row (one running sum a thread
+// was up to 1.9e-6 off in rows of one value, whose roundings all go the same way; this
+// costs 64 x 8 rows 0.5 of 56 us); above the thread sums are integers, in units of
+// 2^-40 in a slice and of 2^-32 between slices.  So equal rows have equal sums
+// wherever they begin.  A slice whose maximum is beyond 2^22 in
 // size, where c would have no fraction left to lose (a row of the type's lowest
 // value, say), is summed again from its differences to that maximum.
 //
@@ -57,6 +61,8 @@ constexpr int kFewLists = 64, kMaxLists = 640;   // of a group
 constexpr int kCap = 1024;            // candidates ranked at once
 constexpr float kLog2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
 constexpr float kFar = 4194304.f;                      // 2^22
+constexpr float kUnit = 1099511627776.f;               // 2^40 (a slice has less than 2^22 elements, each below 2^0.5)
+constexpr unsigned long long kStrange = ~0ull;         // a warp's sum with a NaN or +inf
 
 // fp32 bits in increasing order; both zeros and the subnormals (which the
 // fp32 maximum flushes, and whose scores fp64 cannot tell apart) are one value.
@@ -108,6 +114,9 @@ __device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+__device__ __forceinline__ uint64_t pair_sub(uint64_t a, uint64_t b) {
+    return pair_fma(b, pair(-1.f, -1.f), a);
 }
 
 // The reference c of a maximum, an integer below 2^24; finite for -inf, so that
@@ -268,7 +277,8 @@ struct ScanShared {
     int32_t rich[kThreads];                         // in more than one: the thread
     int num_holders, num_rich, num_found;
     uint64_t bound;
-    float warp_max[kWarps], warp_sum[kWarps];
+    unsigned long long warp_sum[kWarps];            // 2^-40, or kStrange
+    float warp_max[kWarps];
 };
 static_assert(sizeof(ScanShared) <= kScanSmem, "the selection reuses the copies' shared memory");
 
@@ -296,7 +306,7 @@ __device__ __forceinline__ void scan_slice(const BeamParams &p) {
     float m = -INFINITY, second = -INFINITY;        // the largest of the chunks' maxima, and of the others'
     int32_t best = first;
     float c = reference_of(m);
-    uint64_t sum0 = 0, sum1 = 0;                    // pairs
+    uint64_t sum = 0, lost = 0;                     // pairs: the sum, and what it has too much (Kahan's method)
     auto take = [&](const uint4 (&v)[kUnroll], int32_t k) {
         const float top = E::maximum(v);
         second = fmaxf(second, fminf(m, top));
@@ -306,21 +316,30 @@ __device__ __forceinline__ void scan_slice(const BeamParams &p) {
         }
         const float next = fmaxf(c, reference_of(top)), down = fast_exp2(c - next);
         c = next;
-        sum0 = pair_mul(sum0, pair(down, down));
-        sum1 = pair_mul(sum1, pair(down, down));
+        sum = pair_mul(sum, pair(down, down));
+        lost = pair_mul(lost, pair(down, down));
         const uint64_t minus_c = pair(-c, -c), scale = pair(kLog2e, kLog2e);
+        uint64_t of[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             float e[VN];
+            uint64_t t[VN / 2];
             E::unpack(v[u], e);
 #pragma unroll
-            for (int i = 0; i < VN; i += 4) {       // NaN and +inf end up in the sum as NaN or inf
-                const float2 s = unpair(pair_fma(pair(e[i], e[i + 1]), scale, minus_c));
-                const float2 t = unpair(pair_fma(pair(e[i + 2], e[i + 3]), scale, minus_c));
-                sum0 = pair_add(sum0, pair(fast_exp2(s.x), fast_exp2(s.y)));
-                sum1 = pair_add(sum1, pair(fast_exp2(t.x), fast_exp2(t.y)));
+            for (int i = 0; i < VN / 2; ++i) {      // NaN and +inf end up in the sum as NaN or inf
+                const float2 s = unpair(pair_fma(pair(e[2 * i], e[2 * i + 1]), scale, minus_c));
+                t[i] = pair(fast_exp2(s.x), fast_exp2(s.y));
             }
+#pragma unroll
+            for (int i = VN / 4; i > 0; i /= 2)     // by halves: equal elements double exactly
+#pragma unroll
+                for (int k = 0; k < i; ++k) t[k] = pair_add(t[k], t[k + i]);
+            of[u] = t[0];
         }
+        const uint64_t chunk = pair_add(pair_add(of[0], of[1]), pair_add(of[2], of[3]));
+        const uint64_t more = pair_sub(chunk, lost), next_sum = pair_add(sum, more);
+        lost = pair_sub(pair_sub(next_sum, sum), more);
+        sum = next_sum;
     };
     // A thread copies its own vectors and reads its own copies; those of a warp are
     // neighbours, and a row that does not begin on 16 bytes (SKEW) needs the one
@@ -385,8 +404,7 @@ __device__ __forceinline__ void scan_slice(const BeamParams &p) {
         stream(std::false_type());
     else
         stream(std::true_type());
-    const float2 s0 = unpair(sum0), s1 = unpair(sum1);
-    const float sum = (s0.x + s0.y) + (s1.x + s1.y);
+    float2 held = unpair(sum), over = unpair(lost);
     copy_wait<0>();
     __syncthreads();                                // the copies' shared memory is free
 
@@ -414,20 +432,35 @@ __device__ __forceinline__ void scan_slice(const BeamParams &p) {
     const int32_t end = min(last * kChunk, vectors);
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.warp_max[i]);
-    float part = 0.f;
+    float unit = kUnit;
     if (is_far(top)) {
+        held = over = make_float2(0.f, 0.f);
         for (int32_t j = first * kChunk + tid; j < end; j += kThreads) {
             float e[VN];
             E::unpack(x.load(j), e);
 #pragma unroll
-            for (int i = 0; i < VN; ++i) part += fast_exp2((e[i] - top) * kLog2e);
+            for (int i = 0; i < VN; ++i) e[i] = fast_exp2((e[i] - top) * kLog2e);
+#pragma unroll
+            for (int i = VN / 2; i > 0; i /= 2)
+#pragma unroll
+                for (int k = 0; k < i; ++k) e[k] += e[k + i];
+            const float more = e[0] - over.x, next = held.x + more;
+            over.x = (next - held.x) - more;
+            held.x = next;
         }
     } else {
-        part = sum * fast_exp2(c - reference_of(top));
+        unit *= fast_exp2(c - reference_of(top));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == 0) sh.warp_sum[warp] = part;
+    // both halves and what they have too much, exactly: whole and rest, and then integers
+    const float whole_sum = held.x + held.y, second_half = whole_sum - held.x;
+    const float rest = ((held.x - (whole_sum - second_half)) + (held.y - second_half)) - (over.x + over.y);
+    const unsigned long long part = __float2ull_rn(whole_sum * unit) + (unsigned long long)__float2ll_rn(rest * unit);
+    // (32 numbers of 24 bits fit a word)
+    const uint32_t low = __reduce_add_sync(0xffffffffu, (uint32_t)part & 0xffffffu);
+    const uint32_t mid = __reduce_add_sync(0xffffffffu, (uint32_t)(part >> 24) & 0xffffffu);
+    const uint32_t high = __reduce_add_sync(0xffffffffu, (uint32_t)(part >> 48));
+    const bool strange = __any_sync(0xffffffffu, !(fabsf(whole_sum) < INFINITY));
+    if (lane == 0) sh.warp_sum[warp] = strange ? kStrange : low + ((uint64_t)mid << 24) + ((uint64_t)high << 48);
     if (tid < groups) {                             // the n-th largest of the groups' bounds
         const uint64_t mine = sh.keys[tid];
         int above = 0;
@@ -443,10 +476,10 @@ __device__ __forceinline__ void scan_slice(const BeamParams &p) {
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-            bad |= !(fabsf(sh.warp_sum[i]) < INFINITY);
-            total += __float2ull_rn(sh.warp_sum[i] * 4294967296.f);
+            bad |= sh.warp_sum[i] == kStrange;
+            total += sh.warp_sum[i];
         }
-        p.sums[entry] = total;
+        p.sums[entry] = (total + 128) >> 8;
         p.maxima[entry] = bad ? INFINITY : top;
     }
     int found;
@@ -613,12 +646,12 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
             if (maximum == -INFINITY) return;
             if (!far && !is_far(maximum)) {
                 const float down = reference - reference_of(maximum);
-                if (down < 64.f) total += sum >> (int)down;
+                if (down < 64.f) total += (sum + (1ull << (int)down >> 1)) >> (int)down;
             } else {                                // the slice's reference above the row's, in powers of two
                 const float up = !far            ? __fmaf_rn(maximum, kLog2e, -reference)
                                  : is_far(maximum) ? (maximum - top) * kLog2e
                                                    : __fmaf_rn(-top, kLog2e, reference_of(maximum));
-                total += __float2ull_rn((float)sum * fast_exp2(up));
+                total += up == 0.f ? sum : __float2ull_rn((float)sum * fast_exp2(up));
             }
         };
         if (kind == 1 && !bad) {

@@ -2,6 +2,7 @@
 others, at far offsets or in the last bits, and with checks that an unwritten
 component fails."""
 import ctypes
+import math
 import threading
 
 import numpy as np
@@ -158,3 +159,72 @@ def test_compaction_in_blocks_of_more_than_2_31_elements(pa, hkv, rot, fork):
         for block in pool:
             for slab in block:
                 assert int(torch.count_nonzero(slab.view(torch.int64).view(-1))) == 0
+
+
+# ---------------------------------------------------------------------------
+# the error of a row's log sum
+# ---------------------------------------------------------------------------
+
+def _log_sum_bound(mean_distance):
+    """The header's bound of a row's log sum, for rows whose elements lie
+    mean_distance below the maximum, weighted by their probability.  Relative errors
+    of the sum of exponentials: the hardware's 2^x, 2^-22; the argument x log2(e) - c,
+    rounded once, of size at most distance * log2(e) + 1/2: 2^-24 (distance + 0.4) in
+    nats; log2(e) as fp32, 2^-26 distance; a thread's sum, at most four levels of
+    additions of a chunk and a compensated running sum (2 * 2^-24), 6 * 2^-24; the
+    integer units (at most 640 slices, half a unit of 2^-32 each) and the logarithm,
+    2^-23."""
+    return 2.0 ** -24 * (4 + (mean_distance + 0.4) + mean_distance / 4 + 6 + 2)
+
+
+def _log_sum_error(pa, x, lse):
+    """Selects one candidate of each row under a beam score that cancels the log sum
+    nearly, so that fp32 holds the rest: the error of the log sum itself."""
+    best = x.float().amax(-1).double().cpu().numpy()[:, 0]
+    s = torch.as_tensor((lse - best).astype(np.float32), device="cuda")[:, None]
+    scores = ops._select(pa, x, s, 1)[0].double().cpu().numpy()[:, 0]
+    exact = s.double().cpu().numpy()[:, 0] + best - lse
+    # (the score is an fp64 difference of numbers up to |best|, and one fp32 rounding of the rest)
+    return np.abs(scores - exact) - 2.0 ** -24 * np.abs(exact) - 2.0 ** -50 * np.abs(best)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [1, 130])
+@pytest.mark.parametrize("V", [4097, 50257, 128256, 131072, 1000003])
+def test_log_sum_of_equal_logits(pa, V, rows, dtype):
+    """All roundings of a row of one value go the same way."""
+    values = [0.0, 30.625, 6.9375, -11.3125, 0.7109375, 5.5, -0.109375, 100.5]
+    for value in values:
+        x = torch.full((rows, 1, V), value, dtype=dtype, device="cuda")
+        err = _log_sum_error(pa, x, np.full(rows, value + math.log(V)))
+        assert err.max() <= _log_sum_bound(0.0), (value, float(err.max()))
+    assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [50257, 128256])
+def test_log_sum_of_a_peak_and_equal_tails(pa, V, dtype):
+    """One maximum over a tail of one value: an argument rounded alike V times."""
+    for top, below in ((3.0, 11.5), (-20.0, 11.5), (40.25, 9.75), (0.0, 23.0), (7.0, 0.015625)):
+        x = torch.full((2, 1, V), top - below, dtype=torch.float32, device="cuda")
+        x[:, 0, V // 3] = top
+        x = x.to(dtype)
+        tail = float(x[0, 0, 0])
+        weight = (V - 1) * math.exp(tail - top)
+        lse = top + math.log1p(weight)
+        err = _log_sum_error(pa, x, np.full(2, lse))
+        assert err.max() <= _log_sum_bound((top - tail) * weight / (1 + weight)), (top, below, float(err.max()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [6, 140])
+def test_log_sum_of_random_logits(pa, rows, dtype):
+    V = 32003
+    x = (torch.randn((rows, 1, V), generator=torch.Generator().manual_seed(rows)) * 3).to(dtype).cuda()
+    lse, distance = np.zeros(rows), np.zeros(rows)
+    for i in range(rows):
+        y = f64(x[i, 0])
+        p = np.exp(y - y.max())
+        lse[i] = y.max() + math.log(math.fsum(p))
+        distance[i] = ((y.max() - y) * p).sum() / p.sum()
+    assert (_log_sum_error(pa, x, lse) <= _log_sum_bound(distance)).all()
