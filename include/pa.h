@@ -620,8 +620,8 @@ pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, c
  * group has fewer than num_out other candidates, those of -inf fill up, lowest
  * j * vocab + v first.  A row with a NaN or +inf logit, or a beam score of NaN or
  * +inf, raises PA_DEVERR_VALUE and counts as such a row.
- * Within a row candidates are ordered by their logits, across rows by scores
- * compared in fp64 and rounded once to fp32.  A row's log sum is made of fp32
+ * Within a row candidates are ordered by their logits (zeros and subnormal ones
+ * are equal), across rows by scores compared in fp64 and rounded once to fp32.  A row's log sum is made of fp32
  * exponentials: with D the distance of its elements below their maximum, weighted
  * by probability (at most log(vocab)), it is off by at most 2^-24 (1.25 D + 12.4):
  * 2^-22 of the hardware's 2^x, 2^-24 (D + 0.4) of its argument, 2^-26 D of log2(e),

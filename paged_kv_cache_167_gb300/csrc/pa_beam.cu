@@ -538,11 +538,13 @@ __device__ __forceinline__ void scan_slice(const BeamParams &p) {
     if (tid == 0) p.counts[entry] = found < n ? found : n;
 }
 
-// A candidate of a group: fp64 score in increasing integer order, then the flat
-// index, lower first.
+// A candidate of a group: fp64 score in increasing integer order; equal scores by the
+// row, then by the logit (which a score of its size may not hold: 0 and 2^-80), then by
+// the index, as the row's lists are.
 struct Candidate {
     int64_t score;
-    int32_t index;
+    int32_t index;                   // flat: row * vocab + token
+    uint32_t logit;                  // order_of the logit
 };
 __device__ __forceinline__ int64_t order_of(double s) {
     const int64_t b = __double_as_longlong(s);
@@ -551,8 +553,16 @@ __device__ __forceinline__ int64_t order_of(double s) {
 __device__ __forceinline__ double score_of(int64_t o) {
     return __longlong_as_double(o ^ (int64_t)((uint64_t)(o >> 63) >> 1));
 }
-__device__ __forceinline__ bool better(const Candidate &a, const Candidate &b) {
-    return a.score > b.score || (a.score == b.score && a.index < b.index);
+// (Without a branch but for the rare case: 9.7 us at 1 x 4 rows of 32,000, 10.0 with one
+// for each step, and 9.45 without the logit.)
+__device__ __forceinline__ bool better(const Candidate &a, const Candidate &b, int32_t vocab) {
+    const bool equal = a.score == b.score;
+    bool r = a.score > b.score || (equal && a.index < b.index);
+    if (equal && a.logit != b.logit) {
+        const int32_t row_a = a.index / vocab, row_b = b.index / vocab;
+        r = row_a != row_b ? row_a < row_b : a.logit > b.logit;
+    }
+    return r;
 }
 
 // log(t 2^-32) for t > 0.  t = m 2^e with m in [0.707, 1.414]; log m = 2 artanh(z)
@@ -577,6 +587,8 @@ __device__ __forceinline__ double log_units(unsigned long long t) {
     return (e - 32) * 0.693147180559945309417232 + 2.0 * (z + z * (double)series);
 }
 
+constexpr Candidate kNoCandidate = {INT64_MIN, INT32_MAX, 0};
+
 struct Beam {
     double base, offset;             // score(v) = (x - base) + offset
     unsigned long long total;        // the row's sum, 2^-32 units
@@ -587,10 +599,11 @@ struct Beam {
 
 // The number of items in [0, count) better than `mine`, which is item `of`, by
 // the `per` neighbouring threads that share it (a power of two; all get it).
-__device__ __forceinline__ int rank_of(const Candidate *items, int count, const Candidate &mine, int per) {
+__device__ __forceinline__ int rank_of(const Candidate *items, int count, const Candidate &mine, int per,
+                                       int32_t vocab) {
     int rank = 0;
 #pragma unroll 4
-    for (int t = threadIdx.x & (per - 1); t < count; t += per) rank += better(items[t], mine);
+    for (int t = threadIdx.x & (per - 1); t < count; t += per) rank += better(items[t], mine, vocab);
     for (int o = 1; o < per; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     return rank;
 }
@@ -614,8 +627,7 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
     int32_t *counts = reinterpret_cast<int32_t *>(beams + p.num_beams), *deep = counts + lists;
     if (tid == 0) {
         num_found = num_deep = 0;
-        bound.score = INT64_MIN;
-        bound.index = INT32_MAX;
+        bound = kNoCandidate;
     }
     // the fronts, raw, and every list's count: loads that depend on nothing
     for (int e = tid; e < fronts; e += kThreads) {
@@ -682,6 +694,7 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
         Candidate c;
         c.score = order_of(b.kind == 2 ? b.offset : ((double)v - b.base) + b.offset);
         c.index = b.flat + (b.kind == 2 ? p.end_token : token);
+        c.logit = order_of(v);
         return c;
     };
     for (int e = tid; e < fronts; e += kThreads) {
@@ -689,7 +702,7 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
         const Beam &b = beams[j];
         // an ended beam's one candidate is in its first list
         const int count = b.kind == 1 ? counts[l] : b.kind == 2 && l == j * p.slices ? 1 : 0;
-        Candidate c = {INT64_MIN, INT32_MAX};
+        Candidate c = kNoCandidate;
         if (i < count) c = candidate(b, __uint_as_float((uint32_t)front[e].score), front[e].index);
         front[e] = c;
     }
@@ -699,9 +712,9 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
     const Candidate *items = front;
     int num_items = fronts;
     if (fronts > kThreads) {
-        Candidate c = {INT64_MIN, INT32_MAX};
+        Candidate c = kNoCandidate;
         for (int e = tid; e < fronts; e += kThreads)
-            if (better(front[e], c)) c = front[e];
+            if (better(front[e], c, p.vocab)) c = front[e];
         best[tid] = c;
         items = best;
         num_items = kThreads;
@@ -710,7 +723,7 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
     {
         const int per = share_of(num_items), of = tid / per;
         const Candidate mine = items[min(of, num_items - 1)];
-        const int rank = rank_of(items, num_items, mine, per);
+        const int rank = rank_of(items, num_items, mine, per, p.vocab);
         if (of < num_items && rank == n - 1 && mine.score != INT64_MIN) bound = mine;
     }
     __syncthreads();
@@ -720,7 +733,7 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
         // fronts, then what lies behind a front that is all above it.
         const Candidate limit = bound;
         auto take = [&](const Candidate &c) {
-            if (c.score == INT64_MIN || better(limit, c)) return;
+            if (c.score == INT64_MIN || better(limit, c, p.vocab)) return;
             const int at = atomicAdd(&num_found, 1);
             if (at < kCap) found[at] = c;
         };
@@ -728,7 +741,7 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
             const Candidate c = front[e];
             take(c);
             const int l = e / depth;
-            if (e - l * depth == depth - 1 && c.score != INT64_MIN && !better(limit, c) &&
+            if (e - l * depth == depth - 1 && c.score != INT64_MIN && !better(limit, c, p.vocab) &&
                 beams[l / p.slices].kind == 1 && counts[l] > depth)
                 deep[atomicAdd(&num_deep, 1)] = l;
         }
@@ -745,7 +758,7 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
         for (int k = tid; k < kCap; k += kThreads) {       // as in the scan: a higher bound, again
             const Candidate mine = found[k];
             int rank = 0;
-            for (int t = 0; t < kCap; ++t) rank += better(found[t], mine);
+            for (int t = 0; t < kCap; ++t) rank += better(found[t], mine, p.vocab);
             if (rank == n - 1) bound = mine;
         }
         __syncthreads();
@@ -757,7 +770,7 @@ __device__ __forceinline__ void merge_group(const BeamParams &p, int g) {
     for (int k0 = 0; k0 < total; k0 += kThreads / per) {
         const int k = k0 + tid / per;
         const Candidate mine = found[min(k, total - 1)];
-        const int rank = rank_of(found, total, mine, per);
+        const int rank = rank_of(found, total, mine, per, p.vocab);
         if (k >= total || rank >= n || (tid & (per - 1)) != 0) continue;
         const int64_t o = (int64_t)g * n + rank;
         p.scores_out[o] = (float)score_of(mine.score);

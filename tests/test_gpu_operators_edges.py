@@ -228,3 +228,25 @@ def test_log_sum_of_random_logits(pa, rows, dtype):
         lse[i] = y.max() + math.log(math.fsum(p))
         distance[i] = ((y.max() - y) * p).sum() / p.sum()
     assert (_log_sum_error(pa, x, lse) <= _log_sum_bound(distance)).all()
+
+
+# ---------------------------------------------------------------------------
+# logits that fp64 scores cannot tell apart
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("G", [1, 80])
+def test_selection_orders_a_row_by_its_logits(pa, G):
+    """Logits of 0 and of 2^-80 give one fp64 score.  Within a row the larger logit
+    comes first, in a short selection and in a longer one, in one slice and across
+    slices; between rows of equal scores the lower row does."""
+    V = 20001
+    x = torch.full((G, 2, V), -1.0, device="cuda")
+    x[:, :, 5], x[:, :, 6], x[:, :, 19000] = 0.0, 2.0 ** -80, 2.0 ** -70
+    s = torch.full((G, 2), -2.0, device="cuda")
+    for n in range(1, 8):
+        scores, parents, tokens = ops._select(pa, x, s, n)
+        flat = (parents * V + tokens).cpu().numpy()
+        want = [19000, 6, 5, V + 19000, V + 6, V + 5, 0][:n]
+        assert (flat == np.asarray(want)).all(), (n, flat[0])
+        assert bool((scores[:, :6] == scores[:, :1]).all())
+    assert pa.get_device_error() == 0
