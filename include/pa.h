@@ -771,7 +771,10 @@ pa_status pa_bm_reorder(pa_bm *bm, const int32_t *seqs, const int32_t *parents, 
  * *n_pairs_out; the caller runs pa_copy_blocks on them before writing.  What an
  * in-place pa_compact_tokens needs.  PA_ERR_NO_BLOCKS (too few blocks) and
  * PA_ERR_INVALID_ARG (cap too small, first_token < 0) leave the sequence
- * unchanged.
+ * unchanged.  (cap and the blocks needed are counted before any eviction; a block
+ * that an eviction for this call leaves to seq alone stays in its table.)  A source
+ * still has another holder afterwards.  Where that is the prefix cache alone, the
+ * next allocation may evict it: run the copies before it.
  */
 pa_status pa_bm_unshare(pa_bm *bm, int32_t seq, int64_t first_token, int32_t *pairs_out, int32_t cap,
                         int32_t *n_pairs_out);

@@ -114,6 +114,11 @@ struct pa_bm {
         refcount[b] = 1;
         return b;
     }
+    // An unused block of pop_block goes back.
+    void return_block(int32_t b) {
+        refcount[b] = 0;
+        free_stack.push_back(b);
+    }
     void ref_inc(int32_t b) {
         if (evictable(b)) lru.erase({nodes[node_of_block[b]].tick, node_of_block[b]});
         ++refcount[b];
@@ -252,13 +257,17 @@ pa_status pa_bm_append_tokens(pa_bm *bm, int32_t seq, int64_t n, int64_t *slots_
     if (cow) {
         const int32_t src = s.blocks.back();
         const int32_t dst = bm->pop_block();
-        bm->release_block(src);
-        s.blocks.back() = dst;
-        if (cow_pair_out) {
-            cow_pair_out[0] = src;
-            cow_pair_out[1] = dst;
+        if (bm->refcount[src] == 1) {
+            bm->return_block(dst);          // the eviction for dst took the cache's hold of src: it is private
+        } else {
+            bm->release_block(src);
+            s.blocks.back() = dst;
+            if (cow_pair_out) {
+                cow_pair_out[0] = src;
+                cow_pair_out[1] = dst;
+            }
+            if (n_cow_out) *n_cow_out = 1;
         }
-        if (n_cow_out) *n_cow_out = 1;
     }
     for (int64_t i = 0; i < fresh; ++i) s.blocks.push_back(bm->pop_block());
     if (slots_out)
@@ -346,14 +355,18 @@ pa_status pa_bm_unshare(pa_bm *bm, int32_t seq, int64_t first_token, int32_t *pa
     }
     for (size_t i = first; i < s.blocks.size(); ++i)
         if (bm->refcount[s.blocks[i]] > 1) at.push_back(i);
+    for (size_t k = 0; k < at.size(); ++k) pairs_out[2 * k + 1] = bm->pop_block();
     int32_t n = 0;
-    for (size_t i : at) {
-        pairs_out[2 * n] = s.blocks[i];
-        pairs_out[2 * n++ + 1] = bm->pop_block();
-    }
-    for (int32_t k = 0; k < n; ++k) {
-        bm->release_block(pairs_out[2 * k]);
-        s.blocks[at[(size_t)k]] = pairs_out[2 * k + 1];
+    for (size_t k = 0; k < at.size(); ++k) {
+        const int32_t src = s.blocks[at[k]], dst = pairs_out[2 * k + 1];
+        if (bm->refcount[src] == 1) {               // an eviction has made it private meanwhile
+            bm->return_block(dst);
+            continue;
+        }
+        bm->release_block(src);
+        s.blocks[at[k]] = dst;
+        pairs_out[2 * n] = src;
+        pairs_out[2 * n++ + 1] = dst;
     }
     *n_pairs_out = n;
     return PA_OK;
