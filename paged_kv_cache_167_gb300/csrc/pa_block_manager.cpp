@@ -73,11 +73,17 @@ uint64_t fnv_bytes(uint64_t h, uint64_t v, int nbytes) {
 }  // namespace
 
 struct pa_bm {
+    // (tick, entry) of entries no sequence holds.  An entry owns its place in the set
+    // from the beginning and keeps it while it is not in it; free_nodes and
+    // evict_stack have room for every entry.  So taking and releasing blocks, and the
+    // eviction that may need, allocate nothing and cannot fail halfway.
+    using Lru = std::set<std::pair<uint64_t, int32_t>>;
     struct Node {
         PrefixKey key;
         int32_t block = -1;
         uint64_t tick = 0;
         std::vector<int32_t> children;
+        Lru::node_type place;
     };
     struct Seq {
         std::vector<int32_t> blocks;   // device blocks, or host slots while swapped out
@@ -99,7 +105,8 @@ struct pa_bm {
     std::vector<int32_t> free_nodes;
     std::unordered_map<PrefixKey, int32_t, PrefixKeyHash, PrefixKeyEq> index;
     std::vector<int32_t> node_of_block;             // entry caching the block, -1 if none
-    std::set<std::pair<uint64_t, int32_t>> lru;     // (tick, entry) of entries no sequence holds
+    std::vector<int32_t> evict_stack;
+    Lru lru;
     uint64_t clock = 0;
     int64_t hit_tokens = 0, query_tokens = 0;
 
@@ -119,21 +126,42 @@ struct pa_bm {
         refcount[b] = 0;
         free_stack.push_back(b);
     }
+    void lru_add(int32_t n) {
+        nodes[n].place.value() = {nodes[n].tick, n};
+        lru.insert(std::move(nodes[n].place));
+    }
+    void lru_remove(int32_t n) { nodes[n].place = lru.extract({nodes[n].tick, n}); }
     void ref_inc(int32_t b) {
-        if (evictable(b)) lru.erase({nodes[node_of_block[b]].tick, node_of_block[b]});
+        if (evictable(b)) lru_remove(node_of_block[b]);
         ++refcount[b];
     }
     void release_block(int32_t b) {
         if (--refcount[b] == 0)
             free_stack.push_back(b);
         else if (evictable(b))
-            lru.insert({nodes[node_of_block[b]].tick, node_of_block[b]});
+            lru_add(node_of_block[b]);
     }
     void set_tick(int32_t n) {
         const int32_t b = nodes[n].block;
-        if (evictable(b)) lru.erase({nodes[n].tick, n});
+        if (evictable(b)) lru_remove(n);
         nodes[n].tick = ++clock;
-        if (evictable(b)) lru.insert({nodes[n].tick, n});
+        if (evictable(b)) lru_add(n);
+    }
+    // A new entry, with its place in the set and room on the stacks.
+    int32_t new_node() {
+        int32_t n;
+        if (!free_nodes.empty()) {
+            n = free_nodes.back();
+            free_nodes.pop_back();
+        } else {
+            n = (int32_t)nodes.size();
+            nodes.emplace_back();
+            free_nodes.reserve(nodes.capacity());
+            evict_stack.reserve(nodes.capacity());
+        }
+        Lru one{{0, n}};
+        nodes[n].place = one.extract(one.begin());
+        return n;
     }
     // The chain of entries matching tokens[0 .. n) block by block.
     void match(const int32_t *tokens, int64_t n, uint64_t condition, std::vector<int32_t> &chain) const {
@@ -168,14 +196,14 @@ struct pa_bm {
                     break;
                 }
         }
-        std::vector<int32_t> stack{n};
-        while (!stack.empty()) {
-            const int32_t m = stack.back();
-            stack.pop_back();
+        evict_stack.push_back(n);
+        while (!evict_stack.empty()) {
+            const int32_t m = evict_stack.back();
+            evict_stack.pop_back();
             Node &node = nodes[m];
-            for (int32_t c : node.children) stack.push_back(c);
+            for (int32_t c : node.children) evict_stack.push_back(c);
             const int32_t b = node.block;
-            if (evictable(b)) lru.erase({node.tick, m});
+            if (evictable(b)) lru_remove(m);
             node_of_block[b] = -1;
             if (--refcount[b] == 0) {
                 free_stack.push_back(b);
@@ -526,13 +554,7 @@ pa_status pa_bm_cache_seq(pa_bm *bm, int32_t seq, const int32_t *tokens, int64_t
         } else {
             const int32_t blk = s.blocks[(size_t)i];
             if (bm->node_of_block[blk] >= 0) break;       // held under other content: stop here
-            if (!bm->free_nodes.empty()) {
-                n = bm->free_nodes.back();
-                bm->free_nodes.pop_back();
-            } else {
-                n = (int32_t)bm->nodes.size();
-                bm->nodes.emplace_back();
-            }
+            n = bm->new_node();
             pa_bm::Node &node = bm->nodes[n];
             node.key = key;
             node.block = blk;

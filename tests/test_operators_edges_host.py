@@ -1,6 +1,9 @@
 """Host-side edges of the rotary, compaction and beam-selection calls and of the
 block manager calls that go with them (no GPU)."""
 import math
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -78,3 +81,18 @@ def test_append_keeps_a_block_that_eviction_made_private(bm):
     _, cow = m.append_tokens(c, 1)
     assert cow is not None and cow[1] not in before
     assert m.num_free() == 0
+
+
+def test_block_manager_when_memory_runs_out(tmp_path):
+    """Reorder, unshare and truncate with each of their allocations failing in turn."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    from paged_kv_cache_167_gb300 import build
+    exe = tmp_path / "bm_out_of_memory"
+    subprocess.run([cxx, "-std=c++17", "-O1", "-I", build.INCLUDE, "-I",
+                    os.path.join(build._cuda_home(), "include"),
+                    os.path.join(build.ROOT, "tests", "c", "bm_out_of_memory.cpp"),
+                    os.path.join(build.CSRC, "pa_block_manager.cpp"), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout + out.stderr
