@@ -474,9 +474,17 @@ pa_status pa_decode_grouped(void *out, const void *q, const pa_kv_pool *pool, co
  *
  * Frequencies are given to the device as turns[i] = w_i / (2 pi) as a 64-bit
  * fraction of a full turn (2^64 = one turn).  The phase of position t is the
- * product t * turns[i] modulo 2^64: integer wrap-around drops whole turns
- * exactly, so positions of any size and sign keep an angle error of at most
- * |t| * 2^-64 turns, where a product in fp32 would have lost the angle.
+ * product t * turns[i] modulo 2^64: for the fractions given, integer wrap-around
+ * drops whole turns exactly, at positions of any size and sign, where a product
+ * in fp32 would have lost the angle.  What remains:
+ *   - the fractions' own error, times |t|: 2^-64 of a turn, and where
+ *     pa_rotary_frequencies made them its fp64 arithmetic's, R = (16 + 2 ln base) 2^-53
+ *     of the frequency (by parts up to R + s (R + 2^-51) high / (high - low));
+ *   - cosine and sine of that phase, off by less than 2^-19.8 at any position: its
+ *     upper 32 bits (2^-32 of a turn) as fp32, the product with 2 pi (2^-21.3 for the
+ *     two roundings at half a turn), the hardware's functions (2^-20.5).
+ * A component rotated by one call is within 2^-19 (|a| + |b|) mscale of its pair's
+ * rotation by those fractions, before its one rounding to bf16.
  * ------------------------------------------------------------------------- */
 
 /* How pa_rotary_frequencies scales w_i = base^(-2 i / rot_dim) for contexts

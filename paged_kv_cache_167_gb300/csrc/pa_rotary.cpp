@@ -1,9 +1,14 @@
 // pa_rotary.cpp -- host side of the rotary positions: angular frequencies and
 // their scalings, as 64-bit fractions of a turn.
 //
-// A turn count w / (2 pi) is taken modulo 1 and held with 64 fractional bits.
-// The fp64 quotient is off by at most 2^-53 of itself, so position t is off by
-// t * w * 2^-53 radians: 2^-33 at t = 2^20 for the fastest pair.
+// A turn count w / (2 pi) is taken modulo 1 and held with 64 fractional bits (the
+// rest, below 2^-64, is dropped).  In units of 2^-53 of the value the quotient is off
+// by two (its own rounding and that of 2 pi), and w by some 14 + 2 ln(base) more: the
+// power with its rounded exponent, the base's own change and the division by the
+// factor.  So position t is off by t * w * (16 + 2 ln(base)) 2^-53 radians: 2^-28 at
+// t = 2^20 for the fastest pair of base 10,000.  The by-parts mixes add the error of
+// their share g, which is that of L w times high / (high - low), and matters up to s
+// times as much where w / s remains.
 #include <cmath>
 #include <cstdint>
 
