@@ -35,9 +35,9 @@
 //
 // What bounds it: the logits are read once (plus the candidates' vectors from
 // cache).  GB300, of the measured copy bandwidth: 64 x 8 rows of 128,256 fp32 logits
-// 55 us (0.70; the merge takes 5 us, and the SMs' last slices end at different times).
-// Below that a chain of latencies: 32 x 4 rows of 128,256 bf16 logits 14.7 us (about 5
-// to stream, 3 for the slice's end, 4 to merge), 4 rows of 32,000 in one cluster 9.1.
+// 55.6 us (0.70; the merge takes 5 us, and the SMs' last slices end at different times).
+// Below that a chain of latencies: 32 x 4 rows of 128,256 bf16 logits 15.3 us (about 5
+// to stream, 3 for the slice's end, 4 to merge), 4 rows of 32,000 in one cluster 9.7.
 #include <algorithm>
 #include <type_traits>
 
@@ -56,7 +56,7 @@ constexpr int kPart = 33;             // a warp's 32 neighbouring vectors and th
 constexpr size_t kScanSmem = (size_t)kStages * kWarps * kUnroll * kPart * sizeof(uint4);
 constexpr int kCtasPerSm = 4;
 constexpr int kMaxCluster = 16;
-constexpr int kFewCtas = 76;          // half as many as a GB300 has SMs
+constexpr int kHalfTheSms = 76;       // of a GB300
 constexpr int kFewLists = 64, kMaxLists = 640;   // of a group
 constexpr int kCap = 1024;            // candidates ranked at once
 constexpr float kLog2e = 1.44269502162933349609375f;   // log2(e) rounded to fp32
@@ -819,15 +819,18 @@ int32_t chunks_of(int32_t vocab, int32_t vec) {
 }
 
 // Slices of a row (the workspace is sized by it, without a device at hand).  Each is
-// a list to merge, and its end costs some 3 us, so where there are rows enough a
-// slice has up to 16 chunks: 64 x 8 rows of 128,256 fp32 logits take 54 us in 2 slices
-// a row, 55 in one and 61 in 8; 32 x 4 of 128,256 bf16 14.7 in one, 15.6 in 4.  Where
-// rows are few a slice has 4 chunks, or a group at least 16 slices, but no more than
-// 64: 1 x 8 rows of 128,256 bf16 logits 11.8 us in 4 slices a row, 15.1 in one; 1 x 1
-// of 32,000 9.2 in 4 and 10.4 in one; 1 x 64 of 128,256 38.7 in one and 53.6 in 8.
+// a list to merge, and its end costs some 3 us, so where rows give half the SMs a CTA
+// each a slice has up to 16 chunks (64 x 8 rows of 128,256 fp32 logits in 2 slices a row
+// 55.6 us, in one 56.8, in 8 67.6); below that 4, or a group at least 16 slices (1 x 1
+// row of 32,000 bf16 in 4 slices 9.0 us, in one 10.6), but no more than 64 (1 x 64 rows
+// of 128,256 fp32 in 2 slices each 21.3 us, in 8 29.3).  Either side of the border,
+// 128,256 bf16 logits, 4 chunks against 16, us: 8 x 4 rows 11.6 and 14.5, 18 x 4 13.5
+// and 14.9, 72 x 1 16.7 and 14.7, 9 x 8 15.7 and 16.2; 20 x 4 14.7 and 15.0, 10 x 8 17.1
+// and 16.1, 24 x 4 15.0 and 15.1, 100 x 1 20.6 and 15.3, 127 x 1 25.1 and 15.9, 32 x 4
+// 16.6 and 15.5, 64 x 4 25.8 and 21.7.
 int32_t slices_of(int64_t rows, int32_t beams, int32_t row_chunks) {
     int32_t slices = (row_chunks + 15) / 16;
-    if (rows < 128)
+    if (rows < kHalfTheSms)
         slices = std::max({slices, kMaxCluster / beams, std::min((row_chunks + 3) / 4, kFewLists / beams)});
     return std::min({slices, std::max(kMaxLists / beams, 1), row_chunks});
 }
@@ -866,11 +869,13 @@ cudaError_t launch_beam_select(const BeamArgs &a, cudaStream_t stream) {
     p.row_chunks = chunks_of(a.vocab, vec);
     p.slices = slices_of(rows, a.num_beams, p.row_chunks);
     // Where few CTAs have all the work, a group's are one cluster and need no second
-    // launch (1 x 4 rows of 32,000 bf16 logits 9.1 us, in two kernels 9.8, and 2 us
+    // launch (1 x 4 rows of 32,000 bf16 logits 9.7 us, in two kernels 10.1, and 2 us
     // less on the host).  Where they are many, clusters pack the SMs worse than single
-    // CTAs do (32 x 4 rows of 128,256 bf16 logits in 4 slices: 19.1 us, in two kernels
-    // 15.6; 256 x 4 of 32,000: 27.4 and 24.7).
-    const bool cluster = a.num_beams * p.slices <= kMaxCluster && rows * p.slices <= kFewCtas;
+    // CTAs do: with several slices a row much (31 x 4 rows of 128,256 bf16 logits in 4
+    // slices 19.6 us, in two kernels 16.2), with one it depends (as clusters and in two
+    // kernels: 32 x 4 rows 15.6 and 15.5 us, 36 x 4 17.1 and 16.5, 64 x 4 21.3 and 21.8,
+    // 16 x 8 19.9 and 16.8).
+    const bool cluster = a.num_beams * p.slices <= kMaxCluster && rows * p.slices <= kHalfTheSms;
     const size_t entries = (size_t)rows * p.slices;
     char *w = static_cast<char *>(a.workspace);
     p.sums = reinterpret_cast<unsigned long long *>(w);
