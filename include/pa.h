@@ -60,6 +60,7 @@ typedef enum {
 #define PA_DEVERR_ORDER   0x10u /* a group order entry outside [0, num_groups)              */
 #define PA_DEVERR_KEEP    0x20u /* a kept position that is not ascending or out of range     */
 #define PA_DEVERR_VALUE   0x40u /* a NaN or +inf among logits or beam scores                  */
+#define PA_DEVERR_NO_ROOM 0x80u /* pa_extend_tables: free blocks or token places used up      */
 
 typedef enum {
     PA_DTYPE_BF16 = 0,
@@ -464,6 +465,54 @@ pa_status pa_decode_grouped(void *out, const void *q, const pa_kv_pool *pool, co
                             int32_t max_suffix_len, float scale, const void *new_k, const void *new_v,
                             uint32_t flags, cudaStream_t stream);
 
+/*
+ * A step's tables, positions and slots on the GPU: what pa_bm_append_tokens and
+ * pa_slot_mapping do on the host, for steps whose lengths the host does not know yet
+ * (several steps captured in one graph, accepted drafts).  [P1] "A strong answer":
+ * blocks are allocated on demand as a sequence grows; [P3] "A block table maps
+ * logical order to physical storage".  Sequence s has ctx_lens[s] cached tokens and
+ * new_lens[s] new ones; the blocks it lacks, ceil((ctx + new) / b) - ceil(ctx / b), are
+ * taken from the list of free blocks in the sequences' order, one behind the other:
+ * s's first at free_blocks[*cursor + those of the sequences before it].
+ *   block_tables   device, [num_seqs][max_blocks_per_seq] int32: the entries of the
+ *                  blocks taken are written, the others read or left alone
+ *   seq_lens_out   device, [num_seqs] int32: ctx + new (ctx if s is not served)
+ *   cu_seqlens     device, [num_seqs + 1] int32: where each sequence's new tokens
+ *                  begin in the flat arrays, and where the last ones end (all at most
+ *                  max_tokens)
+ *   positions      device, [max_tokens] int64: ctx_lens[s] + j for new token j of s,
+ *                  plus position_offsets[s]; 0 behind the step's tokens
+ *   slot_mapping   device, [max_tokens] int64: the tokens' slots; -1 (padding, which
+ *                  the slot writers skip) behind the step's tokens and for sequences
+ *                  that are not served
+ *   max_tokens     what the flat arrays hold; a fixed number lets a graph be replayed
+ *   ctx_lens, new_lens  device, [num_seqs] int32, each sequence's sum at most
+ *                  max_blocks_per_seq * block_size: else PA_DEVERR_SEQ_LEN, and the
+ *                  sequence counts as one without new tokens
+ *   position_offsets  device, [num_seqs] int32 or NULL for zeros (positions of several
+ *                  axes run behind a prompt's images at their own distance)
+ *   free_blocks    device, [num_free] int32: free block ids, each once
+ *   cursor         device, one int32 in [0, num_free]: how many of them earlier steps
+ *                  took; cursor_out: device, one int32: the same after this step
+ *   block_size     b >= 1; num_blocks: valid ids are [0, num_blocks), at most 2^31 - 1
+ * Sequences are served in order while the free blocks and the token places last: a
+ * sequence whose blocks or places pass the end is not served, raises
+ * PA_DEVERR_NO_ROOM, and takes nothing (later ones that want no block still are, if
+ * their tokens have places).  A bad cursor counts as a list used up, a bad id raises
+ * PA_DEVERR_BLOCK_ID (its tokens' slots, and its entry, are -1).
+ * The partly filled last block of a sequence must be its own (a fork's is copied
+ * before: pa_copy_blocks).  A block manager and a free list share a pool by halves:
+ * the manager over the first blocks, the list of the others.
+ * The inputs must not overlap what is written (PA_ERR_INVALID_ARG): a loop of steps
+ * copies seq_lens_out and cursor_out back, or takes turns with two sets.
+ * num_seqs at most 2^20.  One launch, no workspace.
+ */
+pa_status pa_extend_tables(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *seq_lens_out,
+                           int32_t *cu_seqlens, int64_t *positions, int64_t *slot_mapping, int32_t max_tokens,
+                           const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *position_offsets,
+                           int32_t num_seqs, const int32_t *free_blocks, int32_t num_free, const int32_t *cursor,
+                           int32_t *cursor_out, int32_t block_size, int64_t num_blocks, cudaStream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Rotary positions.  A head's first rot_dim components are rot_dim / 2 pairs;
  * at position t pair i is turned by the angle t * w_i:
@@ -564,6 +613,45 @@ pa_status pa_rotate_and_cache(const pa_kv_pool *pool, void *q_out, const void *q
                               const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                               const int64_t *positions, const int64_t *slot_mapping, int64_t num_tokens,
                               int32_t num_q_heads, const pa_rotary *rotary, cudaStream_t stream);
+
+/*
+ * Positions of several axes: for tokens that lie in time, height and width (images,
+ * video) pair i of a head is turned by the position on axis axis[i].  Text has equal
+ * positions on every axis, which gives what the calls above give.
+ */
+typedef struct {
+    const uint8_t *axis;     /* host memory, [rot_dim / 2]: 0 .. num_axes - 1     */
+    int32_t num_axes;        /* 1 .. 4                                           */
+    int64_t position_stride; /* elements between two axes' positions; 0 = num_tokens */
+} pa_rotary_axes;
+
+/* Host: axis_out[num_pairs] for axes that own sections[a] pairs each (>= 0,
+ * num_pairs together).  PA_AXES_BLOCKS: the sections one behind the other.
+ * PA_AXES_CYCLED: pair i belongs to axis i mod num_axes while i < num_axes *
+ * sections[that axis], every other pair to axis 0, so that each axis has fast and
+ * slow pairs alike.  Frequencies that begin anew in each section are the caller's
+ * own: pa_rotary_turns, or pa_rotary_frequencies of each section, one behind the
+ * other. */
+#define PA_AXES_BLOCKS 0
+#define PA_AXES_CYCLED 1
+pa_status pa_rotary_sections(const int32_t *sections, int32_t num_axes, int32_t order, int32_t num_pairs,
+                             uint8_t *axis_out);
+
+/*
+ * pa_rotate and pa_rotate_and_cache for positions of several axes:
+ *   positions  device, int64: num_axes rows of num_tokens, position_stride apart
+ * Everything else, the bounds on the error among it, as there.  axis is read
+ * before the call returns.  (pa_compact_tokens with a rotary description moves keys
+ * by the same distance on every axis.)
+ */
+pa_status pa_rotate_axes(void *out, const void *x, int64_t x_stride, const int64_t *positions,
+                         int64_t num_tokens, int32_t num_heads, int32_t head_dim, const pa_rotary *rotary,
+                         const pa_rotary_axes *axes, cudaStream_t stream);
+pa_status pa_rotate_and_cache_axes(const pa_kv_pool *pool, void *q_out, const void *q, int64_t q_stride,
+                                   const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                   const int64_t *positions, const int64_t *slot_mapping, int64_t num_tokens,
+                                   int32_t num_q_heads, const pa_rotary *rotary, const pa_rotary_axes *axes,
+                                   cudaStream_t stream);
 
 /*
  * Compaction: the kept tokens of each sequence move to consecutive positions,

@@ -1,6 +1,6 @@
-"""fp64 restatements of the rotary positions, the compaction of cached tokens
-and beam search's selection, for the tests: plain numpy, one token or row at a
-time, sharing no code with the library."""
+"""fp64 restatements of the rotary positions, the compaction of cached tokens,
+beam search's selection, a step's tables and differential attention, for the
+tests: plain numpy, one token or row at a time, sharing no code with the library."""
 from __future__ import annotations
 
 import math
@@ -101,3 +101,75 @@ def best(scores: np.ndarray, n: int):
     flat = scores.ravel()
     order = sorted(range(flat.size), key=lambda f: (-flat[f], f))[:n]
     return flat[order], [f // scores.shape[1] for f in order], [f % scores.shape[1] for f in order]
+
+
+def axis_of_pair(sections, order: str) -> list:
+    """The axis that turns each pair."""
+    if order == "blocks":
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    n = len(sections)
+    return [i % n if i < n * sections[i % n] else 0 for i in range(sum(sections))]
+
+
+def rotate_axes(x: np.ndarray, positions, axis, w, interleaved: bool, mscale: float = 1.0):
+    """One token's rows at one position an axis: each axis's pairs turned alone."""
+    y, size = np.asarray(x, np.float64).copy(), np.zeros_like(x, dtype=np.float64)
+    for a in set(axis):
+        mine = [wi if ax == a else 0.0 for wi, ax in zip(w, axis)]
+        turned, s = rotate(x, int(positions[a]), mine, interleaved, mscale)
+        for i, ax in enumerate(axis):
+            if ax == a:
+                for p in ((2 * i, 2 * i + 1) if interleaved else (i, i + len(w))):
+                    y[..., p], size[..., p] = turned[..., p], s[..., p]
+    return y, size
+
+
+def extend_tables(tables, ctx, new, free, cursor: int, block_size: int, num_blocks: int, max_tokens: int,
+                  offsets=None) -> dict:
+    """A step's tables, positions and slots, one token at a time, and the error
+    bits it raises (tables as after the step; entries written only where taken)."""
+    tables = [list(map(int, row)) for row in tables]
+    width = len(tables[0]) if tables else 0
+    B, b = len(ctx), block_size
+    out = {"tables": tables, "lens": [], "starts": [], "positions": [0] * max_tokens, "slots": [-1] * max_tokens,
+           "errors": 0}
+    left = len(free) - cursor if 0 <= cursor <= len(free) else 0
+    if not 0 <= cursor <= len(free):
+        out["errors"] |= 0x80
+    tok = blk = taken = 0
+    for s in range(B):
+        c, n = int(ctx[s]), int(new[s])
+        if c < 0 or n < 0 or c + n > min(width * b, 2 ** 31 - 1):
+            out["errors"] |= 0x4
+            n = 0
+            have = need = 0
+        else:
+            have = -(-c // b)
+            need = -(-(c + n) // b) - have
+        out["starts"].append(min(tok, max_tokens))
+        served = tok + n <= max_tokens and (need == 0 or blk + need <= left)
+        out["lens"].append(c + n if served else c)
+        if not served:
+            out["errors"] |= 0x80
+        for j in range(n):
+            if tok + j >= max_tokens:
+                break
+            pos = c + j
+            out["positions"][tok + j] = pos + (int(offsets[s]) if offsets is not None else 0)
+            if not served:
+                continue
+            fresh = pos // b >= have
+            block = int(free[cursor + blk + pos // b - have]) if fresh else tables[s][pos // b]
+            if not 0 <= block < num_blocks:
+                out["errors"] |= 0x1
+                block = -1
+            if fresh:
+                tables[s][pos // b] = block
+            out["slots"][tok + j] = block * b + pos % b if block >= 0 else -1
+        if served:
+            taken = max(taken, blk + need) if need else taken
+        tok += n
+        blk += need
+    out["starts"].append(min(tok, max_tokens))
+    out["cursor"] = cursor + taken
+    return out

@@ -24,9 +24,10 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3:
 PA_SWAP_OUT, PA_SWAP_IN = 0, 1
 PA_DECODE_EARLY_METADATA = 0x1
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_SEQ_LEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
-DEVERR_KEEP, DEVERR_VALUE = 0x20, 0x40
+DEVERR_KEEP, DEVERR_VALUE, DEVERR_NO_ROOM = 0x20, 0x40, 0x80
 PA_DTYPE_BF16, PA_DTYPE_F32 = 0, 1
 PA_ROTARY_INTERLEAVED, PA_ROTARY_INVERSE = 0x1, 0x2
+AXES_ORDERS = {"blocks": 0, "cycled": 1}
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3, "parts_index": 4}
 
 # Every function declared in include/pa.h with (restype, argtypes).
@@ -55,6 +56,11 @@ class PaRotary(ctypes.Structure):
                 ("mscale", ctypes.c_float)]
 
 
+class PaRotaryAxes(ctypes.Structure):
+    """``pa_rotary_axes``: which axis's position turns each pair."""
+    _fields_ = [("axis", ctypes.c_void_p), ("num_axes", ctypes.c_int32), ("position_stride", ctypes.c_int64)]
+
+
 class PaKvPool(ctypes.Structure):
     """``pa_kv_pool``: one layer's view of the block pool (strides in elements)."""
     _fields_ = [("base", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("num_kv_heads", ctypes.c_int32),
@@ -64,6 +70,7 @@ class PaKvPool(ctypes.Structure):
 
 _POOL = ctypes.POINTER(PaKvPool)
 _ROTARY = ctypes.POINTER(PaRotary)
+_AXES = ctypes.POINTER(PaRotaryAxes)
 SIGNATURES = {
     "pa_status_string": (ctypes.c_char_p, [_I32]),
     "pa_version": (_I32, []),
@@ -89,6 +96,11 @@ SIGNATURES = {
     "pa_rotary_turns": (_I32, [_P, _I64, _P]),
     "pa_rotate": (_I32, [_P, _P, _I64, _P, _I64, _I32, _I32, _ROTARY, _P]),
     "pa_rotate_and_cache": (_I32, [_POOL, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _ROTARY, _P]),
+    "pa_rotary_sections": (_I32, [_P, _I32, _I32, _I32, _P]),
+    "pa_rotate_axes": (_I32, [_P, _P, _I64, _P, _I64, _I32, _I32, _ROTARY, _AXES, _P]),
+    "pa_rotate_and_cache_axes": (_I32, [_POOL, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I32, _ROTARY, _AXES,
+                                        _P]),
+    "pa_extend_tables": (_I32, [_P, _I32, _P, _P, _P, _P, _I32, _P, _P, _P, _I32, _P, _I32, _P, _P, _I32, _I64, _P]),
     "pa_compact_tokens": (_I32, [_POOL, _P, _P, _I32, _P, _P, _I32, _P, _P, _I32, _ROTARY, _P]),
     "pa_beam_select_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
     "pa_beam_select": (_I32, [_P, _P, _P, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P]),
@@ -553,15 +565,53 @@ def rotary_turns(angular) -> np.ndarray:
     return out
 
 
+def rotary_axes(sections: Sequence[int], order: str = "blocks") -> np.ndarray:
+    """pa_rotary_sections: the axis of each pair (uint8 numpy array, ``axes`` of
+    rotate and rotate_and_cache) for axes that own sections[a] pairs each.  order:
+    "blocks" (one behind the other) or "cycled" (dealt out pair by pair)."""
+    if order not in AXES_ORDERS:
+        raise ValueError(f"order must be one of {sorted(AXES_ORDERS)}")
+    own = np.ascontiguousarray(sections, dtype=np.int32).reshape(-1)
+    out = np.empty(max(int(own.sum()), 1), dtype=np.uint8)
+    _check(lib().pa_rotary_sections(own.ctypes.data_as(_P), len(own), AXES_ORDERS[order], int(own.sum()),
+                                    out.ctypes.data_as(_P)), "pa_rotary_sections")
+    return out
+
+
+def _axes(axes: np.ndarray, positions: torch.Tensor, n: int, freqs: torch.Tensor, device: int):
+    """(description, address of the positions) of int64 [num_axes][tokens]."""
+    if not isinstance(axes, np.ndarray) or axes.dtype != np.uint8 or not axes.flags.c_contiguous:
+        raise TypeError("axes must be a contiguous uint8 numpy array (rotary_axes)")
+    if axes.size != freqs.numel():
+        raise ValueError("axes must name one axis a pair")
+    if positions.dtype is not torch.int64 or positions.get_device() != device:
+        _refuse(positions, torch.int64, "positions", device)
+    if positions.dim() != 2 or positions.shape[1] != n:
+        raise ValueError("positions must be [num_axes][tokens]")
+    s0, s1 = positions.stride()
+    if n > 1 and (s1 != 1 or (positions.shape[0] > 1 and s0 < n)):
+        raise ValueError("each axis's positions must be dense")
+    return PaRotaryAxes(axes.ctypes.data, positions.shape[0], s0 if positions.shape[0] > 1 else 0), \
+        positions.data_ptr()
+
+
 def rotate(out: torch.Tensor, x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
-           interleaved: bool = False, mscale: float = 1.0, inverse: bool = False, stream=None) -> None:
+           interleaved: bool = False, mscale: float = 1.0, inverse: bool = False, stream=None,
+           axes: Optional[np.ndarray] = None) -> None:
     """pa_rotate: x [tokens][heads][d] bf16 (tokens may be strided) turned to
-    ``positions`` (int64) into the dense ``out``, which may be x itself."""
-    if x.dim() != 3 or out.shape != x.shape or positions.numel() != x.shape[0]:
+    ``positions`` (int64) into the dense ``out``, which may be x itself.
+    ``axes`` (rotary_axes): pa_rotate_axes, positions [num_axes][tokens]."""
+    if x.dim() != 3 or out.shape != x.shape or (axes is None and positions.numel() != x.shape[0]):
         raise ValueError("x and out must be [tokens][heads][head_dim] with one position per token")
     dev = torch.cuda.current_device()
     src, stride = _rows(x, "x", dev)
     rot = _rotary(freqs, interleaved, mscale, dev, inverse)
+    if axes is not None:
+        desc, pos = _axes(axes, positions, x.shape[0], freqs, dev)
+        _check(lib().pa_rotate_axes(_at(out, torch.bfloat16, "out", dev), src, stride, pos, x.shape[0], x.shape[1],
+                                    x.shape[2], ctypes.byref(rot), ctypes.byref(desc), _handle(stream, dev)),
+               "pa_rotate_axes")
+        return
     _check(lib().pa_rotate(_at(out, torch.bfloat16, "out", dev), src, stride,
                            _at(positions, torch.int64, "positions", dev), x.shape[0], x.shape[1], x.shape[2],
                            ctypes.byref(rot), _handle(stream, dev)), "pa_rotate")
@@ -570,10 +620,11 @@ def rotate(out: torch.Tensor, x: torch.Tensor, positions: torch.Tensor, freqs: t
 def rotate_and_cache(pool: torch.Tensor, q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: torch.Tensor,
                      v: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor, freqs: torch.Tensor,
                      interleaved: bool = False, mscale: float = 1.0, layer: Optional[int] = None,
-                     stream=None) -> None:
+                     stream=None, axes: Optional[np.ndarray] = None) -> None:
     """pa_rotate_and_cache: q rotated into q_out, k rotated and v stored at their
     slots.  q, k, v: [tokens][heads][d] bf16, tokens may be strided; q_out dense
-    (may be q); q and q_out both None stores keys and values only."""
+    (may be q); q and q_out both None stores keys and values only.  ``axes``
+    (rotary_axes): pa_rotate_and_cache_axes, positions [num_axes][tokens]."""
     desc = pool_desc(pool, layer)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
@@ -581,7 +632,7 @@ def rotate_and_cache(pool: torch.Tensor, q_out: Optional[torch.Tensor], q: Optio
     n = shape[0]
     if len(shape) != 3 or v.shape != shape or shape[1] != desc.num_kv_heads or shape[2] != desc.head_dim:
         raise ValueError("k and v must be [tokens][num_kv_heads][head_dim]")
-    if positions.numel() != n or slot_mapping.numel() != n:
+    if (axes is None and positions.numel() != n) or slot_mapping.numel() != n:
         raise ValueError("positions and slot_mapping must hold one entry per token")
     dev = torch.cuda.current_device()
     if pool.get_device() != dev:
@@ -596,10 +647,47 @@ def rotate_and_cache(pool: torch.Tensor, q_out: Optional[torch.Tensor], q: Optio
         qp, qs = _rows(q, "q", dev)
         qo, hq = _at(q_out, torch.bfloat16, "q_out", dev), shape[1]
     rot = _rotary(freqs, interleaved, mscale, dev)
+    slots = _at(slot_mapping, torch.int64, "slot_mapping", dev)
+    if axes is not None:
+        by_axis, pos = _axes(axes, positions, n, freqs, dev)
+        _check(lib().pa_rotate_and_cache_axes(ctypes.byref(desc), qo, qp, qs, kp, ks, vp, vs, pos, slots, n, hq,
+                                              ctypes.byref(rot), ctypes.byref(by_axis), _handle(stream, dev)),
+               "pa_rotate_and_cache_axes")
+        return
     _check(lib().pa_rotate_and_cache(ctypes.byref(desc), qo, qp, qs, kp, ks, vp, vs,
-                                     _at(positions, torch.int64, "positions", dev),
-                                     _at(slot_mapping, torch.int64, "slot_mapping", dev), n, hq, ctypes.byref(rot),
+                                     _at(positions, torch.int64, "positions", dev), slots, n, hq, ctypes.byref(rot),
                                      _handle(stream, dev)), "pa_rotate_and_cache")
+
+
+def extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens: torch.Tensor,
+                  positions: torch.Tensor, slot_mapping: torch.Tensor, ctx_lens: torch.Tensor,
+                  new_lens: torch.Tensor, free_blocks: torch.Tensor, cursor: torch.Tensor, cursor_out: torch.Tensor,
+                  block_size: int, num_blocks: int, position_offsets: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """pa_extend_tables: tables, positions and slots of a step's new tokens.
+    Written: block_tables [B][W], seq_lens [B], cu_seqlens [B + 1] (int32),
+    positions and slot_mapping [max_tokens] (int64), cursor_out [1] (int32).
+    Read: ctx_lens, new_lens, position_offsets [B], free_blocks and cursor [1]
+    (int32)."""
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs][max_blocks]")
+    B, W = block_tables.shape
+    if seq_lens.numel() != B or ctx_lens.numel() != B or new_lens.numel() != B or cu_seqlens.numel() != B + 1:
+        raise ValueError("seq_lens, ctx_lens, new_lens and cu_seqlens do not match the batch")
+    if position_offsets is not None and position_offsets.numel() != B:
+        raise ValueError("position_offsets must hold one entry per sequence")
+    if positions.numel() != slot_mapping.numel() or cursor.numel() != 1 or cursor_out.numel() != 1:
+        raise ValueError("positions and slot_mapping must be of one size, cursor and cursor_out one number")
+    dev = torch.cuda.current_device()
+    i32, i64 = torch.int32, torch.int64
+    _check(lib().pa_extend_tables(
+        _at(block_tables, i32, "block_tables", dev), W, _at(seq_lens, i32, "seq_lens", dev),
+        _at(cu_seqlens, i32, "cu_seqlens", dev), _at(positions, i64, "positions", dev),
+        _at(slot_mapping, i64, "slot_mapping", dev), slot_mapping.numel(), _at(ctx_lens, i32, "ctx_lens", dev),
+        _at(new_lens, i32, "new_lens", dev),
+        _at(position_offsets, i32, "position_offsets", dev) if position_offsets is not None else None, B,
+        _at(free_blocks, i32, "free_blocks", dev), free_blocks.numel(), _at(cursor, i32, "cursor", dev),
+        _at(cursor_out, i32, "cursor_out", dev), block_size, num_blocks, _handle(stream, dev)), "pa_extend_tables")
 
 
 def compact_tokens(pool: torch.Tensor, src_tables: torch.Tensor, dst_tables: torch.Tensor, seq_lens: torch.Tensor,

@@ -443,6 +443,28 @@ bool token_stride(int64_t *stride, int64_t row) {
     return *stride >= row && *stride % 8 == 0;
 }
 
+// Positions of several axes (null: one axis): the host array checked and packed.
+bool axes_view(const pa_rotary_axes *axes, int32_t rot_dim, int64_t num_tokens, AxesView *out) {
+    if (!axes || !axes->axis || axes->num_axes < 1 || axes->num_axes > kMaxAxes || rot_dim / 2 > kMaxAxisPairs)
+        return false;
+    out->stride = axes->position_stride ? axes->position_stride : num_tokens;
+    if (out->stride < num_tokens) return false;
+    out->num_axes = axes->num_axes;
+    for (uint32_t &word : out->code) word = 0;
+    for (int32_t i = 0; i < rot_dim / 2; ++i) {
+        if (axes->axis[i] >= axes->num_axes) return false;
+        out->code[i / 16] |= (uint32_t)axes->axis[i] << (2 * (i % 16));
+    }
+    return true;
+}
+
+// Do two ranges of bytes share any?  (Empty or null ranges do not.)
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    if (!a || !b || a_bytes <= 0 || b_bytes <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 bool beam_shape_ok(int32_t num_groups, int32_t num_beams, int32_t vocab, int32_t num_out) {
     return num_groups >= 0 && num_beams >= 1 && vocab >= 1 && num_out >= 1 &&
            (int64_t)num_beams * vocab <= (int64_t)INT32_MAX && num_out <= (int64_t)num_beams * vocab &&
@@ -450,30 +472,84 @@ bool beam_shape_ok(int32_t num_groups, int32_t num_beams, int32_t vocab, int32_t
 }
 
 constexpr int32_t kMaxBeams = 64, kMaxBeamOut = 64;
+constexpr int32_t kMaxExtendSeqs = 1 << 20;
 
 }  // namespace
 }  // namespace pa
 
 extern "C" {
 
-pa_status pa_rotate(void *out, const void *x, int64_t x_stride, const int64_t *positions, int64_t num_tokens,
-                    int32_t num_heads, int32_t head_dim, const pa_rotary *rotary, cudaStream_t stream) {
+pa_status pa_extend_tables(int32_t *block_tables, int32_t max_blocks_per_seq, int32_t *seq_lens_out,
+                           int32_t *cu_seqlens, int64_t *positions, int64_t *slot_mapping, int32_t max_tokens,
+                           const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *position_offsets,
+                           int32_t num_seqs, const int32_t *free_blocks, int32_t num_free, const int32_t *cursor,
+                           int32_t *cursor_out, int32_t block_size, int64_t num_blocks, cudaStream_t stream) {
+    if (num_seqs < 0 || num_seqs > kMaxExtendSeqs || max_tokens < 0 || num_free < 0 || max_blocks_per_seq <= 0 ||
+        block_size <= 0 || num_blocks <= 0 || num_blocks > (int64_t)INT32_MAX)
+        return PA_ERR_INVALID_ARG;
+    if (!cu_seqlens || !cursor || !cursor_out) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!block_tables || !seq_lens_out || !ctx_lens || !new_lens)) return PA_ERR_INVALID_ARG;
+    if ((max_tokens > 0 && (!positions || !slot_mapping)) || (num_free > 0 && !free_blocks))
+        return PA_ERR_INVALID_ARG;
+    // what other CTAs still read must not be what one of them writes
+    const struct { const void *p; int64_t bytes; } in[] = {
+        {ctx_lens, 4ll * num_seqs}, {new_lens, 4ll * num_seqs}, {position_offsets, 4ll * num_seqs},
+        {free_blocks, 4ll * num_free}, {cursor, 4}}, out[] = {
+        {block_tables, 4ll * num_seqs * max_blocks_per_seq}, {seq_lens_out, 4ll * num_seqs},
+        {cu_seqlens, 4ll * num_seqs + 4}, {positions, 8ll * max_tokens}, {slot_mapping, 8ll * max_tokens},
+        {cursor_out, 4}};
+    for (const auto &o : out)
+        for (const auto &i : in)
+            if (overlap(o.p, o.bytes, i.p, i.bytes)) return PA_ERR_INVALID_ARG;
+    ExtendArgs a;
+    a.tables = block_tables;
+    a.max_blocks = max_blocks_per_seq;
+    a.seq_lens_out = seq_lens_out;
+    a.cu_seqlens = cu_seqlens;
+    a.positions = positions;
+    a.slots = slot_mapping;
+    a.max_tokens = max_tokens;
+    a.ctx_lens = ctx_lens;
+    a.new_lens = new_lens;
+    a.position_offsets = position_offsets;
+    a.num_seqs = num_seqs;
+    a.free_blocks = free_blocks;
+    a.num_free = num_free;
+    a.cursor = cursor;
+    a.cursor_out = cursor_out;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    return launch_extend_tables(a, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+pa_status rotate_impl(void *out, const void *x, int64_t x_stride, const int64_t *positions, int64_t num_tokens,
+                      int32_t num_heads, int32_t head_dim, const pa_rotary *rotary, const pa_rotary_axes *axes,
+                      bool several, cudaStream_t stream) {
     if (num_tokens < 0 || num_tokens > INT32_MAX || num_heads < 0 || num_heads > 65535 || head_dim <= 0)
         return PA_ERR_INVALID_ARG;
     if (head_dim % 8 != 0 || head_dim > 1024) return PA_ERR_UNSUPPORTED;
     if (!rotary_ok(rotary, head_dim)) return PA_ERR_INVALID_ARG;
     if (!token_stride(&x_stride, (int64_t)num_heads * head_dim)) return PA_ERR_INVALID_ARG;
+    AxesView view;
+    if (several && !axes_view(axes, rotary->rot_dim, num_tokens, &view)) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0 || num_heads == 0) return PA_OK;
     if (!out || !x || !positions || !aligned16(out) || !aligned16(x)) return PA_ERR_INVALID_ARG;
-    return launch_rotate(out, x, x_stride, positions, num_tokens, num_heads, head_dim, *rotary, stream) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    const cudaError_t e = several ? launch_rotate_axes(out, x, x_stride, positions, num_tokens, num_heads, head_dim,
+                                                       *rotary, view, stream)
+                                  : launch_rotate(out, x, x_stride, positions, num_tokens, num_heads, head_dim,
+                                                  *rotary, stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-pa_status pa_rotate_and_cache(const pa_kv_pool *pool, void *q_out, const void *q, int64_t q_stride, const void *k,
-                              int64_t k_stride, const void *v, int64_t v_stride, const int64_t *positions,
-                              const int64_t *slot_mapping, int64_t num_tokens, int32_t num_q_heads,
-                              const pa_rotary *rotary, cudaStream_t stream) {
+pa_status rotate_and_cache_impl(const pa_kv_pool *pool, void *q_out, const void *q, int64_t q_stride, const void *k,
+                                int64_t k_stride, const void *v, int64_t v_stride, const int64_t *positions,
+                                const int64_t *slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                                const pa_rotary *rotary, const pa_rotary_axes *axes, bool several,
+                                cudaStream_t stream) {
     PoolView view;
     pa_status st = resolve_pool(pool, &view);
     if (st != PA_OK) return st;
@@ -484,13 +560,49 @@ pa_status pa_rotate_and_cache(const pa_kv_pool *pool, void *q_out, const void *q
     const int64_t kv_row = (int64_t)view.num_kv_heads * view.head_dim;
     if (!token_stride(&k_stride, kv_row) || !token_stride(&v_stride, kv_row)) return PA_ERR_INVALID_ARG;
     if (num_q_heads > 0 && !token_stride(&q_stride, (int64_t)num_q_heads * view.head_dim)) return PA_ERR_INVALID_ARG;
+    AxesView av;
+    if (several && !axes_view(axes, rotary->rot_dim, num_tokens, &av)) return PA_ERR_INVALID_ARG;
     if (num_tokens == 0) return PA_OK;
     if (!k || !v || !positions || !slot_mapping || !aligned16(k) || !aligned16(v)) return PA_ERR_INVALID_ARG;
     if (num_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out))) return PA_ERR_INVALID_ARG;
-    return launch_rotate_and_cache(view, q_out, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping,
-                                   num_tokens, num_q_heads, *rotary, stream) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    const cudaError_t e =
+        several ? launch_rotate_and_cache_axes(view, q_out, q, q_stride, k, k_stride, v, v_stride, positions,
+                                               slot_mapping, num_tokens, num_q_heads, *rotary, av, stream)
+                : launch_rotate_and_cache(view, q_out, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping,
+                                          num_tokens, num_q_heads, *rotary, stream);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_rotate(void *out, const void *x, int64_t x_stride, const int64_t *positions, int64_t num_tokens,
+                    int32_t num_heads, int32_t head_dim, const pa_rotary *rotary, cudaStream_t stream) {
+    return rotate_impl(out, x, x_stride, positions, num_tokens, num_heads, head_dim, rotary, nullptr, false, stream);
+}
+
+pa_status pa_rotate_axes(void *out, const void *x, int64_t x_stride, const int64_t *positions, int64_t num_tokens,
+                         int32_t num_heads, int32_t head_dim, const pa_rotary *rotary, const pa_rotary_axes *axes,
+                         cudaStream_t stream) {
+    return rotate_impl(out, x, x_stride, positions, num_tokens, num_heads, head_dim, rotary, axes, true, stream);
+}
+
+pa_status pa_rotate_and_cache(const pa_kv_pool *pool, void *q_out, const void *q, int64_t q_stride, const void *k,
+                              int64_t k_stride, const void *v, int64_t v_stride, const int64_t *positions,
+                              const int64_t *slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                              const pa_rotary *rotary, cudaStream_t stream) {
+    return rotate_and_cache_impl(pool, q_out, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping,
+                                 num_tokens, num_q_heads, rotary, nullptr, false, stream);
+}
+
+pa_status pa_rotate_and_cache_axes(const pa_kv_pool *pool, void *q_out, const void *q, int64_t q_stride,
+                                   const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                   const int64_t *positions, const int64_t *slot_mapping, int64_t num_tokens,
+                                   int32_t num_q_heads, const pa_rotary *rotary, const pa_rotary_axes *axes,
+                                   cudaStream_t stream) {
+    return rotate_and_cache_impl(pool, q_out, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping,
+                                 num_tokens, num_q_heads, rotary, axes, true, stream);
 }
 
 pa_status pa_compact_tokens(const pa_kv_pool *pool, const int32_t *src_tables, const int32_t *dst_tables,

@@ -54,13 +54,52 @@ cudaError_t launch_copy_blocks(const PoolView &pool, const int32_t *pairs, int32
 cudaError_t launch_swap_blocks(const PoolView &pool, void *host_dev, int64_t host_blocks, const int32_t *pairs,
                                int32_t num_pairs, int32_t direction, cudaStream_t stream);
 
+// ---- a step's tables, positions and slots (pa_extend.cu) --------------------
+struct ExtendArgs {
+    int32_t *tables;
+    int32_t max_blocks;
+    int32_t *seq_lens_out;
+    int32_t *cu_seqlens;
+    int64_t *positions;
+    int64_t *slots;
+    int32_t max_tokens;
+    const int32_t *ctx_lens;
+    const int32_t *new_lens;
+    const int32_t *position_offsets;   // may be null
+    int32_t num_seqs;
+    const int32_t *free_blocks;
+    int32_t num_free;
+    const int32_t *cursor;
+    int32_t *cursor_out;
+    int32_t block_size;
+    int64_t num_blocks;
+};
+cudaError_t launch_extend_tables(const ExtendArgs &a, cudaStream_t stream);
+
 // ---- rotary positions (pa_rotary.cu); arguments validated, strides resolved --
+// Positions of several axes: two bits a pair name the axis that turns it.
+constexpr int kMaxAxes = 4;
+constexpr int kMaxAxisPairs = 512;     // head_dim up to 1024
+struct AxesView {
+    int64_t stride;                    // elements between two axes' positions
+    int32_t num_axes;
+    uint32_t code[kMaxAxisPairs / 16];
+};
 cudaError_t launch_rotate(void *out, const void *x, int64_t x_stride, const int64_t *positions, int64_t num_tokens,
                           int32_t num_heads, int32_t head_dim, const pa_rotary &rotary, cudaStream_t stream);
 cudaError_t launch_rotate_and_cache(const PoolView &pool, void *q_out, const void *q, int64_t q_stride,
                                     const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                     const int64_t *positions, const int64_t *slots, int64_t num_tokens,
                                     int32_t num_q_heads, const pa_rotary &rotary, cudaStream_t stream);
+// the same with positions of several axes (pa_rotary_axes.cu)
+cudaError_t launch_rotate_axes(void *out, const void *x, int64_t x_stride, const int64_t *positions,
+                               int64_t num_tokens, int32_t num_heads, int32_t head_dim, const pa_rotary &rotary,
+                               const AxesView &axes, cudaStream_t stream);
+cudaError_t launch_rotate_and_cache_axes(const PoolView &pool, void *q_out, const void *q, int64_t q_stride,
+                                         const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                         const int64_t *positions, const int64_t *slots, int64_t num_tokens,
+                                         int32_t num_q_heads, const pa_rotary &rotary, const AxesView &axes,
+                                         cudaStream_t stream);
 
 // ---- compaction of cached tokens (pa_compact.cu) ----------------------------
 cudaError_t launch_compact(const PoolView &pool, const int32_t *src_tables, const int32_t *dst_tables,

@@ -37,6 +37,30 @@ pa_status pa_rotary_turns(const double *angular, int64_t n, uint64_t *turns_out)
     return PA_OK;
 }
 
+pa_status pa_rotary_sections(const int32_t *sections, int32_t num_axes, int32_t order, int32_t num_pairs,
+                             uint8_t *axis_out) {
+    if (!sections || !axis_out || num_axes < 1 || num_axes > 4 || num_pairs < 1) return PA_ERR_INVALID_ARG;
+    if (order != PA_AXES_BLOCKS && order != PA_AXES_CYCLED) return PA_ERR_INVALID_ARG;
+    int64_t sum = 0;
+    for (int32_t a = 0; a < num_axes; ++a) {
+        if (sections[a] < 0) return PA_ERR_INVALID_ARG;
+        sum += sections[a];
+    }
+    if (sum != num_pairs) return PA_ERR_INVALID_ARG;
+    int32_t axis = 0, left = sections[0];
+    for (int32_t i = 0; i < num_pairs; ++i) {
+        if (order == PA_AXES_CYCLED) {
+            axis = i % num_axes;
+            if (i >= (int64_t)num_axes * sections[axis]) axis = 0;
+        } else {
+            while (left == 0) left = sections[++axis];
+            --left;
+        }
+        axis_out[i] = (uint8_t)axis;
+    }
+    return PA_OK;
+}
+
 pa_status pa_rotary_frequencies(const pa_rotary_params *params, uint64_t *turns_out) {
     if (!params || !turns_out) return PA_ERR_INVALID_ARG;
     const pa_rotary_params p = *params;

@@ -1,0 +1,119 @@
+"""Host side of a step's tables, of positions of several axes and of
+differential attention: the axes' layouts and the refusals (no GPU: every call
+here is refused, or has nothing to do, before anything is launched)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import operators as ref
+
+
+@pytest.fixture(scope="module")
+def B():
+    import __graft_entry__
+    __graft_entry__.build()
+    from paged_kv_cache_167_gb300 import binding
+    return binding
+
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+
+
+# ---------------------------------------------------------------------------
+# axes
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("order", ["blocks", "cycled"])
+@pytest.mark.parametrize("sections", [[64], [16, 24, 24], [24, 20, 20], [32, 32], [2, 0, 6], [0, 0, 8], [1, 1, 1, 1],
+                                      [0, 8], [8, 0], [5, 11, 1, 7], [1], [3, 29]])
+def test_axes_of_pairs(B, sections, order):
+    assert B.rotary_axes(sections, order).tolist() == ref.axis_of_pair(sections, order)
+
+
+@pytest.mark.parametrize("sections", [[], [-1, 5], [0], [0, 0], [1, 1, 1, 1, 1]])
+def test_axes_refusals(B, sections):
+    with pytest.raises(B.PagedAttentionError) as e:
+        B.rotary_axes(sections)
+    assert e.value.status == INVALID
+
+
+def test_axes_more_refusals(B):
+    with pytest.raises(ValueError):
+        B.rotary_axes([4, 4], order="striped")
+    own, out = (ctypes.c_int32 * 2)(4, 4), (ctypes.c_uint8 * 8)()
+    f = B.lib().pa_rotary_sections
+    assert f(own, 2, 0, 8, out) == 0 and list(out) == [0] * 4 + [1] * 4
+    assert f(own, 2, 2, 8, out) == INVALID and f(own, 2, 0, 9, out) == INVALID
+    assert f(None, 2, 0, 8, out) == INVALID and f(own, 2, 0, 8, None) == INVALID
+
+
+FAKE = 1 << 20      # an aligned address that no refused call reads
+
+
+def _rotate_axes(B, axis=(0, 1, 2, 0), num_axes=3, stride=0, tokens=4, **kw):
+    axis = (ctypes.c_uint8 * len(axis))(*axis)
+    axes = B.PaRotaryAxes(ctypes.addressof(axis), num_axes, stride)
+    rot = B.PaRotary(FAKE, 8, kw.get("flags", 0), 1.0)
+    return B.lib().pa_rotate_axes(FAKE, FAKE, 0, kw.get("positions", FAKE), tokens, 2, kw.get("d", 16),
+                                  ctypes.byref(rot), kw.get("axes", ctypes.byref(axes)), None)
+
+
+def test_rotate_axes_refusals(B):
+    assert _rotate_axes(B, tokens=0) == 0
+    assert _rotate_axes(B, axis=(0, 1, 3, 0)) == INVALID            # an axis that is not there
+    assert _rotate_axes(B, num_axes=0) == INVALID and _rotate_axes(B, num_axes=5) == INVALID
+    assert _rotate_axes(B, stride=3) == INVALID                     # rows that overlap
+    assert _rotate_axes(B, axes=None) == INVALID
+    assert _rotate_axes(B, positions=None) == INVALID
+    assert _rotate_axes(B, d=12) == UNSUPPORTED and _rotate_axes(B, flags=4) == INVALID
+    null = B.PaRotaryAxes(None, 3, 0)
+    assert _rotate_axes(B, axes=ctypes.byref(null)) == INVALID
+    rot = B.PaRotary(FAKE, 8, 0, 1.0)
+    pool = B.PaKvPool(FAKE, 4, 2, 16, 16, 0, 0, 0)
+    f = B.lib().pa_rotate_and_cache_axes
+    assert f(ctypes.byref(pool), None, None, 0, FAKE, 0, FAKE, 0, FAKE, FAKE, 4, 0, ctypes.byref(rot), None,
+             None) == INVALID
+
+
+# ---------------------------------------------------------------------------
+# tables
+# ---------------------------------------------------------------------------
+
+def _extend(B, **kw):
+    """A call whose arrays lie 2^16 bytes apart (never read: it is refused)."""
+    at = lambda i: FAKE + (i << 16)  # noqa: E731
+    a = dict(tables=at(0), width=4, lens=at(1), starts=at(2), positions=at(3), slots=at(4), tokens=8, ctx=at(5),
+             new=at(6), offsets=None, seqs=3, free=at(7), num_free=10, cursor=at(8), cursor_out=at(9), b=16, blocks=64)
+    a.update(kw)
+    return B.lib().pa_extend_tables(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw", [dict(width=0), dict(tokens=-1), dict(seqs=-1), dict(seqs=(1 << 20) + 1), dict(b=0),
+                                dict(blocks=0), dict(blocks=1 << 31), dict(num_free=-1)] +
+                         [{k: None} for k in ("tables", "lens", "starts", "positions", "slots", "ctx", "new", "free",
+                                              "cursor", "cursor_out")])
+def test_extend_refusals(B, kw):
+    assert _extend(B, **kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(lens=FAKE + (5 << 16)), dict(lens=FAKE + (6 << 16) + 8), dict(starts=FAKE + (5 << 16)),
+                                dict(cursor_out=FAKE + (8 << 16)), dict(offsets=FAKE + (1 << 16)),
+                                dict(free=FAKE + (3 << 16) + 60), dict(ctx=FAKE + 44), dict(new=FAKE + (4 << 16) + 60)])
+def test_extend_refuses_overlap(B, kw):
+    """Inputs that another CTA may still read while one writes them."""
+    assert _extend(B, **kw) == INVALID
+
+
+def test_extend_oracle_by_hand():
+    """The restatement the GPU tests compare with, on a step worked out by hand: b = 4,
+    sequences of 3 + 2, 8 + 1, 0 + 0 and 5 + 1 tokens, one block already taken."""
+    got = ref.extend_tables([[9, -1, -1], [1, 2, -1], [-1] * 3, [4, 5, -1]], [3, 8, 0, 5], [2, 1, 0, 1],
+                            [7, 8, 3, 6], 1, 4, 10, 6)
+    assert got["tables"] == [[9, 8, -1], [1, 2, 3], [-1] * 3, [4, 5, -1]]
+    assert got["lens"] == [5, 9, 0, 6] and got["starts"] == [0, 2, 3, 3, 4] and got["cursor"] == 3
+    assert got["positions"] == [3, 4, 8, 5, 0, 0] and got["slots"] == [39, 32, 12, 21, -1, -1]
+    short = ref.extend_tables([[9, -1, -1], [1, 2, -1], [-1] * 3, [4, 5, -1]], [3, 8, 0, 5], [2, 1, 0, 1],
+                              [7, 8], 1, 4, 10, 6)
+    assert short["lens"] == [5, 8, 0, 6] and short["cursor"] == 2 and short["errors"] == 0x80
+    assert short["slots"] == [39, 32, -1, 21, -1, -1]
