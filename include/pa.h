@@ -514,6 +514,52 @@ pa_status pa_extend_tables(int32_t *block_tables, int32_t max_blocks_per_seq, in
                            int32_t *cursor_out, int32_t block_size, int64_t num_blocks, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Differential attention: a query pair's output is the difference of two softmax
+ * maps over one row of values twice as wide,
+ *     x_h = softmax(scale q_2h K1^T) V - lambda[h] softmax(scale q_2h+1 K2^T) V,
+ * which takes out of each map what both attend alike.  With a norm weight each row
+ * is normed on its own, x_h / sqrt(mean(x_h^2) + eps) * norm_weight, and either way
+ * multiplied by out_scale.  The pages have no counterpart: they describe the cache,
+ * which stays as it is.  KV heads 2g and 2g + 1 of the pool are pair g: K1 and K2
+ * are their keys, V = [V_2g | V_2g+1] their values side by side, so the slot writers,
+ * forks, swaps and compactions serve such a pool unchanged.  Query pair h (query
+ * heads 2h and 2h + 1) belongs to pair h / R, R = num_q_heads / num_kv_heads.
+ * ------------------------------------------------------------------------- */
+#define PA_DIFF_KEYS_BY_HEAD 0x1u /* query head i reads key head i / R (both maps of a query
+                                   * pair the same one where R is even), instead of the
+                                   * pair's first and second by the map                 */
+typedef struct {
+    const float *lambda;      /* device, [num_q_heads / 2]: of the layer's learned vectors */
+    const float *norm_weight; /* device, [2 * head_dim], 16-byte aligned; NULL: no norm    */
+    float eps;                /* > 0 with norm_weight, else ignored                        */
+    float out_scale;          /* finite                                                    */
+    uint32_t flags;           /* PA_DIFF_*                                                 */
+} pa_diff;
+
+/*
+ * Differential decode attention over the paged cache: pa_decode_ex with the
+ * automatic plan.
+ *   out          device, [num_seqs][num_q_heads / 2][2 * head_dim] bf16 (written)
+ *   q, block_tables, seq_lens, max_seq_len, scale, new_k, new_v, flags  as pa_decode_ex
+ *                (a length of 0 gives zeros)
+ *   workspace    device, pa_decode_diff_workspace_size bytes, 256-byte aligned;
+ *                overwritten (calls that may run at the same time, on two streams or
+ *                from two graphs, need one each)
+ * The cache is read once for both maps.  Sums, softmax statistics, the difference and
+ * the norm are fp32; a probability enters its product as two bf16 terms, and out is
+ * rounded once.
+ * Supported: head_dim 64 or 128; an even num_kv_heads; R 1, 2, 4 or 8; block_size 4, 8,
+ * 16, 32 or 64.  Errors as pa_decode_ex; PA_ERR_INVALID_ARG for a bad pa_diff.
+ */
+size_t pa_decode_diff_workspace_size(const pa_kv_pool *pool, int32_t num_seqs, int32_t num_q_heads,
+                                     int32_t max_seq_len);
+pa_status pa_decode_diff(void *out, const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs,
+                         int32_t num_q_heads, int32_t max_seq_len, float scale, const pa_diff *diff,
+                         void *workspace, size_t workspace_bytes, const void *new_k, const void *new_v,
+                         uint32_t flags, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Rotary positions.  A head's first rot_dim components are rot_dim / 2 pairs;
  * at position t pair i is turned by the angle t * w_i:
  *     (x, y) -> mscale * (x cos - y sin, y cos + x sin)

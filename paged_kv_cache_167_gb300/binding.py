@@ -27,6 +27,7 @@ DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_SEQ_LEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x
 DEVERR_KEEP, DEVERR_VALUE, DEVERR_NO_ROOM = 0x20, 0x40, 0x80
 PA_DTYPE_BF16, PA_DTYPE_F32 = 0, 1
 PA_ROTARY_INTERLEAVED, PA_ROTARY_INVERSE = 0x1, 0x2
+DIFF_KEYS = {"map": 0, "head": 1}          # PA_DIFF_KEYS_BY_HEAD
 AXES_ORDERS = {"blocks": 0, "cycled": 1}
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3, "parts_index": 4}
 
@@ -61,6 +62,12 @@ class PaRotaryAxes(ctypes.Structure):
     _fields_ = [("axis", ctypes.c_void_p), ("num_axes", ctypes.c_int32), ("position_stride", ctypes.c_int64)]
 
 
+class PaDiff(ctypes.Structure):
+    """``pa_diff``: weights of differential attention."""
+    _fields_ = [("lam", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("out_scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
 class PaKvPool(ctypes.Structure):
     """``pa_kv_pool``: one layer's view of the block pool (strides in elements)."""
     _fields_ = [("base", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("num_kv_heads", ctypes.c_int32),
@@ -71,6 +78,7 @@ class PaKvPool(ctypes.Structure):
 _POOL = ctypes.POINTER(PaKvPool)
 _ROTARY = ctypes.POINTER(PaRotary)
 _AXES = ctypes.POINTER(PaRotaryAxes)
+_DIFF = ctypes.POINTER(PaDiff)
 SIGNATURES = {
     "pa_status_string": (ctypes.c_char_p, [_I32]),
     "pa_version": (_I32, []),
@@ -89,6 +97,8 @@ SIGNATURES = {
     "pa_prefix_attention": (_I32, [_P, _P, _P, _POOL, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _F, _P]),
     "pa_decode_cascade": (_I32, [_P, _P, _POOL, _P, _I32, _P, _I32, _I32, _I32, _F, _I32, _P, _SZ, _P, _P, _P, _P,
                                  _U32, _P]),
+    "pa_decode_diff_workspace_size": (_SZ, [_POOL, _I32, _I32, _I32]),
+    "pa_decode_diff": (_I32, [_P, _P, _POOL, _P, _I32, _P, _I32, _I32, _I32, _F, _DIFF, _P, _SZ, _P, _P, _U32, _P]),
     "pa_cascade_plan": (_I32, [_P, _I32, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "pa_decode_grouped": (_I32, [_P, _P, _POOL, _P, _I32, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F,
                                  _P, _P, _U32, _P]),
@@ -717,6 +727,65 @@ def compact_tokens(pool: torch.Tensor, src_tables: torch.Tensor, dst_tables: tor
                                    _at(keep_lens, i32, "keep_lens", dev),
                                    _at(starts, i32, "starts", dev) if starts is not None else None, B, rot,
                                    _handle(stream, dev)), "pa_compact_tokens")
+
+
+# ---- differential attention ---------------------------------------------------
+
+def decode_diff_workspace_size(pool: torch.Tensor, num_seqs: int, num_q_heads: int, max_seq_len: int,
+                               layer: Optional[int] = None) -> int:
+    desc = pool_desc(pool, layer)
+    return int(lib().pa_decode_diff_workspace_size(ctypes.byref(desc), num_seqs, num_q_heads, max_seq_len))
+
+
+def _diff(lam: torch.Tensor, norm_weight: Optional[torch.Tensor], eps: float, out_scale: float, keys: str, hq: int,
+          d: int, device: int) -> PaDiff:
+    if keys not in DIFF_KEYS:
+        raise ValueError(f"keys must be one of {sorted(DIFF_KEYS)}")
+    if 2 * lam.numel() != hq:
+        raise ValueError("lam must hold one weight a pair of query heads")
+    weight = None
+    if norm_weight is not None:
+        if norm_weight.numel() != 2 * d:
+            raise ValueError("norm_weight must hold 2 * head_dim weights")
+        weight = _at(norm_weight, torch.float32, "norm_weight", device)
+    return PaDiff(_at(lam, torch.float32, "lam", device), weight, eps, out_scale, DIFF_KEYS[keys])
+
+
+def decode_diff(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor, block_tables: torch.Tensor,
+                seq_lens: torch.Tensor, max_seq_len: int, scale: float, lam: torch.Tensor,
+                norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-5, out_scale: float = 1.0,
+                keys: str = "map", workspace: Optional[torch.Tensor] = None, layer: Optional[int] = None, stream=None,
+                flags: int = 0, new_k: Optional[torch.Tensor] = None, new_v: Optional[torch.Tensor] = None) -> None:
+    """pa_decode_diff: q [B][Hq][d] over KV heads in pairs -> out [B][Hq / 2][2 d].
+    lam fp32 [Hq / 2]; norm_weight fp32 [2 d] or None; keys "map" or "head"
+    (PA_DIFF_KEYS_BY_HEAD); workspace a uint8 CUDA tensor of
+    decode_diff_workspace_size(...) bytes; the rest as decode."""
+    desc = pool_desc(pool, layer)
+    B, Hq, d = q.shape
+    if d != desc.head_dim or Hq % 2 or tuple(out.shape) != (B, Hq // 2, 2 * d):
+        raise ValueError("q must be [num_seqs][num_q_heads][head_dim] and out [num_seqs][num_q_heads / 2][2 head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_tables / seq_lens do not match the batch")
+    dev = torch.cuda.current_device()
+    if pool.get_device() != dev:
+        _refuse(pool, torch.bfloat16, "pool", dev)
+    nk = nv = None
+    if new_k is not None:
+        nk = _at(new_k, torch.bfloat16, "new_k", dev)
+    if new_v is not None:
+        nv = _at(new_v, torch.bfloat16, "new_v", dev)
+    for name, t in (("new_k", new_k), ("new_v", new_v)):
+        if t is not None and (t.dim() != 3 or t.shape[0] != B or t.shape[1:] != (desc.num_kv_heads, desc.head_dim)):
+            raise ValueError(f"{name} must be [num_seqs][num_kv_heads][head_dim]")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _at(workspace, torch.uint8, "workspace", dev), workspace.numel()
+    weights = _diff(lam, norm_weight, eps, out_scale, keys, Hq, d, dev)
+    _check(lib().pa_decode_diff(_at(out, torch.bfloat16, "out", dev), _at(q, torch.bfloat16, "q", dev),
+                                ctypes.byref(desc), _at(block_tables, torch.int32, "block_tables", dev),
+                                block_tables.shape[1], _at(seq_lens, torch.int32, "seq_lens", dev), B, Hq,
+                                max_seq_len, scale, ctypes.byref(weights), ws, ws_bytes, nk, nv, flags,
+                                _handle(stream, dev)), "pa_decode_diff")
 
 
 def beam_select_workspace_size(num_groups: int, num_beams: int, vocab: int, num_out: int) -> int:

@@ -13,6 +13,8 @@
 namespace pa {
 cudaError_t launch_decode_d64(const DecodeArgs &a, cudaStream_t stream);
 cudaError_t launch_decode_d128(const DecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_decode_diff_d64(const DecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_decode_diff_d128(const DecodeArgs &a, cudaStream_t stream);
 
 namespace {
 
@@ -65,6 +67,27 @@ struct DecodePlan {
     size_t total_bytes() const { return ws_o_bytes + ws_ml_bytes; }
 };
 
+// The balanced schedule's grid and records: `units` (sequence, kv-head) runs a batch
+// has at most, records of `maps` rows of `width`.
+void plan_stream_k(DecodePlan *plan, int64_t units, int64_t max_seq_len, int block_size, int ctas_per_sm, int maps,
+                   int width) {
+    const int64_t max_stages = units * ceil_div(max_seq_len, (int64_t)decode_stage_tokens(block_size));
+    int64_t ctas = g_stream_k_ctas.load(std::memory_order_relaxed);
+    if (ctas <= 0) {
+        int sms = device_sm_count();
+        if (sms <= 0) sms = 148;
+        ctas = (int64_t)sms * ctas_per_sm;
+    }
+    if (ctas > max_stages) ctas = max_stages;
+    if (ctas < 1) ctas = 1;
+    plan->stream_k = true;
+    plan->partition_tokens = max_seq_len > 0 ? (int32_t)max_seq_len : 1;   // length bound used by the kernel
+    plan->num_partitions = 1;
+    plan->num_ctas = (int32_t)ctas;
+    plan->ws_o_bytes = round_up((size_t)2 * ctas * maps * width * sizeof(float), kWsAlign);
+    plan->ws_ml_bytes = round_up((size_t)2 * ctas * maps * 2 * sizeof(float), kWsAlign);
+}
+
 pa_status plan_decode(const PoolView &pool, int32_t num_seqs, int32_t num_q_heads, int32_t max_seq_len,
                       int32_t partition_tokens, DecodePlan *plan) {
     if (num_seqs < 0 || num_q_heads <= 0 || max_seq_len < 0 || partition_tokens < 0) return PA_ERR_INVALID_ARG;
@@ -75,22 +98,8 @@ pa_status plan_decode(const PoolView &pool, int32_t num_seqs, int32_t num_q_head
     if (partition_tokens == 0) {
         // Persistent stream-K: two CTAs per SM share all (sequence, kv-head,
         // stage) work equally; at most two partial records per CTA.
-        const int64_t stage = decode_stage_tokens(pool.block_size);
-        const int64_t max_stages = (int64_t)num_seqs * pool.num_kv_heads * ceil_div(max_seq_len, stage);
-        int64_t ctas = g_stream_k_ctas.load(std::memory_order_relaxed);
-        if (ctas <= 0) {
-            int sms = device_sm_count();
-            if (sms <= 0) sms = 148;
-            ctas = (int64_t)sms * kStreamKCtasPerSm;
-        }
-        if (ctas > max_stages) ctas = max_stages;
-        if (ctas < 1) ctas = 1;
-        plan->stream_k = true;
-        plan->partition_tokens = max_seq_len > 0 ? max_seq_len : 1;   // length bound used by the kernel
-        plan->num_partitions = 1;
-        plan->num_ctas = (int32_t)ctas;
-        plan->ws_o_bytes = round_up((size_t)2 * ctas * group * pool.head_dim * sizeof(float), kWsAlign);
-        plan->ws_ml_bytes = round_up((size_t)2 * ctas * group * 2 * sizeof(float), kWsAlign);
+        plan_stream_k(plan, (int64_t)num_seqs * pool.num_kv_heads, max_seq_len, pool.block_size, kStreamKCtasPerSm,
+                      group, pool.head_dim);
         return PA_OK;
     }
     if (partition_tokens % pool.block_size != 0) return PA_ERR_INVALID_ARG;
@@ -104,6 +113,26 @@ pa_status plan_decode(const PoolView &pool, int32_t num_seqs, int32_t num_q_head
         plan->ws_ml_bytes = round_up(rows * 2 * sizeof(float), kWsAlign);
     }
     return PA_OK;
+}
+
+// Differential decode: a unit is a pair of KV heads with 2R maps over rows two heads
+// wide.  One CTA an SM where a stage of such rows fills twice the shared memory.
+pa_status plan_decode_diff(const PoolView &pool, int32_t num_seqs, int32_t num_q_heads, int32_t max_seq_len,
+                           DecodePlan *plan) {
+    if (num_seqs < 0 || num_q_heads <= 0 || max_seq_len < 0) return PA_ERR_INVALID_ARG;
+    if (num_q_heads % pool.num_kv_heads != 0 || pool.num_kv_heads % 2 != 0) return PA_ERR_INVALID_ARG;
+    const int pairs = num_q_heads / pool.num_kv_heads;
+    if (!decode_supported(pool.head_dim, pairs, pool.block_size)) return PA_ERR_UNSUPPORTED;
+    *plan = DecodePlan{};
+    plan_stream_k(plan, (int64_t)num_seqs * (pool.num_kv_heads / 2), max_seq_len, pool.block_size,
+                  pool.head_dim == 128 ? 1 : kStreamKCtasPerSm, 2 * pairs, 2 * pool.head_dim);
+    return PA_OK;
+}
+
+bool diff_ok(const pa_diff *d) {
+    if (!d || !d->lambda || (reinterpret_cast<uintptr_t>(d->lambda) & 3u) != 0) return false;
+    if (!std::isfinite(d->out_scale) || (d->flags & ~PA_DIFF_KEYS_BY_HEAD) != 0) return false;
+    return !d->norm_weight || (aligned16(d->norm_weight) && std::isfinite(d->eps) && d->eps > 0.f);
 }
 
 }  // namespace
@@ -123,6 +152,10 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream) {
         case 128: return launch_decode_d128(a, stream);
         default: return cudaErrorInvalidValue;
     }
+}
+
+cudaError_t launch_decode_diff(const DecodeArgs &a, cudaStream_t stream) {
+    return a.pool.head_dim == 64 ? launch_decode_diff_d64(a, stream) : launch_decode_diff_d128(a, stream);
 }
 
 }  // namespace pa
@@ -269,6 +302,59 @@ pa_status pa_decode_cascade(void *out, const void *q, const pa_kv_pool *pool, co
     return decode_impl(out, q, pool, suffix_tables, max_blocks_per_seq, suffix_lens, num_seqs, num_q_heads,
                        max_suffix_len, scale, partition_tokens, workspace, workspace_bytes, prefix_o, prefix_lse,
                        new_k, new_v, flags, stream);
+}
+
+size_t pa_decode_diff_workspace_size(const pa_kv_pool *pool, int32_t num_seqs, int32_t num_q_heads,
+                                     int32_t max_seq_len) {
+    PoolView view;
+    DecodePlan plan;
+    if (resolve_pool(pool, &view) != PA_OK) return 0;
+    if (plan_decode_diff(view, num_seqs, num_q_heads, max_seq_len, &plan) != PA_OK) return 0;
+    return plan.total_bytes();
+}
+
+pa_status pa_decode_diff(void *out, const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t num_seqs,
+                         int32_t num_q_heads, int32_t max_seq_len, float scale, const pa_diff *diff,
+                         void *workspace, size_t workspace_bytes, const void *new_k, const void *new_v,
+                         uint32_t flags, cudaStream_t stream) {
+    if ((flags & ~PA_DECODE_EARLY_METADATA) != 0 || !diff_ok(diff)) return PA_ERR_INVALID_ARG;
+    if ((new_k == nullptr) != (new_v == nullptr)) return PA_ERR_INVALID_ARG;
+    if (new_k && (!aligned16(new_k) || !aligned16(new_v))) return PA_ERR_INVALID_ARG;
+    PoolView view;
+    pa_status st = resolve_pool(pool, &view);
+    if (st != PA_OK) return st;
+    DecodePlan plan;
+    st = plan_decode_diff(view, num_seqs, num_q_heads, max_seq_len, &plan);
+    if (st != PA_OK) return st;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !q || !block_tables || !seq_lens || max_blocks_per_seq <= 0) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !std::isfinite(scale) || num_seqs > 65535) return PA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < plan.total_bytes() ||
+        (reinterpret_cast<uintptr_t>(workspace) % kWsAlign) != 0)
+        return PA_ERR_WORKSPACE;
+    DecodeArgs a;
+    a.out = out;
+    a.q = q;
+    a.pool = view;
+    a.tables = block_tables;
+    a.max_blocks = max_blocks_per_seq;
+    a.seq_lens = seq_lens;
+    a.num_seqs = num_seqs;
+    a.num_q_heads = num_q_heads;
+    a.max_seq_len = max_seq_len;
+    a.scale = scale;
+    a.partition_tokens = plan.partition_tokens;
+    a.num_partitions = plan.num_partitions;
+    a.ws_o = static_cast<float *>(workspace);
+    a.ws_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.ws_o_bytes);
+    a.stream_k = true;
+    a.num_ctas = plan.num_ctas;
+    a.early_meta = (flags & PA_DECODE_EARLY_METADATA) != 0;
+    a.new_k = new_k;
+    a.new_v = new_v;
+    a.diff = diff;
+    return launch_decode_diff(a, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_copy_blocks(const pa_kv_pool *pool, const int32_t *pairs, int32_t num_pairs, cudaStream_t stream) {

@@ -71,6 +71,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -132,7 +133,7 @@ struct Shape {
     static constexpr int SLOT = BPS * REGION;         // bytes of a stage's K (or V) slot
     static constexpr int NCH = D / 32;                // 16-byte chunks of a K row that one lane reads
     static constexpr int DK = D / 16;                 // Q.K steps over d = P.V tiles of d
-    static_assert(D == 64 || D == 128, "head_dim");
+    static_assert(D == 64 || D == 128 || D == 256, "head_dim, or two of them");
     static_assert(BS == 4 || BS == 8 || BS == 16 || BS == 32 || BS == 64, "block size");
     // logical block of box ib of the stage starting at token tok0, and the
     // first slot the box copies (stages start on multiples of 16 tokens when
@@ -150,13 +151,14 @@ struct alignas(1024) WarpRing {
     unsigned char v[NS][Shape<D, BS>::SLOT];
 };
 
-// CTA-level scratch of the stream-K kernel (after the warps' rings).
-template <int D, int G>
+// CTA-level scratch of the stream-K kernel (after the warps' rings); q rows have DQ
+// components.
+template <int D, int G, int DQ = D>
 struct alignas(16) SkSmem {
     float cm[kWarps * G];             // warps' running maxima
     float cl[kWarps * G];             // warps' denominators
     float co[kWarps * G * D];         // warps' numerators
-    __nv_bfloat16 q[2][G * D];        // q of the current and next unit
+    __nv_bfloat16 q[2][G * DQ];       // q of the current and next unit
     int seg_s[kMaxSegs], seg_g[kMaxSegs], seg_kb[kMaxSegs], seg_ke[kMaxSegs], seg_lb[kMaxSegs + 1];
     int scan[kWarps];                 // block-scan scratch
     int found_s, found_base, nseg, more, next_pos;
@@ -207,6 +209,11 @@ struct Params {
     // every final output row (nullptr: none)
     const float *pre_o;          // [B][Hq][D]
     const float *pre_lse;        // [B][Hq]
+    // differential attention (num_kv_heads then counts pairs of KV heads)
+    const float *lambda;         // [Hq / 2]
+    const float *norm_weight;    // [D] or nullptr: no norm
+    float eps, out_scale;
+    int32_t by_head;             // query head i of a group reads key head i / R
 };
 
 // The prefix term of one output row: its log-sum-exp and N dims of its
@@ -571,6 +578,35 @@ __device__ __forceinline__ void cta_combine_store(const CombinePrefix<D, G> &pre
     }
 }
 
+}  // namespace decode
+}  // namespace pa
+
+#include "pa_decode_diff.cuh"
+
+namespace pa {
+namespace decode {
+
+// What the stream-K kernel does per unit, for plain attention; DiffOp
+// (pa_decode_diff.cuh) for the differential one.
+template <int D, int G, int BS>
+struct PlainOp {
+    using State = WarpState<D>;
+    struct Q {
+        uint32_t w[D / 8];
+    };
+    static __device__ __forceinline__ void load_q(Q &q, const __nv_bfloat16 *rows, int lane, bool) {
+        load_qf<D, G, true>(q.w, rows, lane);
+    }
+    static __device__ __forceinline__ void compute(uint32_t kslot, uint32_t vslot, const Q &q, int tok0, int tok_end,
+                                                   float scale_log2, int lane, State &st) {
+        stage_compute<D, G, BS>(kslot, vslot, q.w, tok0, tok_end, scale_log2, lane, st);
+    }
+    static __device__ __forceinline__ void publish(State &st, bool has_work, int lane, int warp, float *cm, float *cl,
+                                                   float *co) {
+        warp_publish<D, G>(st, has_work, lane, warp, cm, cl, co);
+    }
+};
+
 // ---- split-context partition kernel --------------------------------------------
 
 template <int D, int G, int BS>
@@ -787,14 +823,20 @@ __device__ __forceinline__ int block_inclusive_scan(int v, int *scratch, int &to
     return v + offset;
 }
 
-template <int D, int G, int BS>
-__global__ void __launch_bounds__(kWarps * 32, kMinCtas)
+// Differential attention (kDiff): D is two heads wide, G = 2R map columns, and a
+// "kv-head" g is the pair of KV heads (2g, 2g + 1).  Two CTAs an SM where the rings
+// allow it (D = 256: one, with twice the bytes a stage).
+template <int D, int G, int BS, bool kDiff = false>
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
     paged_decode_sk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                            const Params p) {
     using S = Shape<D, BS>;
     using WR = WarpRing<D, BS, kSkStages>;
     using SP = SmemPlan<D, BS, kSkStages>;
-    using SK = SkSmem<D, G>;
+    constexpr int DQ = kDiff ? D / 2 : D;      // components of a query row
+    constexpr int HB = kDiff ? 2 : 1;          // KV heads of a copy box
+    using SK = SkSmem<D, G, DQ>;
+    using Op = typename std::conditional<kDiff, DiffOp<D, G, BS>, PlainOp<D, G, BS>>::type;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = align1024(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -1004,8 +1046,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
             // wait find them there.
             if (tid < 2 && tid < nseg) {
                 const size_t head0 = (size_t)sk->seg_s[tid] * p.num_q_heads + (size_t)sk->seg_g[tid] * G;
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + head0 * D),
-                             "r"((uint32_t)(G * D * 2))
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + head0 * DQ),
+                             "r"((uint32_t)(G * DQ * 2))
                              : "memory");
             }
 #pragma unroll 1
@@ -1019,8 +1061,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
                 for (int ib = 0; ib < S::BPS; ++ib) {
                     const int id = __shfl_sync(0xffffffffu, id_cache, k * S::BPS + ib);
                     if (lane == 0 && id >= 0) {
-                        tensor_prefetch_l2_5d(&tmk, 0, c_slot, 0, g, id);
-                        tensor_prefetch_l2_5d(&tmv, 0, c_slot, 0, g, id);
+                        tensor_prefetch_l2_5d(&tmk, 0, c_slot, 0, g * HB, id);
+                        tensor_prefetch_l2_5d(&tmv, 0, c_slot, 0, g * HB, id);
                     }
                 }
             }
@@ -1032,8 +1074,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
             if (j >= nseg) return;
             const int b = (jbase + j) & 1;
             const size_t head0 = (size_t)sk->seg_s[j] * p.num_q_heads + (size_t)sk->seg_g[j] * G;
-            mbar_arrive_expect_tx(&sk->qbar[b], (uint32_t)(G * D * 2));
-            bulk_g2s(sk->q[b], p.q + head0 * D, (uint32_t)(G * D * 2), &sk->qbar[b]);
+            mbar_arrive_expect_tx(&sk->qbar[b], (uint32_t)(G * DQ * 2));
+            bulk_g2s(sk->q[b], p.q + head0 * DQ, (uint32_t)(G * DQ * 2), &sk->qbar[b]);
         };
         if (tid == 0) {
             issue_q(0);
@@ -1069,8 +1111,20 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
                     for (int x = 0; x < S::BPS; ++x) blk = x == ib ? ids[x] : blk;
                     if (blk >= 0) {
                         constexpr int CH = D / 8;   // 16-byte chunks per row
+                        if constexpr (kDiff) {      // the rows of both heads
+#pragma unroll
+                            for (int x = lane; x < 2 * CH; x += 32) {
+                                const int half = x / CH, h = (x % CH) / (CH / 2), c16 = x % (CH / 2);
+                                const size_t head = (size_t)g * 2 + h;
+                                const __nv_bfloat16 *src = (half == 0 ? p.new_k : p.new_v) +
+                                                           ((size_t)s * p.num_kv_heads * 2 + head) * DQ + c16 * 8;
+                                __nv_bfloat16 *dst = p.pool + (size_t)blk * p.block_stride + half * p.kv_stride +
+                                                     (head * BS + last % BS) * DQ + c16 * 8;
+                                *reinterpret_cast<uint4 *>(dst) = __ldg(reinterpret_cast<const uint4 *>(src));
+                            }
+                        }
                         const int half = lane / CH, c16 = lane % CH;
-                        if (half < 2) {
+                        if (!kDiff && half < 2) {
                             const __nv_bfloat16 *src = (half == 0 ? p.new_k : p.new_v) +
                                                        ((size_t)s * p.num_kv_heads + g) * D + c16 * 8;
                             __nv_bfloat16 *dst = p.pool + (size_t)blk * p.block_stride + half * p.kv_stride +
@@ -1091,8 +1145,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
 #pragma unroll
                 for (int ib = 0; ib < S::BPS; ++ib) {
                     if (ids[ib] >= 0) {
-                        tensor_copy_5d(kslot + ib * S::REGION, &tmk, 0, c_slot, 0, g, ids[ib], &bar[slot]);
-                        tensor_copy_5d(vslot + ib * S::REGION, &tmv, 0, c_slot, 0, g, ids[ib], &bar[slot]);
+                        tensor_copy_5d(kslot + ib * S::REGION, &tmk, 0, c_slot, 0, g * HB, ids[ib], &bar[slot]);
+                        tensor_copy_5d(vslot + ib * S::REGION, &tmv, 0, c_slot, 0, g * HB, ids[ib], &bar[slot]);
                     }
                 }
             }
@@ -1110,16 +1164,16 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
             const bool complete = sk->seg_kb[j] == 0 && sk->seg_ke[j] == ns;
             const size_t head0 = (size_t)s * p.num_q_heads + (size_t)g * G;
             CombinePrefix<D, G> pre;   // loaded now, used at the segment's end
-            pre.load(p, head0, complete);
+            if constexpr (!kDiff) pre.load(p, head0, complete);
             const int jg = jbase + j;
             const bool qok = mbar_wait_bounded(&sk->qbar[jg & 1], (uint32_t)((jg >> 1) & 1), p.err);
             if (!__syncthreads_and(qok)) {
                 ok = false;
                 break;
             }
-            uint32_t qf[D / 8];
-            load_qf<D, G, true>(qf, sk->q[jg & 1], lane);
-            WarpState<D> st;
+            typename Op::Q qf;
+            Op::load_q(qf, sk->q[jg & 1], lane, p.by_head != 0);
+            typename Op::State st;
             st.reset();
             const int lend = sk->seg_lb[j + 1];
             int done = 0;
@@ -1133,22 +1187,26 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
                     break;
                 }
                 const int tok0 = (sk->seg_kb[j] + i - sk->seg_lb[j]) * S::TPS;
-                stage_compute<D, G, BS>(ring + slot * S::SLOT, ring + (kSkStages + slot) * S::SLOT, qf, tok0, L,
-                                        p.scale_log2, lane, st);
+                Op::compute(ring + slot * S::SLOT, ring + (kSkStages + slot) * S::SLOT, qf, tok0, L, p.scale_log2,
+                            lane, st);
                 __syncwarp();   // every lane is done with the slot before it is refilled
                 issue(k + kSkStages);
                 ++k;
                 ++done;
             }
-            warp_publish<D, G>(st, done > 0, lane, warp, sk->cm, sk->cl, sk->co);
+            Op::publish(st, done > 0, lane, warp, sk->cm, sk->cl, sk->co);
             if (!__syncthreads_and(ok)) {
                 ok = false;
                 break;
             }
             const bool is_first = first_seg && j == 0;
             const int rec = 2 * c + (is_first ? 0 : 1);
-            cta_combine_store<D, G>(pre, sk->cm, sk->cl, sk->co, complete, p.out + head0 * D,
-                                    p.ws_o + (size_t)rec * G * D, D, p.ws_ml + (size_t)rec * G * 2, 2);
+            if constexpr (kDiff)
+                Op::combine_store(p, sk->cm, sk->cl, sk->co, complete, head0 / 2, g * (G / 2),
+                                  p.ws_o + (size_t)rec * G * D, p.ws_ml + (size_t)rec * G * 2);
+            else
+                cta_combine_store<D, G>(pre, sk->cm, sk->cl, sk->co, complete, p.out + head0 * D,
+                                        p.ws_o + (size_t)rec * G * D, D, p.ws_ml + (size_t)rec * G * 2, 2);
             __syncthreads();   // scratch and this q buffer are free again
             if (tid == 0) issue_q(j + 2);
         }
@@ -1196,8 +1254,9 @@ constexpr int kMergeThreads = PA_MERGE_THREADS;
 // uneven placement of warps: at 56, some SMs kept the next call's decode CTAs
 // waiting for merge blocks to exit (34.93 against 34.43 us a call on the
 // Llama-shaped batch).
-template <int D, int G, int BS>
-__global__ void __launch_bounds__(kMergeThreads, PA_MERGE_MIN_BLOCKS) paged_decode_sk_merge_kernel(const Params p) {
+template <int D, int G, int BS, bool kDiff = false>
+__global__ void __launch_bounds__(kMergeThreads, kDiff ? 4 : PA_MERGE_MIN_BLOCKS)
+    paged_decode_sk_merge_kernel(const Params p) {
     grid_launch_dependents();   // the next kernel waits for this grid's completion before using its data
     constexpr int NT = kMergeThreads, NW = NT / 32;
     __shared__ int scan[NW];
@@ -1254,6 +1313,9 @@ __global__ void __launch_bounds__(kMergeThreads, PA_MERGE_MIN_BLOCKS) paged_deco
         // it (which ends kUnitCost positions before u0) lies in that CTA's range
         const int first_rec = (u0 - ca * per > kUnitCost) ? 1 : 0;
         const size_t row0 = (size_t)s * p.num_q_heads + (size_t)g * G;
+        if constexpr (kDiff) {
+            DiffOp<D, G, BS>::merge(p, ca, cb, first_rec, row0 / 2, g * (G / 2), warp, NW, lane);
+        } else {
         // A thread's items (head, four dims) and up to kR records per pass are
         // loaded before any is combined, so a pass costs one memory round trip;
         // passes merge online (running maximum, rescaled sums).
@@ -1319,10 +1381,16 @@ __global__ void __launch_bounds__(kMergeThreads, PA_MERGE_MIN_BLOCKS) paged_deco
                 make_uint2(pack_bf16x2(acc[t][0] * inv, acc[t][1] * inv), pack_bf16x2(acc[t][2] * inv, acc[t][3] * inv));
         }
         }
+        }
     }
     // sequences with no keys of their own: zero rows, or the prefix term alone
     for (int s = c; s < B; s += C) {
         if (seq_stages<BS>(p, s, false) != 0) continue;
+        if constexpr (kDiff) {   // zeros: both maps of no keys (the norm of zeros is zero)
+            const int n = p.num_q_heads / 2 * (D / 4);
+            for (int it = tid; it < n; it += NT)
+                reinterpret_cast<uint2 *>(p.out)[(size_t)s * n + it] = make_uint2(0u, 0u);
+        } else {
         for (int it = tid; it < p.num_q_heads * (D / 4); it += NT) {
             const size_t row = (size_t)s * p.num_q_heads + it / (D / 4);
             const int i = (it % (D / 4)) * 4;
@@ -1331,6 +1399,7 @@ __global__ void __launch_bounds__(kMergeThreads, PA_MERGE_MIN_BLOCKS) paged_deco
             const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
             *reinterpret_cast<uint2 *>(p.out + row * D + i) =
                 make_uint2(pack_bf16x2(a4[0] * inv, a4[1] * inv), pack_bf16x2(a4[2] * inv, a4[3] * inv));
+        }
         }
     }
 }
@@ -1411,17 +1480,17 @@ cudaError_t launch_group(const CUtensorMap &tmk, const CUtensorMap &tmv, const P
     }
 }
 
-template <int D>
-cudaError_t launch_for_dim(const DecodeArgs &a, cudaStream_t stream) {
+// The kernels' parameters and the K and V maps (boxes of `heads` KV heads).
+inline cudaError_t make_params(const DecodeArgs &a, int heads, CUtensorMap *tmk, CUtensorMap *tmv, Params *out) {
     unsigned int *err = device_error_word();
     if (!err) return cudaErrorUnknown;
-    CUtensorMap tmk, tmv;
     const int rows = a.pool.block_size < 16 ? a.pool.block_size : 16;   // slots per copy box
-    cudaError_t e = encode_pool_block_map(&tmk, a.pool, 0, rows);
+    cudaError_t e = encode_pool_block_map(tmk, a.pool, 0, rows, heads);
     if (e != cudaSuccess) return e;
-    e = encode_pool_block_map(&tmv, a.pool, 1, rows);
+    e = encode_pool_block_map(tmv, a.pool, 1, rows, heads);
     if (e != cudaSuccess) return e;
-    Params prm;
+    Params &prm = *out;
+    prm = Params{};
     prm.out = static_cast<__nv_bfloat16 *>(a.out);
     prm.q = static_cast<const __nv_bfloat16 *>(a.q);
     prm.num_blocks = a.pool.num_blocks;
@@ -1447,6 +1516,15 @@ cudaError_t launch_for_dim(const DecodeArgs &a, cudaStream_t stream) {
     prm.block_stride = a.pool.block_stride;
     prm.kv_stride = a.pool.kv_stride;
     prm.err = err;
+    return cudaSuccess;
+}
+
+template <int D>
+cudaError_t launch_for_dim(const DecodeArgs &a, cudaStream_t stream) {
+    CUtensorMap tmk, tmv;
+    Params prm;
+    const cudaError_t e = make_params(a, 1, &tmk, &tmv, &prm);
+    if (e != cudaSuccess) return e;
     const int G = a.num_q_heads / a.pool.num_kv_heads;
     const int bs = a.pool.block_size, H = a.pool.num_kv_heads, B = a.num_seqs;
     const bool sk = a.stream_k;
@@ -1455,6 +1533,57 @@ cudaError_t launch_for_dim(const DecodeArgs &a, cudaStream_t stream) {
         case 2: return launch_group<D, 2>(tmk, tmv, prm, bs, H, B, sk, stream);
         case 4: return launch_group<D, 4>(tmk, tmv, prm, bs, H, B, sk, stream);
         case 8: return launch_group<D, 8>(tmk, tmv, prm, bs, H, B, sk, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// Differential attention: D = 2d, G = 2R map columns a pair of KV heads.
+template <int D, int G, int BS>
+cudaError_t launch_diff_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &prm,
+                              cudaStream_t stream) {
+    constexpr size_t smem = SmemPlan<D, BS, kSkStages>::bytes(sizeof(SkSmem<D, G, D / 2>));
+    static_assert(smem <= 232448, "shared memory");
+    static bool configured[64] = {};
+    cudaError_t e = ensure_smem(paged_decode_sk_kernel<D, G, BS, true>, smem, configured);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(paged_decode_sk_kernel<D, G, BS, true>, dim3(prm.num_ctas), dim3(kWarps * 32), smem, stream, tmk,
+                   tmv, prm);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_decode_sk_merge_kernel<D, G, BS, true>, dim3(prm.num_ctas), dim3(kMergeThreads), 0, stream,
+                      prm);
+}
+
+template <int D, int G>
+cudaError_t launch_diff_group(const CUtensorMap &tmk, const CUtensorMap &tmv, const Params &prm, int bs,
+                              cudaStream_t stream) {
+    switch (bs) {
+        case 4: return launch_diff_shape<D, G, 4>(tmk, tmv, prm, stream);
+        case 8: return launch_diff_shape<D, G, 8>(tmk, tmv, prm, stream);
+        case 16: return launch_diff_shape<D, G, 16>(tmk, tmv, prm, stream);
+        case 32: return launch_diff_shape<D, G, 32>(tmk, tmv, prm, stream);
+        case 64: return launch_diff_shape<D, G, 64>(tmk, tmv, prm, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <int D>
+cudaError_t launch_diff_for_dim(const DecodeArgs &a, cudaStream_t stream) {
+    CUtensorMap tmk, tmv;
+    Params prm;
+    const cudaError_t e = make_params(a, 2, &tmk, &tmv, &prm);
+    if (e != cudaSuccess) return e;
+    prm.num_kv_heads = a.pool.num_kv_heads / 2;
+    prm.lambda = a.diff->lambda;
+    prm.norm_weight = a.diff->norm_weight;
+    prm.eps = a.diff->eps;
+    prm.out_scale = a.diff->out_scale;
+    prm.by_head = (a.diff->flags & PA_DIFF_KEYS_BY_HEAD) != 0;
+    const int bs = a.pool.block_size;
+    switch (a.num_q_heads / a.pool.num_kv_heads) {
+        case 1: return launch_diff_group<D, 2>(tmk, tmv, prm, bs, stream);
+        case 2: return launch_diff_group<D, 4>(tmk, tmv, prm, bs, stream);
+        case 4: return launch_diff_group<D, 8>(tmk, tmv, prm, bs, stream);
+        case 8: return launch_diff_group<D, 16>(tmk, tmv, prm, bs, stream);
         default: return cudaErrorInvalidValue;
     }
 }

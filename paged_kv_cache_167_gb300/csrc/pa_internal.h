@@ -39,8 +39,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // a 64-wide half, slot, half of d, kv-head, block): one box is `box_rows`
 // slots (the whole block when box_rows = block_size) of one (block, K|V,
 // kv-head) slab, laid out [half][slot][64] with 128-byte swizzle (head_dim 64
-// or 128).  A block coordinate of num_blocks reads as zeros.
-cudaError_t encode_pool_block_map(CUtensorMap *map, const PoolView &pool, int kv, int box_rows);
+// or 128), or of box_heads such slabs one behind the other.  A block coordinate of
+// num_blocks reads as zeros.
+cudaError_t encode_pool_block_map(CUtensorMap *map, const PoolView &pool, int kv, int box_rows, int box_heads = 1);
 
 // ---- slot writer and block copies (pa_cache.cu) ---------------------------
 cudaError_t launch_reshape_and_cache(const PoolView &pool, const void *k, const void *v,
@@ -146,6 +147,7 @@ struct DecodeArgs {
     const void *new_v = nullptr;
     const float *pre_o = nullptr;      // cascade: prefix partial [B][Hq][d] fp32 (normalised)
     const float *pre_lse = nullptr;    // and its log-sum-exp [B][Hq]
+    const pa_diff *diff = nullptr;     // differential attention (stream-K only)
 };
 
 // Tokens per pipeline stage of the decode kernel for a block size (the
@@ -153,6 +155,7 @@ struct DecodeArgs {
 int decode_stage_tokens(int block_size);
 bool decode_supported(int head_dim, int group, int block_size);
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_decode_diff(const DecodeArgs &a, cudaStream_t stream);   // pa_decode_diff_*.cu
 
 // ---- prefill (pa_prefill.cu) -----------------------------------------------
 struct PrefillArgs {

@@ -117,3 +117,34 @@ def test_extend_oracle_by_hand():
                               [7, 8], 1, 4, 10, 6)
     assert short["lens"] == [5, 8, 0, 6] and short["cursor"] == 2 and short["errors"] == 0x80
     assert short["slots"] == [39, 32, -1, 21, -1, -1]
+
+
+# ---------------------------------------------------------------------------
+# differential attention
+# ---------------------------------------------------------------------------
+
+def _decode_diff(B, hkv=2, hq=4, d=64, b=16, seqs=3, seq_len=40, q=FAKE, lam=FAKE, weight=FAKE, eps=1e-5, scale=0.1,
+                 out_scale=1.0, dflags=0, flags=0, ws=FAKE, ws_bytes=1 << 40, new_k=None, new_v=None, diff=True):
+    pool = B.PaKvPool(FAKE, 64, hkv, b, d, 0, 0, 0)
+    weights = B.PaDiff(lam, weight, eps, out_scale, dflags)
+    return B.lib().pa_decode_diff(FAKE, q, ctypes.byref(pool), FAKE, 4, FAKE, seqs, hq, seq_len, scale,
+                                  ctypes.byref(weights) if diff else None, ws, ws_bytes, new_k, new_v, flags, None)
+
+
+@pytest.mark.parametrize("kw", [dict(hkv=3, hq=3), dict(hq=5), dict(seqs=-1), dict(seq_len=-1), dict(q=None),
+                                dict(q=FAKE + 8), dict(lam=None), dict(lam=FAKE + 2), dict(weight=FAKE + 4),
+                                dict(eps=0.0), dict(eps=float("nan")), dict(eps=-1.0), dict(scale=float("inf")),
+                                dict(out_scale=float("nan")), dict(dflags=2), dict(flags=2), dict(new_k=FAKE),
+                                dict(new_k=FAKE, new_v=FAKE + 8), dict(diff=False), dict(seqs=65536)])
+def test_decode_diff_refusals(B, kw):
+    assert _decode_diff(B, **kw) == INVALID
+
+
+def test_decode_diff_more_refusals(B):
+    assert _decode_diff(B, d=32) == UNSUPPORTED and _decode_diff(B, b=12) == UNSUPPORTED
+    assert _decode_diff(B, hq=6) == UNSUPPORTED
+    assert _decode_diff(B, ws=None) == WORKSPACE and _decode_diff(B, ws_bytes=64) == WORKSPACE
+    assert _decode_diff(B, ws=FAKE + 16) == WORKSPACE
+    assert _decode_diff(B, seqs=0) == 0 and _decode_diff(B, seqs=0, weight=None, eps=0.0) == 0
+    pool = B.PaKvPool(FAKE, 64, 3, 16, 64, 0, 0, 0)
+    assert B.lib().pa_decode_diff_workspace_size(ctypes.byref(pool), 4, 6, 100) == 0
