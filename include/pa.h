@@ -559,6 +559,24 @@ pa_status pa_decode_diff(void *out, const void *q, const pa_kv_pool *pool, const
                          void *workspace, size_t workspace_bytes, const void *new_k, const void *new_v,
                          uint32_t flags, cudaStream_t stream);
 
+/*
+ * Differential attention of a chunk against the paged context: pa_prefill_chunk's
+ * queries, positions and causal mask.
+ *   out          device, [num_seqs][chunk_len][num_q_heads / 2][2 * head_dim] bf16
+ *   q, block_tables, ctx_lens, max_ctx_len, scale  as pa_prefill_chunk
+ * The chunk's own K/V must already be in the pool.  Both products run on the tcgen05
+ * tensor cores with fp32 accumulation, a cluster of two CTAs a tile of queries, one
+ * for each map; a probability is rounded to bf16 (relative 2^-8, its sum is not), the
+ * difference and the norm are fp32, and out is rounded once.
+ * Supported: head_dim 64 or 128; an even num_kv_heads; R 1, 2, 4 or 8; block_size 8, 16,
+ * 32 or 64; at most 65,535 sequences.  Errors as pa_prefill_chunk;
+ * PA_ERR_INVALID_ARG for a bad pa_diff.
+ */
+pa_status pa_prefill_diff(void *out, const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                          int32_t max_blocks_per_seq, const int32_t *ctx_lens, int32_t num_seqs,
+                          int32_t chunk_len, int32_t num_q_heads, int32_t max_ctx_len, float scale,
+                          const pa_diff *diff, cudaStream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Rotary positions.  A head's first rot_dim components are rot_dim / 2 pairs;
  * at position t pair i is turned by the angle t * w_i:
@@ -813,7 +831,8 @@ pa_status pa_set_stream_k_ctas(int32_t ctas);
 
 /*
  * Testing hook: the number of persistent CTAs of the tensor-core kernel
- * behind pa_prefill_chunk, pa_prefix_attention and pa_decode_grouped.  That
+ * behind pa_prefill_chunk, pa_prefix_attention and pa_decode_grouped, and (half as
+ * many clusters of two, at least one) of pa_prefill_diff's.  That
  * kernel splits its work into units of one (M-tile, kv-head, sequence) each and
  * runs one CTA per SM by default, each CTA walking its share of the units (in
  * rounds of alternating direction) with its copy and tensor-core pipeline

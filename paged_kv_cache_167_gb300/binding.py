@@ -99,6 +99,7 @@ SIGNATURES = {
                                  _U32, _P]),
     "pa_decode_diff_workspace_size": (_SZ, [_POOL, _I32, _I32, _I32]),
     "pa_decode_diff": (_I32, [_P, _P, _POOL, _P, _I32, _P, _I32, _I32, _I32, _F, _DIFF, _P, _SZ, _P, _P, _U32, _P]),
+    "pa_prefill_diff": (_I32, [_P, _P, _POOL, _P, _I32, _P, _I32, _I32, _I32, _I32, _F, _DIFF, _P]),
     "pa_cascade_plan": (_I32, [_P, _I32, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
     "pa_decode_grouped": (_I32, [_P, _P, _POOL, _P, _I32, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _F,
                                  _P, _P, _U32, _P]),
@@ -786,6 +787,29 @@ def decode_diff(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor, block_ta
                                 block_tables.shape[1], _at(seq_lens, torch.int32, "seq_lens", dev), B, Hq,
                                 max_seq_len, scale, ctypes.byref(weights), ws, ws_bytes, nk, nv, flags,
                                 _handle(stream, dev)), "pa_decode_diff")
+
+
+def prefill_diff(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor, block_tables: torch.Tensor,
+                 ctx_lens: torch.Tensor, max_ctx_len: int, scale: float, lam: torch.Tensor,
+                 norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-5, out_scale: float = 1.0,
+                 keys: str = "map", layer: Optional[int] = None, stream=None) -> None:
+    """pa_prefill_diff: q [B][C][Hq][d] over KV heads in pairs -> out
+    [B][C][Hq / 2][2 d], causal; the weights as decode_diff, the rest as
+    prefill_chunk."""
+    desc = pool_desc(pool, layer)
+    B, C, Hq, d = q.shape
+    if d != desc.head_dim or Hq % 2 or tuple(out.shape) != (B, C, Hq // 2, 2 * d):
+        raise ValueError("q must be [num_seqs][chunk][num_q_heads][head_dim] and out [..][num_q_heads / 2][2 head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or ctx_lens.numel() != B:
+        raise ValueError("block_tables / ctx_lens do not match the batch")
+    dev = torch.cuda.current_device()
+    if pool.get_device() != dev:
+        _refuse(pool, torch.bfloat16, "pool", dev)
+    weights = _diff(lam, norm_weight, eps, out_scale, keys, Hq, d, dev)
+    _check(lib().pa_prefill_diff(_at(out, torch.bfloat16, "out", dev), _at(q, torch.bfloat16, "q", dev),
+                                 ctypes.byref(desc), _at(block_tables, torch.int32, "block_tables", dev),
+                                 block_tables.shape[1], _at(ctx_lens, torch.int32, "ctx_lens", dev), B, C, Hq,
+                                 max_ctx_len, scale, ctypes.byref(weights), _handle(stream, dev)), "pa_prefill_diff")
 
 
 def beam_select_workspace_size(num_groups: int, num_beams: int, vocab: int, num_out: int) -> int:

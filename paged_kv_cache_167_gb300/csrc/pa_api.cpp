@@ -357,6 +357,38 @@ pa_status pa_decode_diff(void *out, const void *q, const pa_kv_pool *pool, const
     return launch_decode_diff(a, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+pa_status pa_prefill_diff(void *out, const void *q, const pa_kv_pool *pool, const int32_t *block_tables,
+                          int32_t max_blocks_per_seq, const int32_t *ctx_lens, int32_t num_seqs, int32_t chunk_len,
+                          int32_t num_q_heads, int32_t max_ctx_len, float scale, const pa_diff *diff,
+                          cudaStream_t stream) {
+    PoolView view;
+    pa_status st = resolve_pool(pool, &view);
+    if (st != PA_OK) return st;
+    if (num_seqs < 0 || chunk_len < 0 || num_q_heads <= 0 || max_ctx_len < 0 || !diff_ok(diff))
+        return PA_ERR_INVALID_ARG;
+    if (num_q_heads % view.num_kv_heads != 0 || view.num_kv_heads % 2 != 0) return PA_ERR_INVALID_ARG;
+    if (!prefill_diff_supported(view.head_dim, num_q_heads / view.num_kv_heads, view.block_size))
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || chunk_len == 0) return PA_OK;
+    if (num_seqs > 65535 || (int64_t)num_seqs * chunk_len > (int64_t)INT32_MAX) return PA_ERR_INVALID_ARG;
+    if (!out || !q || !block_tables || !ctx_lens || max_blocks_per_seq <= 0) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+    if ((int64_t)max_ctx_len + chunk_len > (int64_t)max_blocks_per_seq * view.block_size) return PA_ERR_INVALID_ARG;
+    PrefillArgs a;
+    a.out = out;
+    a.q = q;
+    a.pool = view;
+    a.tables = block_tables;
+    a.max_blocks = max_blocks_per_seq;
+    a.ctx_lens = ctx_lens;
+    a.num_seqs = num_seqs;
+    a.chunk_len = chunk_len;
+    a.num_q_heads = num_q_heads;
+    a.max_ctx_len = max_ctx_len;
+    a.scale = scale;
+    return launch_prefill_diff(a, *diff, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 pa_status pa_copy_blocks(const pa_kv_pool *pool, const int32_t *pairs, int32_t num_pairs, cudaStream_t stream) {
     PoolView view;
     pa_status st = resolve_pool(pool, &view);

@@ -187,5 +187,10 @@ struct PrefillArgs {
 bool prefill_supported(int head_dim, int group, int block_size);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
 void set_prefill_ctas(int32_t ctas);   // 0: one CTA per SM
+int32_t prefill_ctas();
+
+// ---- differential prefill (pa_prefill_diff.cu) -------------------------------
+bool prefill_diff_supported(int head_dim, int pairs, int block_size);
+cudaError_t launch_prefill_diff(const PrefillArgs &a, const pa_diff &diff, cudaStream_t stream);
 
 }  // namespace pa

@@ -63,25 +63,12 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "pa_device.cuh"
-#include "pa_internal.h"
+#include "pa_prefill_common.cuh"
 
 namespace pa {
 namespace prefill {
 
-constexpr int kSoftWarps = 8;               // softmax warps: two per TMEM lane quadrant
-constexpr int kParts = kSoftWarps / 4;      // warps sharing a row: each owns kPK of its 128 keys
-constexpr int kPK = 128 / kParts;           // keys of a row per softmax thread (64)
-constexpr int kPC = kPK / 32;               // 32-column TMEM accesses per thread and tile
-constexpr int kMmaWarp = kSoftWarps;        // lane 0 issues the P.V MMAs
-constexpr int kKWarp = kSoftWarps + 1;      // copies Q and the K tiles
-constexpr int kVWarp = kSoftWarps + 2;      // copies the V tiles
-constexpr int kQkWarp = kSoftWarps + 3;     // lane 0 issues the Q.K MMAs
-constexpr int kThreads = (kSoftWarps + 4) * 32;
-constexpr int kRows = 128;                  // M tile
-constexpr int kKeys = 128;                  // N tile of Q.K (keys per iteration)
 constexpr int kD = 128;                     // head_dim
-constexpr uint32_t kHalf = 128u * 128u;     // one [128 rows][64 bf16] swizzled half tile, bytes
 constexpr uint32_t kTile = 2u * kHalf;      // [2 halves][128 rows][128 B]
 constexpr uint32_t kOffQ = 0;               // two Q buffers (a unit's Q lands while the previous one finishes)
 #ifndef PA_PREFILL_KV_STAGES
@@ -98,9 +85,6 @@ constexpr uint32_t kOffUnits = kOffX + (uint32_t)kParts * 128u * 12u;
 constexpr uint32_t kSmemBytes = kOffUnits + kMaxUnits * 8 + 1024;   // + alignment slack
 constexpr int kSBufs = 2;                   // S accumulators in tensor memory
 constexpr uint32_t kTmemCols = 512;         // S0, S1, O0, O1 (128 columns each)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;   // log2 domain
 #ifndef PA_PREFILL_PRECISE_KEYS
 #define PA_PREFILL_PRECISE_KEYS 512
 #endif
@@ -145,192 +129,6 @@ struct Params {
     int64_t kv_stride;
 };
 
-
-// ---- PTX wrappers -----------------------------------------------------------
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                            uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-        : "memory");
-}
-
-// Shared -> global copy of one box of a 4-D tensor map at (c0 .. c3), in this
-// thread's current bulk group (coordinates >= 0, c0 * 2 B a multiple of 16 B).
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, int c0, int c1, int c2, int c3, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// this thread's bulk stores have finished reading shared memory / have completed
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// Hint: bring one box of a 4-D tensor map at (c0 .. c3) into L2 (changes no
-// data and orders nothing, so it may run before the data's writer finishes).
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, int c2, int c3) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(c0),
-                 "r"(c1), "r"(c2), "r"(c3)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                            int c4, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5, %6}], [%7];" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned int *err) {
-    return mbar_wait_bounded(reinterpret_cast<uint64_t *>(__cvta_shared_to_generic(bar)), parity, err);
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Shared-memory matrix descriptor: 128-byte swizzle, descriptor version 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-
-// Instruction descriptor, kind::f16: fp32 accumulate, bf16 A and B, A K-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool b_mn_major) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
-           ((uint32_t)(m >> 4) << 24);
-}
-
-__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
-// A operand from tensor memory (M rows in lanes, K along columns, two bf16 per column).
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-#define PA_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
-                 "=r"(r[i + 6]), "=r"(r[i + 7])
-#define PA_W8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
-                 "r"(r[i + 6]), "r"(r[i + 7])
-
-// 32 consecutive fp32 columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : PA_R8(0), PA_R8(8), PA_R8(16), PA_R8(24)
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        PA_W8(0), PA_W8(8), PA_W8(16), PA_W8(24)
-        : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[N]) {   // r[0..15]
-    static_assert(N >= 16, "16 words");
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16};" ::"r"(taddr),
-        PA_W8(0), PA_W8(8)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// ---- the kernel ---------------------------------------------------------------
-
-__device__ __forceinline__ void mbar_arrive_u32(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Tensor-memory column of keys kk*16 .. kk*16+15 of P in S buffer sb: each
-// part of a row's keys is written, two bf16 per column, by the warp that read
-// it, into the first half of the S columns it read.
-__device__ __forceinline__ uint32_t p_col(int sb, int kk) {
-    constexpr int kSteps = kPK / 16;   // 16-key P.V steps per softmax thread
-    return (uint32_t)(sb * 128 + (kk / kSteps) * kPK + (kk % kSteps) * 8);
-}
-
-__device__ __forceinline__ void part_sync(int warp) {   // warps w, w + 4, ... own the same rows
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp & 3)), "r"(kParts * 32) : "memory");
-}
-
-__device__ __forceinline__ void soft_sync() {   // all softmax warps
-    asm volatile("bar.sync 5, %0;" ::"n"(kSoftWarps * 32) : "memory");
-}
-
-__device__ __forceinline__ float max_tree32(const uint32_t (&a)[32]) {
-    float m[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m[i] = fmaxf(__uint_as_float(a[i]), __uint_as_float(a[i + 16]));
-#pragma unroll
-    for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-        for (int i = 0; i < w; ++i) m[i] = fmaxf(m[i], m[i + w]);
-    return m[0];
-}
-
-// Three-input maximum (one instruction on sm_100 and later).
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// Maximum of 64 values by three-input steps: 64 -> 22 -> 8 -> 4 -> 2 -> 1
-// (32 instructions, five deep, against 63 and six with two-input steps).
-__device__ __forceinline__ float max_tree64(const uint32_t (&a)[32], const uint32_t (&b)[32]) {
-    float v[64];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        v[i] = __uint_as_float(a[i]);
-        v[32 + i] = __uint_as_float(b[i]);
-    }
-    float m1[22];
-#pragma unroll
-    for (int i = 0; i < 21; ++i) m1[i] = max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
-    m1[21] = v[63];
-    float m2[8];
-#pragma unroll
-    for (int i = 0; i < 7; ++i) m2[i] = max3(m1[3 * i], m1[3 * i + 1], m1[3 * i + 2]);
-    m2[7] = m1[21];
-    const float x = max3(m2[0], m2[1], m2[2]), y = max3(m2[3], m2[4], m2[5]);
-    return fmaxf(max3(x, y, m2[6]), m2[7]);
-}
 
 // Work units: one (M-tile mt, kv-head g, sequence slot z) each, numbered
 // u = mt + num_mt * (g + num_kv * z).  The grid is persistent (one CTA per SM
@@ -1207,6 +1005,8 @@ cudaError_t launch_group(const PrefillArgs &a, const CUtensorMap &mq, const CUte
 }
 
 }  // namespace prefill
+
+int32_t prefill_ctas() { return prefill::g_prefill_ctas.load(std::memory_order_relaxed); }
 
 void set_prefill_ctas(int32_t ctas) { prefill::g_prefill_ctas.store(ctas, std::memory_order_relaxed); }
 

@@ -1,0 +1,867 @@
+// pa_prefill_diff.cu -- differential attention of a chunk of prompt tokens against
+// the paged context, on the tcgen05 tensor cores (sm_103a).
+//
+// The mathematics (pa_decode_diff.cuh): pair g of KV heads has keys K1, K2 and one
+// value row V = [V_2g | V_2g+1] of 2d components; query pair h computes
+//     x_h = softmax(s q_2h K1^T) V - lambda_h softmax(s q_2h+1 K2^T) V
+// for each query j over keys 0 .. ctx + j, then (optionally) the norm of the row.
+//
+// Why a cluster of two CTAs: one map of a 128-row tile holds 128 x 2d fp32 sums, half
+// of an SM's tensor memory at d = 128; with two score tiles beside it the other half
+// is gone as well, so the two maps cannot share an SM.  CTA r of a cluster runs map r
+// as an attention of its own (scores 128 x 128 x d, products 128 x 2d x 128: with
+// values twice as wide the tensor cores have one and a half times the work a score
+// that plain attention has, against one exponential).  The maps meet once a unit:
+// each CTA finishes one half of the 2d columns, so it sends the other half of its own
+// map, divided by the row's sum and weighted, to the other CTA through distributed
+// shared memory (fp32: the difference and the norm lose nothing before the one
+// rounding to bf16), a quarter at a time into the unit's query tile, which nothing
+// reads any more.
+//
+// Design, as far as it is not pa_prefill.cu's:
+//  * A unit is an M-tile of 128 rows (query j0 + r / G, pair r % G of the G query
+//    pairs that share their keys), one KV pair and one sequence; the grid is
+//    persistent, clusters walking units in rounds of alternating direction.
+//  * Rows' keys 0-63 and 64-127 belong to two threads of different warps, which share
+//    one accumulator, so they agree on the reference maximum: each writes its own
+//    maximum of the tile to shared memory and a barrier of the two warps makes both
+//    take the larger.  The reference moves only when it is exceeded by 8 (log2).
+//  * Shared memory (d = 128): two query tiles 64 KB, two key tiles 64 KB, three half
+//    value tiles of 64 keys 96 KB.  Value tiles in halves, because two whole ones
+//    (128 KB) would leave one query tile, and a unit's start would wait for its copy.
+//  * A wait that another CTA's threads complete acquires at cluster scope; all waits
+//    are bounded, and both CTAs meet at the end before either's shared memory goes.
+#include <algorithm>
+#include <type_traits>
+
+#include "pa_prefill_common.cuh"
+
+namespace pa {
+namespace prefill {
+namespace {
+
+struct DiffParams {
+    __nv_bfloat16 *out;          // [B][C][pairs][2 DH]
+    const int32_t *tables;
+    int32_t max_blocks;
+    const int32_t *ctx_lens;
+    int32_t max_ctx_len;
+    int32_t chunk;
+    int32_t num_pairs;           // query pairs of a token
+    int64_t num_blocks;
+    float scale_log2;
+    unsigned int *err;
+    int32_t num_mt;              // M-tiles per sequence
+    int32_t num_kv;              // groups of G query pairs
+    int32_t num_seqs;
+    int32_t by_head;             // group u reads key head u for both maps, values of pair u / 2
+    const float *lambda;         // [pairs]
+    const float *norm_weight;    // [2 DH] or nullptr
+    float eps, out_scale;
+};
+
+template <int DH>
+struct DiffSmem {
+    static constexpr int kHalves = DH / 64;                      // 64-wide halves of a head
+    static constexpr uint32_t kQTile = kHalves * kHalf;          // [half][128 rows][128 B]
+    static constexpr uint32_t kKTile = kHalves * kHalf;          // [half][128 keys][128 B]
+    static constexpr uint32_t kVHalf = 64u * 2u * DH * 2u;       // 64 keys: [block][head][half][BS][128 B]
+    static constexpr int kVSlots = 3;
+    static constexpr uint32_t kOffQ = 0;
+    static constexpr uint32_t kOffK = kOffQ + 2 * kQTile;
+    static constexpr uint32_t kOffV = kOffK + 2 * kKTile;
+    static constexpr uint32_t kOffX = kOffV + kVSlots * kVHalf;  // float [2][2][128]: see mx
+    static constexpr uint32_t kOffBar = kOffX + 2048;
+    static constexpr uint32_t kBytes = kOffBar + 384;
+    static_assert(kBytes <= 232448, "shared memory");
+};
+
+// ---- cluster ------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The other CTA's address of this CTA's shared-memory address.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {   // a shared::cluster address
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(hint_ns)
+        : "memory");
+    return ok != 0;
+}
+// As mbar_wait, for a phase that threads of the other CTA complete.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, unsigned int *err) {
+    if (try_wait_cluster(bar, parity, 0u)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (try_wait_cluster(bar, parity, 20000u)) return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            raise_error(err, PA_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Named barriers whose threads all learn whether any of them saw `mine`: the two warps
+// of the same rows, and all softmax warps.  A warp that gives up alone would leave the
+// others waiting for it, and these barriers have no limit; so giving up is decided
+// here, by everyone alike.
+__device__ __forceinline__ bool barrier_or(int id, int threads, bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)mine), "r"(id), "r"(threads)
+        : "memory");
+    return any != 0;
+}
+__device__ __forceinline__ bool part_or(int warp, bool mine) { return barrier_or(1 + (warp & 3), kParts * 32, mine); }
+__device__ __forceinline__ bool soft_or(bool mine) { return barrier_or(5, kSoftWarps * 32, mine); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : PA_R8(0), PA_R8(8)
+        : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 32) tmem_ld32(taddr, r);
+    else tmem_ld16(taddr, r);
+}
+
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+// ---- the kernel -----------------------------------------------------------------
+
+// Barriers, as in pa_prefill.cu unless noted: Q landed[2], K landed[2], V half
+// landed[3], S ready[2], P ready[2], P.V done[2], P.V done per S buffer[2], K slot
+// free[2], V half free[3], Q free[2], unit's P.V done, O read, the two MMA lanes'
+// drains; then, completed by the other CTA: go[8] (its warp of the same index may be
+// written to), full[8] (its data has landed), norm[4] (both CTAs' partial sums of
+// squares of a lane quadrant's rows).
+// The tiles of the CTA's units are numbered T = 0, 1, ...; its value halves H = 2T, 2T + 1.
+template <int DH, int G, int BS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefill_diff_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                        const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
+                        const DiffParams p) {
+    using SM = DiffSmem<DH>;
+    constexpr int QPT = kRows / G;                 // queries per M-tile
+    constexpr int DV = 2 * DH;                     // value components
+    constexpr int NBK = kKeys / BS;                // blocks of a key tile
+    constexpr int NBV = 64 / BS;                   // blocks of half a value tile
+    constexpr int kVS = SM::kVSlots;
+    constexpr uint32_t kVBlock = (uint32_t)(DV / 64) * BS * 128u;   // one block's V box
+    constexpr uint32_t kTmem = 512;                // S0, S1, O
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t base = smem_addr(smem_raw);
+    const uint32_t sQ = base + SM::kOffQ, sK = base + SM::kOffK, sV = base + SM::kOffV;
+    const uint32_t barQ = base + SM::kOffBar, barK = barQ + 16, barV = barK + 16, barS = barV + 8 * kVS,
+                   barP = barS + 16, barOP = barP + 16, barSdone = barOP + 16, barKfree = barSdone + 16,
+                   barVfree = barKfree + 16, barQfree = barVfree + 8 * kVS, barUnit = barQfree + 16,
+                   barOfree = barUnit + 8, barEnd = barOfree + 8, barEndQk = barEnd + 8, barGo = barEndQk + 8,
+                   barFull = barGo + 64, barNorm = barFull + 64;
+    constexpr int kNumBars = 2 + 2 + kVS + 2 + 2 + 2 + 2 + 2 + kVS + 2 + 1 + 1 + 1 + 1 + 8 + 8 + 4;
+    static_assert(8 * kNumBars + 8 <= 384, "barrier area");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + SM::kOffBar + 8 * kNumBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem_raw + SM::kOffBar + 8 * kNumBars + 4);
+    // The halves' maxima of a tile ([tile parity][half][row]), in the epilogue their
+    // sums, then the four partial sums of squares of a row ([2 * CTA + half][row]).
+    float *mx = reinterpret_cast<float *>(smem_raw + SM::kOffX);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kNumBars; ++i) {
+            const uint32_t b = barQ + 8 * i;
+            uint32_t count = 1;
+            if ((b >= barP && b < barOP) || b == barOfree) count = kSoftWarps * 32;
+            if (b >= barQfree && b < barUnit) count = 2;     // the Q.K lane's commit and the epilogue's release
+            if (b >= barGo && b < barNorm) count = 32;       // the other CTA's warp
+            if (b >= barNorm) count = 128;                   // the four warps that share the rows
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(count) : "memory");
+        }
+        // the tiles' swizzle wants 1,024-byte alignment, which dynamic shared memory
+        // has where nothing static lies before it; checked, not assumed
+        *abort_flag = (base & 1023u) != 0 ? 1 : 0;
+        if ((base & 1023u) != 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();        // both CTAs' barriers are set up before either arrives on the other's
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tO = tmem + 256;
+    const bool usable = *abort_flag == 0;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- this cluster's units
+    const int C = (int)gridDim.x / 2, cl = (int)blockIdx.x / 2;
+    const int per_seq = p.num_mt * p.num_kv;
+    const int n_units = usable ? per_seq * p.num_seqs : 0;
+    auto unit_index = [&](int k) { return k * C + ((k & 1) ? C - 1 - cl : cl); };
+    const int rounds = (n_units + C - 1) / C;
+    const int my_units = rounds > 0 ? rounds - 1 + (unit_index(rounds - 1) < n_units ? 1 : 0) : 0;
+    struct Unit {
+        int s, g, j0, ctx, seq_end, nblk, n_tiles;
+    };
+    auto unit = [&](int k) {
+        Unit U;
+        const int u = unit_index(k);
+        U.s = u / per_seq;
+        U.g = (u / p.num_mt) % p.num_kv;
+        U.j0 = (p.num_mt - 1 - u % p.num_mt) * QPT;     // the longest rows first
+        int ctx = __ldg(p.ctx_lens + U.s);
+        if (ctx < 0 || ctx > p.max_ctx_len) {
+            raise_error(p.err, PA_DEVERR_SEQ_LEN);
+            ctx = ctx < 0 ? 0 : p.max_ctx_len;
+        }
+        U.ctx = ctx;
+        U.seq_end = ctx + p.chunk;
+        U.nblk = (U.seq_end + BS - 1) / BS;
+        const int last_q = min(U.j0 + QPT, p.chunk) - 1;
+        U.n_tiles = (ctx + last_q + 1 + kKeys - 1) / kKeys;    // at least one
+        return U;
+    };
+    constexpr uint32_t idesc_qk = idesc_bf16(kRows, kKeys, false);
+    constexpr uint32_t idesc_pv = idesc_bf16(kRows, DV, true);
+
+    if (warp == kKWarp || warp == kVWarp) {
+        // ---- copy warps: a lane per box, block ids in registers a load of 32 ahead.  The
+        // K warp copies tiles of NBK blocks, the V warp halves of NBV.
+        const bool is_k = warp == kKWarp;
+        const int nb = is_k ? NBK : NBV, per_tile = is_k ? 1 : 2, spl = 32 / nb, slots = is_k ? 2 : kVS;
+        const uint32_t bar0 = is_k ? barK : barV, free0 = is_k ? barKfree : barVfree;
+        auto ids_load = [&](const Unit &U, int c) -> int {
+            const int bi = c * 32 + lane;
+            return bi < U.nblk && bi < U.n_tiles * NBK ? __ldg(p.tables + (size_t)U.s * p.max_blocks + bi) : 0;
+        };
+        auto ids_check = [&](int v, const Unit &U, int c) -> int {   // out-of-bounds coordinate: zero fill
+            const int bi = c * 32 + lane;
+            if (!(bi < U.nblk && bi < U.n_tiles * NBK)) return (int)p.num_blocks;
+            if (v < 0 || v >= p.num_blocks) {
+                raise_error(p.err, PA_DEVERR_BLOCK_ID);
+                return (int)p.num_blocks;
+            }
+            return v;
+        };
+        bool ok = true;
+        int N = 0;      // tiles or halves issued so far
+        int nq = 0;     // query tiles issued (K warp)
+        Unit U;
+        int raw_cur = 0, raw_next = 0;
+        if (my_units > 0) {
+            U = unit(0);
+            raw_cur = ids_load(U, 0);
+            raw_next = ids_load(U, 1);
+        }
+        for (int k = 0; k < my_units && ok; ++k) {
+            Unit X = U;            // the next unit, and its first ids
+            int nraw_cur = 0, nraw_next = 0;
+            if (k + 1 < my_units) {
+                X = unit(k + 1);
+                nraw_cur = ids_load(X, 0);
+                nraw_next = ids_load(X, 1);
+            }
+            if (is_k) {
+                // Q buffer k % 2 held unit k - 2's Q, its exchange and its output tile
+                const int qb = k & 1;
+                if (k >= 2)
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(barQfree + 8 * qb, (uint32_t)(((k >> 1) - 1) & 1), p.err));
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                nq = k + 1;
+                if (lane == 0) mbar_expect(barQ + 8 * qb, SM::kQTile);
+                __syncwarp();
+                if (lane < SM::kHalves)
+                    tma_load_5d(sQ + qb * SM::kQTile + lane * kHalf, &tmap_q, lane * 64, (int)rank, 0, U.g,
+                                U.s * p.chunk + U.j0, barQ + 8 * qb);
+            }
+            const int key_head = p.by_head ? U.g : 2 * U.g + (int)rank;
+            const int value_head = p.by_head ? (U.g >> 1) * 2 : 2 * U.g;
+            int ids_cur = ids_check(raw_cur, U, 0);
+            const int steps = U.n_tiles * per_tile;
+            for (int t = 0; t < steps; ++t, ++N) {
+                if (*abort_flag) {
+                    ok = false;
+                    break;
+                }
+                if (t > 0 && t % spl == 0) {
+                    ids_cur = ids_check(raw_next, U, t / spl);
+                    raw_next = ids_load(U, t / spl + 1);
+                }
+                const int tb = (t % spl) * nb, st = N % slots;
+                const int blk = is_k ? __shfl_sync(0xffffffffu, ids_cur, (tb + lane / SM::kHalves) & 31)
+                                     : __shfl_sync(0xffffffffu, ids_cur, (tb + lane) & 31);
+                if (N >= slots) {   // the slot's previous tile has been consumed by its MMAs
+                    const int np = N - slots;
+                    ok = __all_sync(0xffffffffu, mbar_wait(free0 + 8 * (np % slots), (uint32_t)((np / slots) & 1),
+                                                           p.err));
+                    if (!ok) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                }
+                if (lane == 0) mbar_expect(bar0 + 8 * st, is_k ? SM::kKTile : SM::kVHalf);
+                __syncwarp();
+                if (is_k) {
+                    const int b = lane / SM::kHalves, h = lane % SM::kHalves;
+                    if (b < NBK)
+                        tma_load_5d(sK + st * SM::kKTile + h * kHalf + b * (BS * 128), &tmap_k, h * 64, 0, key_head, 0,
+                                    blk, bar0 + 8 * st);
+                } else if (lane < NBV) {
+                    tma_load_5d(sV + st * SM::kVHalf + lane * kVBlock, &tmap_v, 0, 0, 0, value_head, blk,
+                                bar0 + 8 * st);
+                }
+            }
+            U = X;
+            raw_cur = nraw_cur;
+            raw_next = nraw_next;
+        }
+        if (!ok || *abort_flag) {
+            // wait (bounded) for this warp's copies still in flight before the memory is released
+            for (int t = max(0, N - slots); t < N; ++t)
+                mbar_wait(bar0 + 8 * (t % slots), (uint32_t)((t / slots) & 1), p.err);
+            for (int k = max(0, nq - 2); k < nq; ++k) mbar_wait(barQ + 8 * (k & 1), (uint32_t)((k >> 1) & 1), p.err);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp || warp == kQkWarp) {
+        // ---- two issuing lanes, as in pa_prefill.cu
+        if (lane == 0) {
+            const bool is_qk = warp == kQkWarp;
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (ok && !mbar_wait(bar, parity, p.err)) {
+                    ok = false;
+                    *abort_flag = 1;
+                }
+                return ok;
+            };
+            int T = 0;
+            for (int k = 0; k < my_units && ok && !*abort_flag; ++k) {
+                const Unit U = unit(k);
+                if (is_qk) {
+                    const int qb = k & 1;
+                    if (!wait(barQ + 8 * qb, (uint32_t)((k >> 1) & 1))) break;
+                    const uint32_t sQb = sQ + qb * SM::kQTile;
+                    for (int t = 0; t < U.n_tiles; ++t, ++T) {
+                        if (*abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                        const int st = T & 1;      // K slot and S buffer
+                        if (!wait(barK + 8 * st, (uint32_t)((T >> 1) & 1))) break;
+                        // S buffer st held P(T - 2): its P.V must have completed
+                        if (T >= 2 && !wait(barSdone + 8 * st, (uint32_t)(((T - 2) >> 1) & 1))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < DH / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+                            umma(tmem + st * 128, smem_desc(sQb + off, 16, 1024),
+                                 smem_desc(sK + st * SM::kKTile + off, 16, 1024), idesc_qk, kk > 0);
+                        }
+                        umma_commit(barS + 8 * st);
+                        umma_commit(barKfree + 8 * st);
+                    }
+                    if (!ok) break;
+                    umma_commit(barQfree + 8 * qb);
+                } else {
+                    // O is overwritten by this unit's first P.V: the previous unit's epilogue has read it
+                    if (k > 0 && !wait(barOfree, (uint32_t)((k - 1) & 1))) break;
+                    for (int t = 0; t < U.n_tiles; ++t, ++T) {
+                        if (*abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                        if (!wait(barP + 8 * (T & 1), (uint32_t)((T >> 1) & 1))) break;
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int H = 2 * T + hf, st = H % kVS;
+                            if (!wait(barV + 8 * st, (uint32_t)((H / kVS) & 1))) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                // 16 keys: within one block for b >= 16 (8-key groups 1024 B apart), or
+                                // two whole blocks for b = 8 (groups one block apart)
+                                const uint32_t v_off =
+                                    (uint32_t)(kk * 16 / BS) * kVBlock + (uint32_t)((kk * 16) % BS) * 128u;
+                                umma_ts(tO, tmem + p_col(T & 1, hf * 4 + kk),
+                                        smem_desc(sV + st * SM::kVHalf + v_off, BS * 128, BS >= 16 ? 1024 : kVBlock),
+                                        idesc_pv, (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
+                            }
+                            umma_commit(barVfree + 8 * st);
+                        }
+                        if (!ok) break;
+                        umma_commit(barOP + 8 * (T & 1));
+                        umma_commit(barSdone + 8 * (T & 1));
+                    }
+                    if (!ok) break;
+                    umma_commit(barUnit);   // every P.V of the unit has completed
+                }
+            }
+            // one more commit, on a barrier used once, tracks every MMA this lane issued
+            if (!ok || *abort_flag) *abort_flag = 1;   // give up: drain what was issued
+            const uint32_t end = is_qk ? barEndQk : barEnd;
+            umma_commit(end);
+            mbar_wait(end, 0, p.err);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax warps: row r, key half pt (scale_log2 > 0: maxima of raw scores)
+        const int r = (warp & 3) * 32 + lane, pt = warp >> 2;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const float c = p.scale_log2;
+        const uint32_t other = rank ^ 1u;
+        // thread 0: the Q buffer whose release it owes once the tensor store of the output
+        // tile staged there has read it (-1: none)
+        int q_owed = -1;
+        auto release = [&]() {
+            bulk_wait_read();
+            mbar_arrive_u32(barQfree + 8 * q_owed);
+            q_owed = -1;
+        };
+        int T = 0;
+        for (int k = 0; k < my_units; ++k) {
+            const Unit U = unit(k);
+            const int jr = U.j0 + r / G;
+            const int pos = min(U.ctx + jr, U.seq_end - 1);   // last key this row may attend
+            const int pair = U.g * G + r % G;
+            const float lam = rank == 0 ? 1.f : -__ldg(p.lambda + pair);
+            float m_ref = -INFINITY;                          // reference maximum, log2 domain
+            float l = 0.f;                                    // of this thread's keys
+            int done = 0;
+            for (int t = 0; t < U.n_tiles; ++t, ++T) {
+                const int sb = T & 1;
+                bool ok = mbar_wait(barS + 8 * sb, (uint32_t)((T >> 1) & 1), p.err);
+                if (t == 1 && tid == 0 && q_owed >= 0) release();
+                uint32_t sr[kPC][32];
+                if (__all_sync(0xffffffffu, ok)) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int cc = 0; cc < kPC; ++cc) tmem_ld32(tmem + sb * 128 + lane_off + pt * kPK + cc * 32, sr[cc]);
+                    tmem_ld_wait();
+                } else {
+                    ok = false;
+                }
+                const int key0 = t * kKeys + pt * kPK;
+                if (!__all_sync(0xffffffffu, key0 + kPK - 1 <= pos)) {   // tile crosses some row's causal edge
+#pragma unroll
+                    for (int cc = 0; cc < kPC; ++cc)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (key0 + cc * 32 + i > pos) sr[cc][i] = __float_as_uint(-INFINITY);
+                }
+                // the row's maximum of the tile: both halves, so that both move alike
+                const float mine = max_tree64(sr[0], sr[1]);
+                mx[(sb * 2 + pt) * 128 + r] = mine;
+                if (part_or(warp, !ok || *abort_flag)) {   // give up
+                    *abort_flag = 1;
+                    mbar_arrive_u32(barP + 8 * sb);   // keep the arrival count balanced
+                    break;
+                }
+                const float mh = fmaxf(mine, mx[(sb * 2 + (pt ^ 1)) * 128 + r]);
+                const float mt_ = mh * c;
+                float alpha = 1.f;
+                if (mt_ > m_ref + kRescaleThreshold || (m_ref == -INFINITY && mt_ != -INFINITY)) {
+                    alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - mt_);
+                    m_ref = mt_;
+                }
+                const float2 c2 = make_float2(c, c);
+                const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                const float2 nm2 = make_float2(nm, nm);
+                float2 ps2 = make_float2(0.f, 0.f), ps2b = make_float2(0.f, 0.f);
+                uint32_t pw[32];
+#pragma unroll
+                for (int cc = 0; cc < kPC; ++cc) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = __ffma2_rn(
+                            make_float2(__uint_as_float(sr[cc][2 * e]), __uint_as_float(sr[cc][2 * e + 1])), c2, nm2);
+                        const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        if (e & 1) ps2b = __fadd2_rn(ps2b, pe);
+                        else ps2 = __fadd2_rn(ps2, pe);
+                        pw[cc * 16 + e] = pack_bf16x2(pe.x, pe.y);
+                    }
+                }
+                // P as bf16 into the S columns read above; each probability one term (with
+                // few keys the plain kernel's grouped form takes two; a prompt's rows see many)
+                tmem_st32(tmem + sb * 128 + lane_off + pt * kPK, pw);
+                tmem_st_wait();
+                ps2 = __fadd2_rn(ps2, ps2b);
+                l = l * alpha + (ps2.x + ps2.y);
+                // rescale this thread's half of the accumulator's columns once P.V(T - 1) has
+                // completed (its barrier's previous phase, P.V(T - 3), completed before Q.K(T - 1)
+                // was issued, which S(T - 1), read before this tile, needed)
+                if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    const int tp = T - 1;
+                    mbar_wait(barOP + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1), p.err);
+                    tc_fence_after();
+#pragma unroll
+                    for (int cc = 0; cc < DH / 32; ++cc) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + pt * DH + lane_off + cc * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(tO + pt * DH + lane_off + cc * 32, o);
+                    }
+                    tmem_st_wait();
+                }
+                // keys past the sequence end inside its last block: zero their V rows (their p is
+                // 0, but the slots may hold non-finite junk).  P.V(T - 1) is waited for first, so
+                // that the wait for the half's copy is exact: every half before tile T has then
+                // landed, and P.V(T) cannot take this one before P(T) is signalled below.
+                const int tail_lo = U.seq_end - t * kKeys;
+                if (tail_lo > 0 && tail_lo < kKeys && (U.seq_end % BS) != 0) {
+                    if (T > 0) {
+                        const int tp = T - 1;
+                        mbar_wait(barOP + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1), p.err);
+                    }
+                    const int H = 2 * T + tail_lo / 64, sv = H % kVS;
+                    mbar_wait(barV + 8 * sv, (uint32_t)((H / kVS) & 1), p.err);
+                    const int lo = tail_lo % 64, nrows = (BS - U.seq_end % BS);   // to the block's end
+                    constexpr int kChunks = DV / 8;                               // 16-byte chunks of a row
+                    for (int idx = tid; idx < nrows * kChunks; idx += kSoftWarps * 32) {
+                        const int rr = lo + idx / kChunks, c16 = idx % kChunks;
+                        const uint32_t addr = sV + sv * SM::kVHalf + (uint32_t)(rr / BS) * kVBlock +
+                                              (uint32_t)(c16 / 8) * (BS * 128u) + (uint32_t)(rr % BS) * 128u +
+                                              (uint32_t)(c16 % 8) * 16u;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                tc_fence_before();
+                mbar_arrive_u32(barP + 8 * sb);
+                done = t + 1;
+            }
+            // ---- epilogue.  The row's sum over both halves (the reference is one); -1: gave up
+            if (tid == 0 && q_owed >= 0) release();   // (units of one tile)
+            const bool fin = done == U.n_tiles && !*abort_flag && mbar_wait(barUnit, (uint32_t)(k & 1), p.err);
+            float *lx = mx + (T & 1) * 256;           // the parity that the last tile did not use
+            lx[pt * 128 + r] = fin ? l : -1.f;
+            part_sync(warp);
+            const float lo = lx[(pt ^ 1) * 128 + r];
+            part_sync(warp);                          // read, before squares are written there
+            bool ok = __all_sync(0xffffffffu, fin && lo != -1.f);   // the partner warp finds the same
+            const float lt = l + lo;
+            const float f = lt > 0.f ? lam / lt : 0.f;
+            tc_fence_after();
+            // ---- the maps meet: x = this CTA's half of the columns, a quarter of 2d at a time
+            const uint32_t sX = sQ + (uint32_t)(k & 1) * SM::kQTile;
+            const uint32_t mine_x = sX + (uint32_t)(pt * (DH / 16) * 128 + r) * 16u;   // chunk i: + i * 2048
+            const uint32_t peer_x = peer_addr(mine_x, other);
+            constexpr int W = DH / 4;                 // columns of a thread and quarter
+            float x[2][W];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!__all_sync(0xffffffffu, ok)) break;
+                const uint32_t ph = (uint32_t)((2 * k + q) & 1);
+                arrive_cluster(peer_addr(barGo + 8 * warp, other));    // this warp's place may be written
+                ok = ok && wait_cluster(barGo + 8 * warp, ph, p.err);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                {
+                    uint32_t o[W];
+                    tmem_ld<W>(tO + lane_off + other * DH + q * (DH / 2) + pt * W, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i)
+                        store_cluster(peer_x + i * 2048u, make_float4(__uint_as_float(o[4 * i]) * f,
+                                                                      __uint_as_float(o[4 * i + 1]) * f,
+                                                                      __uint_as_float(o[4 * i + 2]) * f,
+                                                                      __uint_as_float(o[4 * i + 3]) * f));
+                }
+                arrive_cluster(peer_addr(barFull + 8 * warp, other));
+                {
+                    uint32_t o[W];
+                    tmem_ld<W>(tO + lane_off + rank * DH + q * (DH / 2) + pt * W, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < W; ++i) x[q][i] = __uint_as_float(o[i]) * f;
+                }
+                ok = ok && wait_cluster(barFull + 8 * warp, ph, p.err);
+                if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i) {
+                    const float4 v = lds_f4(mine_x + i * 2048u);
+                    x[q][4 * i] += v.x;
+                    x[q][4 * i + 1] += v.y;
+                    x[q][4 * i + 2] += v.z;
+                    x[q][4 * i + 3] += v.w;
+                }
+            }
+            // O has been read: the next unit's first P.V may overwrite it
+            tc_fence_before();
+            mbar_arrive_u32(barOfree);
+            float scale = p.out_scale;
+            if (p.norm_weight != nullptr && __all_sync(0xffffffffu, ok)) {
+                float ss = 0.f;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) ss += x[q][i] * x[q][i];
+                const int at = (int)(2 * rank) + pt;
+                const uint32_t bar = barNorm + 8 * (warp & 3);
+                mx[at * 128 + r] = ss;
+                store_cluster(peer_addr(smem_addr(mx + at * 128 + r), other), ss);
+                arrive_cluster(peer_addr(bar, rank));
+                arrive_cluster(peer_addr(bar, other));
+                ok = wait_cluster(bar, (uint32_t)(k & 1), p.err);
+                ss = (mx[r] + mx[128 + r]) + (mx[256 + r] + mx[384 + r]);
+                scale *= rsqrtf(ss * (1.f / DV) + p.eps);
+            }
+            // every softmax thread has read the exchanged halves, sums and squares
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (soft_or(!ok)) {
+                *abort_flag = 1;
+                break;
+            }
+            // ---- this CTA's half of the row: staged for a tensor store, or written straight
+            const bool tma_out = U.j0 + min(QPT, p.chunk) <= p.chunk;
+            const bool row_ok = jr < p.chunk;
+            __nv_bfloat16 *dst =
+                p.out + (((size_t)U.s * p.chunk + jr) * p.num_pairs + pair) * DV + rank * DH;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c0 = q * (DH / 2) + pt * W;     // first column within the CTA's half
+#pragma unroll
+                for (int i8 = 0; i8 < W / 8; ++i8) {
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = x[q][i8 * 8 + e] * scale;
+                    if (p.norm_weight != nullptr) {
+                        const float4 *w4 =
+                            reinterpret_cast<const float4 *>(p.norm_weight + rank * DH + c0 + i8 * 8);
+                        const float4 wa = __ldg(w4), wb = __ldg(w4 + 1);
+                        y[0] *= wa.x;
+                        y[1] *= wa.y;
+                        y[2] *= wa.z;
+                        y[3] *= wa.w;
+                        y[4] *= wb.x;
+                        y[5] *= wb.y;
+                        y[6] *= wb.z;
+                        y[7] *= wb.w;
+                    }
+                    uint4 v;
+                    v.x = pack_bf16x2(y[0], y[1]);
+                    v.y = pack_bf16x2(y[2], y[3]);
+                    v.z = pack_bf16x2(y[4], y[5]);
+                    v.w = pack_bf16x2(y[6], y[7]);
+                    const int col = c0 + i8 * 8;
+                    if (tma_out) {
+                        // 16-byte chunk j of a 128-byte line goes to chunk j ^ (r % 8): the swizzle
+                        // that the tensor store undoes
+                        const uint32_t line = sX + (uint32_t)(col / 64) * kHalf + (uint32_t)r * 128u;
+                        const uint32_t c16 = (uint32_t)(col % 64) / 8;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line +
+                                                                                      ((c16 ^ ((uint32_t)r & 7u)) << 4)),
+                                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                     : "memory");
+                    } else if (row_ok) {
+                        *reinterpret_cast<uint4 *>(dst + col) = v;
+                    }
+                }
+            }
+            if (tma_out) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                soft_sync();
+                if (tid == 0) {
+#pragma unroll
+                    for (int h = 0; h < SM::kHalves; ++h)
+                        tma_store_4d(&tmap_o, (int)rank * DH + h * 64, 0, U.g, U.s * p.chunk + U.j0, sX + h * kHalf);
+                    bulk_commit();
+                    q_owed = k & 1;   // released once the stores have read it
+                }
+            } else if (tid == 0) {
+                mbar_arrive_u32(barQfree + 8 * (k & 1));
+            }
+        }
+        if (tid == 0) {   // no store may still read shared memory, or be in flight, when the CTA ends
+            if (q_owed >= 0) release();
+            bulk_wait_all();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();        // the other CTA may still write to this one's shared memory until here
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+    }
+}
+
+// ---- host side --------------------------------------------------------------------
+
+template <int DH, int G, int BS>
+cudaError_t launch_kernel(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
+                          const DiffParams &prm, cudaStream_t stream) {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && !configured[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(prefill_diff_kernel<DH, G, BS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DiffSmem<DH>::kBytes);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    const int64_t n_units = (int64_t)prm.num_mt * prm.num_kv * prm.num_seqs;
+    if (n_units == 0) return cudaSuccess;
+    if (n_units > INT32_MAX / 2) return cudaErrorInvalidValue;
+    int64_t clusters = prefill_ctas() / 2;
+    if (prefill_ctas() == 1) clusters = 1;
+    if (clusters <= 0) clusters = device_sm_count() / 2;
+    if (clusters <= 0) return cudaErrorUnknown;
+    clusters = std::min(clusters, n_units);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = DiffSmem<DH>::kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefill_diff_kernel<DH, G, BS>, mq, mk, mv, mo, prm);
+}
+
+bool encode_bf16(CUtensorMap *map, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+                 const cuuint32_t *box) {
+    auto encode = tensor_map_encoder();
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims,
+                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DH, int G>
+cudaError_t launch_pairs(const PrefillArgs &a, const pa_diff &diff, bool by_head, cudaStream_t stream) {
+    const int BS = a.pool.block_size, Hkv = a.pool.num_kv_heads, groups = by_head ? Hkv : Hkv / 2;
+    const cuuint64_t row = (cuuint64_t)a.num_q_heads * DH * 2, rows = (cuuint64_t)a.num_seqs * a.chunk_len;
+    CUtensorMap mq, mk, mv, mo;
+    {   // q as (d, map, pair in group, group, token); box one map of 128 / G tokens' pairs
+        const cuuint64_t dims[5] = {DH, 2, G, (cuuint64_t)groups, rows};
+        const cuuint64_t strides[4] = {DH * 2, 2 * DH * 2, (cuuint64_t)G * 2 * DH * 2, row};
+        const cuuint32_t box[5] = {64, 1, G, 1, kRows / G};
+        if (!encode_bf16(&mq, 5, a.q, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    {   // the output as (2d, pair in group, group, token); box a whole M-tile's queries, or all of them when fewer
+        const cuuint64_t dims[4] = {2 * DH, G, (cuuint64_t)groups, rows};
+        const cuuint64_t strides[3] = {2 * DH * 2, (cuuint64_t)G * 2 * DH * 2, row};
+        const cuuint32_t box[4] = {64, G, 1, (cuuint32_t)std::max(1, std::min(kRows / G, a.chunk_len))};
+        if (!encode_bf16(&mo, 4, a.out, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    {   // keys as (d, slot, kv-head, K|V, block); box one half of d of one head's block
+        const cuuint64_t dims[5] = {DH, (cuuint64_t)BS, (cuuint64_t)Hkv, 2, (cuuint64_t)a.pool.num_blocks};
+        const cuuint64_t strides[4] = {DH * 2, (cuuint64_t)BS * DH * 2, (cuuint64_t)a.pool.kv_stride * 2,
+                                       (cuuint64_t)a.pool.block_stride * 2};
+        const cuuint32_t box[5] = {64, (cuuint32_t)BS, 1, 1, 1};
+        if (!encode_bf16(&mk, 5, a.pool.base, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    // values: one box per block, both heads
+    if (encode_pool_block_map(&mv, a.pool, 1, BS, 2) != cudaSuccess) return cudaErrorInvalidValue;
+    DiffParams prm;
+    prm.out = static_cast<__nv_bfloat16 *>(a.out);
+    prm.tables = a.tables;
+    prm.max_blocks = a.max_blocks;
+    prm.ctx_lens = a.ctx_lens;
+    prm.max_ctx_len = a.max_ctx_len;
+    prm.chunk = a.chunk_len;
+    prm.num_pairs = a.num_q_heads / 2;
+    prm.num_blocks = a.pool.num_blocks;
+    prm.scale_log2 = a.scale * kLog2e;
+    prm.err = device_error_word();
+    if (!prm.err) return cudaErrorUnknown;
+    prm.num_mt = (a.chunk_len + kRows / G - 1) / (kRows / G);
+    prm.num_kv = groups;
+    prm.num_seqs = a.num_seqs;
+    prm.by_head = by_head ? 1 : 0;
+    prm.lambda = diff.lambda;
+    prm.norm_weight = diff.norm_weight;
+    prm.eps = diff.eps;
+    prm.out_scale = diff.out_scale;
+    switch (BS) {
+        case 8: return launch_kernel<DH, G, 8>(mq, mk, mv, mo, prm, stream);
+        case 16: return launch_kernel<DH, G, 16>(mq, mk, mv, mo, prm, stream);
+        case 32: return launch_kernel<DH, G, 32>(mq, mk, mv, mo, prm, stream);
+        case 64: return launch_kernel<DH, G, 64>(mq, mk, mv, mo, prm, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <int DH>
+cudaError_t launch_dim(const PrefillArgs &a, const pa_diff &diff, cudaStream_t stream) {
+    const int R = a.num_q_heads / a.pool.num_kv_heads;
+    // Keys by head: the R query heads of a key head are R / 2 whole pairs, both maps on
+    // the one key head.  With R = 1 it is what keys by map are.
+    const bool by_head = (diff.flags & PA_DIFF_KEYS_BY_HEAD) != 0 && R > 1;
+    switch (by_head ? R / 2 : R) {
+        case 1: return launch_pairs<DH, 1>(a, diff, by_head, stream);
+        case 2: return launch_pairs<DH, 2>(a, diff, by_head, stream);
+        case 4: return launch_pairs<DH, 4>(a, diff, by_head, stream);
+        case 8: return launch_pairs<DH, 8>(a, diff, by_head, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+}  // namespace prefill
+
+bool prefill_diff_supported(int head_dim, int pairs, int block_size) {
+    return (head_dim == 64 || head_dim == 128) && (pairs == 1 || pairs == 2 || pairs == 4 || pairs == 8) &&
+           (block_size == 8 || block_size == 16 || block_size == 32 || block_size == 64);
+}
+
+cudaError_t launch_prefill_diff(const PrefillArgs &a, const pa_diff &diff, cudaStream_t stream) {
+    return a.pool.head_dim == 64 ? prefill::launch_dim<64>(a, diff, stream)
+                                 : prefill::launch_dim<128>(a, diff, stream);
+}
+
+}  // namespace pa

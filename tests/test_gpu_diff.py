@@ -22,6 +22,7 @@ def pa():
     pa.get_device_error(clear=True)
     yield pa
     pa.set_stream_k_ctas(0)
+    pa.set_prefill_ctas(0)
 
 
 class Batch:
@@ -81,6 +82,21 @@ class Batch:
                        workspace=self.workspace(pa) if workspace is None else workspace, layer=self.layer,
                        **self.weights(), **kw)
         return out
+
+    def prefill(self, pa, **kw):
+        """The last `chunk` tokens of each sequence as queries, the others as context."""
+        ctx = [n - self.chunk for n in self.lens]
+        self.ctx_dev = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+        pa.prefill_diff(self.out, self.q, self.pool, self.tables, self.ctx_dev, max(ctx, default=0), self.scale,
+                        layer=self.layer, **self.weights(), **kw)
+        return self.out
+
+    def check_prefill(self, pa, what="", only=None):
+        for s in range(len(self.lens)) if only is None else only:
+            seen = self.lens[s] - self.chunk + 1 + torch.arange(self.chunk, device="cuda")
+            want, tol = self.want(s, seen)
+            dr.check(self.out[s], want, tol, f"{what} sequence {s}, {self.chunk} of {self.lens[s]} tokens")
+        assert pa.get_device_error() == 0
 
     def want(self, s, lens=None):
         """Of sequence s: the definition's output and the tolerance."""
@@ -256,4 +272,134 @@ def test_decode_diff_refusals_of_the_binding(pa):
         with pytest.raises(pa.PagedAttentionError) as e:
             pa.decode_diff(**{**good, **kw})
         assert e.value.status == status
+    assert pa.get_device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# chunks of prompt tokens
+# ---------------------------------------------------------------------------
+
+def chunked(ctx, chunk, *args, **kw):
+    return Batch([c + chunk for c in ctx], *args, chunk=chunk, **kw)
+
+
+@pytest.mark.parametrize("b", [8, 16, 32, 64])
+@pytest.mark.parametrize("per", [1, 2, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_diff(pa, d, per, b):
+    x = chunked([0, 1, 127, 300], 40, 2 * per, 2, d, b, seed=b + per, norm=per != 2)
+    x.prefill(pa)
+    x.check_prefill(pa, f"d={d} R={per} b={b}")
+
+
+@pytest.mark.parametrize("chunk", [1, 2, 15, 16, 17, 31, 64, 128, 129, 200, 333])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_diff_chunks(pa, d, chunk):
+    """Chunks from one token on, whole and partial tiles of queries."""
+    x = chunked([0, 63, 64, 65, 200], chunk, 8, 2, d, 16, seed=chunk)
+    x.prefill(pa)
+    x.check_prefill(pa)
+
+
+@pytest.mark.parametrize("per", [1, 2, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_diff_keys_by_head(pa, d, per):
+    for hkv in (2, 4):
+        x = chunked([0, 77], 150, hkv * per, hkv, d, 32, seed=per, layers=2, keys="head")
+        before = x.pool.clone()
+        x.prefill(pa)
+        x.check_prefill(pa)
+        assert np.array_equal(bits(x.pool), bits(before))
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 4, 6, 20, 152])
+def test_prefill_diff_hand_overs(pa, ctas):
+    """One cluster walking every unit, up to one a pair of SMs: units of one tile and of
+    many behind one another, with and without the norm's exchange."""
+    pa.set_prefill_ctas(ctas)
+    for d, per, norm in ((128, 4, True), (64, 1, True), (128, 1, False)):
+        x = chunked([0, 500, 3, 100], 70, 2 * per, 2, d, 16, seed=ctas, norm=norm)
+        x.prefill(pa)
+        x.check_prefill(pa, f"{ctas} CTAs")
+    pa.set_prefill_ctas(0)
+
+
+@pytest.mark.parametrize("d,per,ctx,chunk", [(128, 8, [4000, 17], 256), (64, 2, [9000], 100), (128, 1, [0], 3100),
+                                             (128, 4, [0] * 40, 33)])
+def test_prefill_diff_long_and_many(pa, d, per, ctx, chunk):
+    x = chunked(ctx, chunk, 2 * per, 2, d, 16, seed=21)
+    x.prefill(pa)
+    x.check_prefill(pa)
+
+
+@pytest.mark.parametrize("spread", [0.0, 25.0])
+def test_prefill_diff_flat_and_sharp(pa, spread):
+    """Equal logits, and maps that move their maximum often."""
+    x = chunked([700, 0], 130, 8, 2, 128, 16, seed=22, spread=spread)
+    x.prefill(pa)
+    x.check_prefill(pa)
+
+
+def test_prefill_diff_agrees_with_decode(pa):
+    """A chunk of one token is a decode step: both within the definition's bounds."""
+    x = chunked([300, 64, 0], 1, 16, 4, 128, 16, seed=23)
+    x.prefill(pa)
+    x.check_prefill(pa)
+    out = torch.empty((3, 8, 256), dtype=torch.bfloat16, device="cuda")
+    pa.decode_diff(out, x.q[:, 0].contiguous(), x.pool, x.tables, x.lens_dev, x.max_len, x.scale,
+                   workspace=x.workspace(pa), **x.weights())
+    for s in range(3):
+        want, tol = x.want(s, torch.tensor([x.lens[s]], device="cuda"))
+        dr.check(out[s:s + 1], want, tol, "decode")
+
+
+def test_prefill_diff_captured_and_concurrent(pa):
+    x, y = (chunked([200, 40], 130, 8, 2, 128, 16, seed=24 + i) for i in range(2))
+    x.prefill(pa)
+    graph = torch.cuda.CUDAGraph()
+    ctx = x.ctx_dev
+    with torch.cuda.graph(graph):
+        pa.prefill_diff(x.out, x.q, x.pool, x.tables, ctx, 200, x.scale, **x.weights())
+    x.q.neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    x.check_prefill(pa, "replayed")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    x.out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for one, stream in zip((x, y), streams):
+            pa.prefill_diff(one.out, one.q, one.pool, one.tables, ctx, 200, one.scale, stream=stream,
+                            **one.weights())
+    torch.cuda.synchronize()
+    x.check_prefill(pa, "two streams")
+    y.check_prefill(pa, "two streams")
+
+
+def test_prefill_diff_bad_pages(pa):
+    x = chunked([100, 50, 20], 30, 4, 2, 64, 16, seed=26)
+    x.tables[0, 2] = 10 ** 6
+    x.tables[0, 3] = -3
+    x.ctx_dev = torch.tensor([100, 5000, 20], dtype=torch.int32, device="cuda")
+    pa.prefill_diff(x.out, x.q, x.pool, x.tables, x.ctx_dev, 100, x.scale, **x.weights())
+    assert pa.get_device_error(clear=True) == 0x1 | 0x4
+    x.check_prefill(pa, only=[2])
+
+
+def test_prefill_diff_refusals_of_the_binding(pa):
+    x = chunked([20, 3], 5, 4, 2, 64, 16, seed=27)
+    x.prefill(pa)
+    good = dict(out=x.out, q=x.q, pool=x.pool, block_tables=x.tables, ctx_lens=x.ctx_dev, max_ctx_len=20,
+                scale=0.125, **x.weights())
+    for kw in (dict(out=x.out[:, :1]), dict(q=x.q[:, :, :3]), dict(lam=x.lam[:1]), dict(keys="both"),
+               dict(ctx_lens=x.ctx_dev[:1])):
+        with pytest.raises(ValueError):
+            pa.prefill_diff(**{**good, **kw})
+    for kw in (dict(lam=x.lam.double()), dict(q=x.q.float()), dict(ctx_lens=x.ctx_dev.cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            pa.prefill_diff(**{**good, **kw})
+    for kw in (dict(eps=-1.0), dict(scale=0.0), dict(max_ctx_len=4000)):
+        with pytest.raises(pa.PagedAttentionError) as e:
+            pa.prefill_diff(**{**good, **kw})
+        assert e.value.status == 1
     assert pa.get_device_error() == 0

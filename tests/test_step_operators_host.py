@@ -148,3 +148,26 @@ def test_decode_diff_more_refusals(B):
     assert _decode_diff(B, seqs=0) == 0 and _decode_diff(B, seqs=0, weight=None, eps=0.0) == 0
     pool = B.PaKvPool(FAKE, 64, 3, 16, 64, 0, 0, 0)
     assert B.lib().pa_decode_diff_workspace_size(ctypes.byref(pool), 4, 6, 100) == 0
+
+
+def _prefill_diff(B, hkv=2, hq=4, d=64, b=16, seqs=3, chunk=5, ctx=30, q=FAKE, lam=FAKE, eps=1e-5, scale=0.1,
+                  out_scale=1.0, dflags=0, diff=True):
+    pool = B.PaKvPool(FAKE, 64, hkv, b, d, 0, 0, 0)
+    weights = B.PaDiff(lam, FAKE, eps, out_scale, dflags)
+    return B.lib().pa_prefill_diff(FAKE, q, ctypes.byref(pool), FAKE, 4, FAKE, seqs, chunk, hq, ctx, scale,
+                                   ctypes.byref(weights) if diff else None, None)
+
+
+@pytest.mark.parametrize("kw", [dict(hkv=3, hq=3), dict(hq=5), dict(seqs=-1), dict(chunk=-1), dict(ctx=-1),
+                                dict(ctx=60), dict(q=None), dict(q=FAKE + 8), dict(lam=None), dict(eps=0.0),
+                                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(dflags=4),
+                                dict(out_scale=float("inf")), dict(diff=False), dict(seqs=65536),
+                                dict(hkv=-2, hq=4)])
+def test_prefill_diff_refusals(B, kw):
+    assert _prefill_diff(B, **kw) == INVALID
+
+
+def test_prefill_diff_more_refusals(B):
+    assert _prefill_diff(B, d=32) == UNSUPPORTED and _prefill_diff(B, b=4) == UNSUPPORTED
+    assert _prefill_diff(B, hq=6) == UNSUPPORTED and _prefill_diff(B, hq=32) == UNSUPPORTED
+    assert _prefill_diff(B, seqs=0) == 0 and _prefill_diff(B, chunk=0) == 0
