@@ -13,10 +13,12 @@
 // values twice as wide the tensor cores have one and a half times the work a score
 // that plain attention has, against one exponential).  The maps meet once a unit:
 // each CTA finishes one half of the 2d columns, so it sends the other half of its own
-// map, divided by the row's sum and weighted, to the other CTA through distributed
-// shared memory (fp32: the difference and the norm lose nothing before the one
-// rounding to bf16), a quarter at a time into the unit's query tile, which nothing
-// reads any more.
+// map, divided by the row's sum and weighted, to the other CTA: 64 KB of fp32 (the
+// difference and the norm lose nothing before the one rounding to bf16), stored
+// asynchronously into the unit's query tile and its last value slot there, which
+// nothing reads any more; the bytes themselves complete the receiver's barrier.  (With
+// plain remote stores and a release at cluster scope, in two rounds through the query
+// tile alone, this took 20,000 cycles a unit; MEASURED_EXCHANGE.)
 //
 // Design, as far as it is not pa_prefill.cu's:
 //  * A unit is an M-tile of 128 rows (query j0 + r / G, pair r % G of the G query
@@ -25,10 +27,17 @@
 //  * Rows' keys 0-63 and 64-127 belong to two threads of different warps, which share
 //    one accumulator, so they agree on the reference maximum: each writes its own
 //    maximum of the tile to shared memory and a barrier of the two warps makes both
-//    take the larger.  The reference moves only when it is exceeded by 8 (log2).
-//  * Shared memory (d = 128): two query tiles 64 KB, two key tiles 64 KB, three half
-//    value tiles of 64 keys 96 KB.  Value tiles in halves, because two whole ones
-//    (128 KB) would leave one query tile, and a unit's start would wait for its copy.
+//    take the larger.  The reference moves only when it is exceeded by 8 (log2).  P.V
+//    of a half starts when that half's probabilities are there.
+//  * Shared memory (d = 128): one query tile 32 KB, two key tiles 64 KB, four half value
+//    tiles of 64 keys 128 KB.  With three of them (and two query tiles) the second half
+//    of a product waited for its copy.  The query tile is free once a unit's last scores
+//    are there, so the next unit's is copied under the last products; the exchange and
+//    the output tile use the unit's last two value slots, and the warp that copies
+//    values stores the output from there before it fills them again.
+//  * Both maps multiply the same values: each CTA copies one head's half of them to both
+//    (multicast), which takes a third off what the SMs read from L2, 96 KB a tile and CTA
+//    without it (that read held a tile at 2,300 cycles; its products take 1,536).
 //  * A wait that another CTA's threads complete acquires at cluster scope; all waits
 //    are bounded, and both CTAs meet at the end before either's shared memory goes.
 #include <algorithm>
@@ -66,13 +75,14 @@ struct DiffSmem {
     static constexpr uint32_t kQTile = kHalves * kHalf;          // [half][128 rows][128 B]
     static constexpr uint32_t kKTile = kHalves * kHalf;          // [half][128 keys][128 B]
     static constexpr uint32_t kVHalf = 64u * 2u * DH * 2u;       // 64 keys: [block][head][half][BS][128 B]
-    static constexpr int kVSlots = 3;
+    static constexpr int kVSlots = 4;
     static constexpr uint32_t kOffQ = 0;
-    static constexpr uint32_t kOffK = kOffQ + 2 * kQTile;
+    static constexpr uint32_t kOffK = kOffQ + kQTile;
     static constexpr uint32_t kOffV = kOffK + 2 * kKTile;
     static constexpr uint32_t kOffX = kOffV + kVSlots * kVHalf;  // float [2][2][128]: see mx
     static constexpr uint32_t kOffBar = kOffX + 2048;
-    static constexpr uint32_t kBytes = kOffBar + 384;
+    static constexpr uint32_t kOffW = kOffBar + 384;             // float [DH]: this CTA's half of the norm's weights
+    static constexpr uint32_t kBytes = kOffW + DH * 4;
     static_assert(kBytes <= 232448, "shared memory");
 };
 
@@ -93,40 +103,70 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
     return a;
 }
+// Stores to the other CTA's shared memory that complete their bytes on its barrier.
+__device__ __forceinline__ void store_async(uint32_t addr, float4 v, uint32_t bar) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+        "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+        : "memory");
+}
+// A box to the same place in both CTAs, completing its bytes on the same barrier in each.
+__device__ __forceinline__ void tma_load_5d_both(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                                 int c4, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar), "h"((uint16_t)3)
+        : "memory");
+}
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {   // a shared::cluster address
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ void store_cluster(uint32_t addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
-                 "f"(v.w)
-                 : "memory");
+// Arrives, once this thread's MMAs so far have completed, on the barrier at this offset
+// in the other CTA as well.
+__device__ __forceinline__ void umma_commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
-__device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
+// As mbar_wait, for a phase that the other CTA's stores complete.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(hint_ns)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
-// As mbar_wait, for a phase that threads of the other CTA complete.
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, unsigned int *err) {
-    if (try_wait_cluster(bar, parity, 0u)) return true;
+    for (int i = 0; i < 64; ++i)
+        if (try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
-        if (try_wait_cluster(bar, parity, 20000u)) return true;
+        if (try_wait_cluster(bar, parity)) return true;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             raise_error(err, PA_DEVERR_TIMEOUT);
             return false;
         }
     }
 }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// A matrix descriptor that lies `bytes` behind another.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (uint64_t)(bytes >> 4); }
 
 // Named barriers whose threads all learn whether any of them saw `mine`: the two warps
 // of the same rows, and all softmax warps.  A warp that gives up alone would leave the
@@ -168,12 +208,13 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
 
 // ---- the kernel -----------------------------------------------------------------
 
-// Barriers, as in pa_prefill.cu unless noted: Q landed[2], K landed[2], V half
-// landed[3], S ready[2], P ready[2], P.V done[2], P.V done per S buffer[2], K slot
-// free[2], V half free[3], Q free[2], unit's P.V done, O read, the two MMA lanes'
-// drains; then, completed by the other CTA: go[8] (its warp of the same index may be
-// written to), full[8] (its data has landed), norm[4] (both CTAs' partial sums of
-// squares of a lane quadrant's rows).
+// Barriers, as in pa_prefill.cu unless noted: Q landed, K landed[2], V half landed[4],
+// S ready[2] (a K slot is free with it), P ready[2][half of the keys], P.V done[2] (a S
+// buffer is free with it), V half free[4] (in both CTAs: two arrivals), Q free, unit's P.V
+// done (in both CTAs), O read, the two MMA lanes' drains; then full[8] (the other CTA's data for a warp has landed),
+// norm[4] (its partial sums of squares of a lane quadrant's rows), out[2] (a unit's
+// output is staged in its last value slots, or written: by unit parity), other out[2]
+// (the other CTA's is stored).
 // The tiles of the CTA's units are numbered T = 0, 1, ...; its value halves H = 2T, 2T + 1.
 template <int DH, int G, int BS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -191,20 +232,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t base = smem_addr(smem_raw);
     const uint32_t sQ = base + SM::kOffQ, sK = base + SM::kOffK, sV = base + SM::kOffV;
-    const uint32_t barQ = base + SM::kOffBar, barK = barQ + 16, barV = barK + 16, barS = barV + 8 * kVS,
-                   barP = barS + 16, barOP = barP + 16, barSdone = barOP + 16, barKfree = barSdone + 16,
-                   barVfree = barKfree + 16, barQfree = barVfree + 8 * kVS, barUnit = barQfree + 16,
-                   barOfree = barUnit + 8, barEnd = barOfree + 8, barEndQk = barEnd + 8, barGo = barEndQk + 8,
-                   barFull = barGo + 64, barNorm = barFull + 64;
-    constexpr int kNumBars = 2 + 2 + kVS + 2 + 2 + 2 + 2 + 2 + kVS + 2 + 1 + 1 + 1 + 1 + 8 + 8 + 4;
+    const uint32_t barQ = base + SM::kOffBar, barK = barQ + 8, barV = barK + 16, barS = barV + 8 * kVS,
+                   barP = barS + 16, barOP = barP + 32, barVfree = barOP + 16, barQfree = barVfree + 8 * kVS, barUnit = barQfree + 8,
+                   barOfree = barUnit + 8, barEnd = barOfree + 8, barEndQk = barEnd + 8, barFull = barEndQk + 8,
+                   barNorm = barFull + 64, barOut = barNorm + 32,
+                   barOtherOut = barOut + 16;
+    constexpr int kNumBars = 1 + 2 + kVS + 2 + 4 + 2 + kVS + 1 + 1 + 1 + 1 + 1 + 8 + 4 + 2 + 2;
     static_assert(8 * kNumBars + 8 <= 384, "barrier area");
+    static_assert(kVS == 4, "two tiles of value halves");
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + SM::kOffBar + 8 * kNumBars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem_raw + SM::kOffBar + 8 * kNumBars + 4);
     // The halves' maxima of a tile ([tile parity][half][row]), in the epilogue their
     // sums, then the four partial sums of squares of a row ([2 * CTA + half][row]).
     float *mx = reinterpret_cast<float *>(smem_raw + SM::kOffX);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in every lane, and known to be
     const uint32_t rank = cluster_rank();
 
     if (warp == kMmaWarp) {
@@ -217,10 +260,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kNumBars; ++i) {
             const uint32_t b = barQ + 8 * i;
             uint32_t count = 1;
-            if ((b >= barP && b < barOP) || b == barOfree) count = kSoftWarps * 32;
-            if (b >= barQfree && b < barUnit) count = 2;     // the Q.K lane's commit and the epilogue's release
-            if (b >= barGo && b < barNorm) count = 32;       // the other CTA's warp
-            if (b >= barNorm) count = 128;                   // the four warps that share the rows
+            if ((b >= barP && b < barOP) || b == barOfree || (b >= barOut && b < barOtherOut)) count = kSoftWarps * 32;
+            if (b >= barVfree && b < barQfree) count = 2;    // both CTAs' P.V lanes
+            if (b == barUnit) count = 2;                     // both CTAs' P.V lanes
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(count) : "memory");
         }
         // the tiles' swizzle wants 1,024-byte alignment, which dynamic shared memory
@@ -236,9 +278,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const uint32_t tO = tmem + 256;
     const bool usable = *abort_flag == 0;
+    float *weights = reinterpret_cast<float *>(smem_raw + SM::kOffW);
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (tid < DH) weights[tid] = p.norm_weight ? __ldg(p.norm_weight + rank * DH + tid) : 1.f;
+    __syncthreads();
 
     // ---- this cluster's units
     const int C = (int)gridDim.x / 2, cl = (int)blockIdx.x / 2;
@@ -276,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // K warp copies tiles of NBK blocks, the V warp halves of NBV.
         const bool is_k = warp == kKWarp;
         const int nb = is_k ? NBK : NBV, per_tile = is_k ? 1 : 2, spl = 32 / nb, slots = is_k ? 2 : kVS;
-        const uint32_t bar0 = is_k ? barK : barV, free0 = is_k ? barKfree : barVfree;
+        const uint32_t bar0 = is_k ? barK : barV, free0 = is_k ? barS : barVfree;
         auto ids_load = [&](const Unit &U, int c) -> int {
             const int bi = c * 32 + lane;
             return bi < U.nblk && bi < U.n_tiles * NBK ? __ldg(p.tables + (size_t)U.s * p.max_blocks + bi) : 0;
@@ -290,9 +336,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             return v;
         };
+        // Unit x's output, from its value slot to memory; then both CTAs' value slots of the
+        // unit are free for copies from either (V warp; every unit once, in order: two barriers
+        // by parity, so that none is lapped).
+        int out_slot[2] = {0, 0};
+        auto store_out = [&](int x) -> bool {
+            const bool done = __all_sync(0xffffffffu, mbar_wait(barOut + 8 * (x & 1), (uint32_t)((x >> 1) & 1), p.err));
+            const Unit Y = unit(x);
+            if (done && Y.j0 + min(QPT, p.chunk) <= p.chunk) {
+                if (lane == 0) {
+                    const uint32_t src = sV + (uint32_t)(x & 1 ? out_slot[1] : out_slot[0]) * SM::kVHalf;
+#pragma unroll
+                    for (int h = 0; h < SM::kHalves; ++h)
+                        tma_store_4d(&tmap_o, (int)rank * DH + h * 64, 0, Y.g, Y.s * p.chunk + Y.j0, src + h * kHalf);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+                __syncwarp();
+            }
+            if (!done) return false;
+            if (lane == 0) arrive_cluster(peer_addr(barOtherOut + 8 * (x & 1), rank ^ 1u));
+            return __all_sync(0xffffffffu, wait_cluster(barOtherOut + 8 * (x & 1), (uint32_t)((x >> 1) & 1), p.err));
+        };
         bool ok = true;
         int N = 0;      // tiles or halves issued so far
         int nq = 0;     // query tiles issued (K warp)
+        int prev_steps = 0;
         Unit U;
         int raw_cur = 0, raw_next = 0;
         if (my_units > 0) {
@@ -309,21 +378,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 nraw_next = ids_load(X, 1);
             }
             if (is_k) {
-                // Q buffer k % 2 held unit k - 2's Q, its exchange and its output tile
-                const int qb = k & 1;
-                if (k >= 2)
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(barQfree + 8 * qb, (uint32_t)(((k >> 1) - 1) & 1), p.err));
+                if (k > 0)     // the previous unit's Q.K have all read the query tile
+                    ok = __all_sync(0xffffffffu, mbar_wait(barQfree, (uint32_t)((k - 1) & 1), p.err));
                 if (!ok) {
                     *abort_flag = 1;
                     break;
                 }
                 nq = k + 1;
-                if (lane == 0) mbar_expect(barQ + 8 * qb, SM::kQTile);
+                if (lane == 0) mbar_expect(barQ, SM::kQTile);
                 __syncwarp();
                 if (lane < SM::kHalves)
-                    tma_load_5d(sQ + qb * SM::kQTile + lane * kHalf, &tmap_q, lane * 64, (int)rank, 0, U.g,
-                                U.s * p.chunk + U.j0, barQ + 8 * qb);
+                    tma_load_5d(sQ + lane * kHalf, &tmap_q, lane * 64, (int)rank, 0, U.g, U.s * p.chunk + U.j0, barQ);
             }
             const int key_head = p.by_head ? U.g : 2 * U.g + (int)rank;
             const int value_head = p.by_head ? (U.g >> 1) * 2 : 2 * U.g;
@@ -343,9 +408,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                      : __shfl_sync(0xffffffffu, ids_cur, (tb + lane) & 31);
                 if (N >= slots) {   // the slot's previous tile has been consumed by its MMAs
                     const int np = N - slots;
-                    ok = __all_sync(0xffffffffu, mbar_wait(free0 + 8 * (np % slots), (uint32_t)((np / slots) & 1),
-                                                           p.err));
+                    const uint32_t bar = free0 + 8 * (np % slots), parity = (uint32_t)((np / slots) & 1);
+                    ok = __all_sync(0xffffffffu, is_k ? mbar_wait(bar, parity, p.err) : wait_cluster(bar, parity, p.err));
                     if (!ok) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                }
+                // A unit's last two value slots also hold its exchange and its output, and are
+                // next filled four halves on: from this unit's third half on, or, behind a unit
+                // of two halves, from the first of the unit after.
+                if (!is_k) {
+                    const int x = t == 2 ? k - 1 : t == 0 && prev_steps == 2 ? k - 2 : -1;
+                    if (x >= 0 && !store_out(x)) {
+                        ok = false;
                         *abort_flag = 1;
                         break;
                     }
@@ -358,101 +434,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tma_load_5d(sK + st * SM::kKTile + h * kHalf + b * (BS * 128), &tmap_k, h * 64, 0, key_head, 0,
                                     blk, bar0 + 8 * st);
                 } else if (lane < NBV) {
-                    tma_load_5d(sV + st * SM::kVHalf + lane * kVBlock, &tmap_v, 0, 0, 0, value_head, blk,
-                                bar0 + 8 * st);
+                    // one of the block's two heads, to both CTAs; the other CTA copies the other
+                    tma_load_5d_both(sV + st * SM::kVHalf + lane * kVBlock + rank * (kVBlock / 2), &tmap_v, 0, 0, 0,
+                                     value_head + (int)rank, blk, bar0 + 8 * st);
                 }
             }
+            prev_steps = steps;
+            if (k & 1) out_slot[1] = (N + kVS - 2) % kVS;     // where this unit's output will be staged
+            else out_slot[0] = (N + kVS - 2) % kVS;
             U = X;
             raw_cur = nraw_cur;
             raw_next = nraw_next;
+        }
+        if (!is_k) {    // the outputs no later half waited for
+            for (int x = max(0, my_units - (prev_steps == 2 ? 2 : 1)); x < my_units && ok && !*abort_flag; ++x)
+                ok = store_out(x);
+            if (lane == 0) bulk_wait_all();   // no store in flight when the CTA ends
         }
         if (!ok || *abort_flag) {
             // wait (bounded) for this warp's copies still in flight before the memory is released
             for (int t = max(0, N - slots); t < N; ++t)
                 mbar_wait(bar0 + 8 * (t % slots), (uint32_t)((t / slots) & 1), p.err);
-            for (int k = max(0, nq - 2); k < nq; ++k) mbar_wait(barQ + 8 * (k & 1), (uint32_t)((k >> 1) & 1), p.err);
+            if (nq > 0) mbar_wait(barQ, (uint32_t)((nq - 1) & 1), p.err);
         }
         __syncwarp();
     } else if (warp == kMmaWarp || warp == kQkWarp) {
-        // ---- two issuing lanes, as in pa_prefill.cu
-        if (lane == 0) {
-            const bool is_qk = warp == kQkWarp;
-            bool ok = true;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                if (ok && !mbar_wait(bar, parity, p.err)) {
-                    ok = false;
-                    *abort_flag = 1;
-                }
-                return ok;
-            };
-            int T = 0;
-            for (int k = 0; k < my_units && ok && !*abort_flag; ++k) {
-                const Unit U = unit(k);
-                if (is_qk) {
-                    const int qb = k & 1;
-                    if (!wait(barQ + 8 * qb, (uint32_t)((k >> 1) & 1))) break;
-                    const uint32_t sQb = sQ + qb * SM::kQTile;
-                    for (int t = 0; t < U.n_tiles; ++t, ++T) {
-                        if (*abort_flag) {
-                            ok = false;
-                            break;
-                        }
-                        const int st = T & 1;      // K slot and S buffer
-                        if (!wait(barK + 8 * st, (uint32_t)((T >> 1) & 1))) break;
-                        // S buffer st held P(T - 2): its P.V must have completed
-                        if (T >= 2 && !wait(barSdone + 8 * st, (uint32_t)(((T - 2) >> 1) & 1))) break;
-                        tc_fence_after();
+        // ---- two issuing warps, as in pa_prefill.cu.  The whole warp walks the tiles and one
+        // lane issues, from descriptors that differ by an addition: issued by one lane on its
+        // own, with every descriptor put together anew, a tile's sixteen products and their
+        // waits took as long as the products themselves.
+        const bool is_qk = warp == kQkWarp;
+        const bool leader = elect_one();
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err));
+            return ok;
+        };
+        const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(sK, 16, 1024);
+        const uint64_t dV = smem_desc(sV, BS * 128, BS >= 16 ? 1024 : kVBlock);
+        int T = 0;
+        for (int k = 0; k < my_units && ok && !*abort_flag; ++k) {
+            const int n_tiles = unit(k).n_tiles;
+            if (is_qk) {
+                if (!wait(barQ, (uint32_t)(k & 1))) break;
+                for (int t = 0; t < n_tiles; ++t, ++T) {
+                    const int st = T & 1;      // K slot and S buffer
+                    const uint32_t ph = (uint32_t)((T >> 1) & 1);
+                    if (!wait(barK + 8 * st, ph)) break;
+                    // S buffer st held P(T - 2): its P.V must have completed
+                    if (T >= 2 && !wait(barOP + 8 * st, ph ^ 1u)) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t dk = desc_at(dK, st * SM::kKTile);
+                        const uint32_t dst = tmem + st * 128;
 #pragma unroll
                         for (int kk = 0; kk < DH / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                            umma(tmem + st * 128, smem_desc(sQb + off, 16, 1024),
-                                 smem_desc(sK + st * SM::kKTile + off, 16, 1024), idesc_qk, kk > 0);
+                            umma(dst, desc_at(dQ, off), desc_at(dk, off), idesc_qk, kk > 0);
                         }
                         umma_commit(barS + 8 * st);
-                        umma_commit(barKfree + 8 * st);
                     }
-                    if (!ok) break;
-                    umma_commit(barQfree + 8 * qb);
-                } else {
-                    // O is overwritten by this unit's first P.V: the previous unit's epilogue has read it
-                    if (k > 0 && !wait(barOfree, (uint32_t)((k - 1) & 1))) break;
-                    for (int t = 0; t < U.n_tiles; ++t, ++T) {
-                        if (*abort_flag) {
-                            ok = false;
-                            break;
-                        }
-                        if (!wait(barP + 8 * (T & 1), (uint32_t)((T >> 1) & 1))) break;
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (leader) umma_commit(barQfree);
+            } else {
+                // O is overwritten by this unit's first P.V: the previous unit's epilogue has read it
+                if (k > 0 && !wait(barOfree, (uint32_t)((k - 1) & 1))) break;
+                for (int t = 0; t < n_tiles && ok; ++t, ++T) {
+                    const int sb = T & 1;
+                    const uint32_t ph = (uint32_t)((T >> 1) & 1);
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const int H = 2 * T + hf, st = H % kVS;
-                            if (!wait(barV + 8 * st, (uint32_t)((H / kVS) & 1))) break;
-                            tc_fence_after();
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int st = (2 * T + hf) & (kVS - 1);
+                        if (!wait(barV + 8 * st, ph)) break;     // half 2T + hf, four slots: (2T + hf) / 4 = T / 2
+                        if (!wait(barP + 16 * sb + 8 * hf, ph)) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint64_t dv = desc_at(dV, st * SM::kVHalf);
+                            const uint32_t tP = tmem + sb * 128 + hf * 64;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
                                 // 16 keys: within one block for b >= 16 (8-key groups 1024 B apart), or
-                                // two whole blocks for b = 8 (groups one block apart)
+                                // two whole blocks for b = 8 (groups one block apart).  P of 32 keys
+                                // lies in 16 columns, the first half of those its scores had.
                                 const uint32_t v_off =
                                     (uint32_t)(kk * 16 / BS) * kVBlock + (uint32_t)((kk * 16) % BS) * 128u;
-                                umma_ts(tO, tmem + p_col(T & 1, hf * 4 + kk),
-                                        smem_desc(sV + st * SM::kVHalf + v_off, BS * 128, BS >= 16 ? 1024 : kVBlock),
-                                        idesc_pv, (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
+                                umma_ts(tO, tP + (kk >> 1) * 32 + (kk & 1) * 8, desc_at(dv, v_off), idesc_pv,
+                                        (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
                             }
-                            umma_commit(barVfree + 8 * st);
+                            umma_commit_both(barVfree + 8 * st);
+                            if (hf == 1) umma_commit(barOP + 8 * sb);
                         }
-                        if (!ok) break;
-                        umma_commit(barOP + 8 * (T & 1));
-                        umma_commit(barSdone + 8 * (T & 1));
+                        __syncwarp();
                     }
-                    if (!ok) break;
-                    umma_commit(barUnit);   // every P.V of the unit has completed
                 }
+                if (!ok) break;
+                if (leader) umma_commit_both(barUnit);   // every P.V of the unit has completed, in this CTA
             }
-            // one more commit, on a barrier used once, tracks every MMA this lane issued
-            if (!ok || *abort_flag) *abort_flag = 1;   // give up: drain what was issued
-            const uint32_t end = is_qk ? barEndQk : barEnd;
-            umma_commit(end);
-            mbar_wait(end, 0, p.err);
         }
+        // one more commit, on a barrier used once, tracks every MMA this warp issued
+        if (!ok) *abort_flag = 1;   // give up: drain what was issued
+        const uint32_t end = is_qk ? barEndQk : barEnd;
+        if (leader) umma_commit(end);
+        __syncwarp();
+        mbar_wait(end, 0, p.err);
         __syncwarp();
     } else {
         // ---- softmax warps: row r, key half pt (scale_log2 > 0: maxima of raw scores)
@@ -460,14 +546,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const float c = p.scale_log2;
         const uint32_t other = rank ^ 1u;
-        // thread 0: the Q buffer whose release it owes once the tensor store of the output
-        // tile staged there has read it (-1: none)
-        int q_owed = -1;
-        auto release = [&]() {
-            bulk_wait_read();
-            mbar_arrive_u32(barQfree + 8 * q_owed);
-            q_owed = -1;
-        };
         int T = 0;
         for (int k = 0; k < my_units; ++k) {
             const Unit U = unit(k);
@@ -481,46 +559,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = 0; t < U.n_tiles; ++t, ++T) {
                 const int sb = T & 1;
                 bool ok = mbar_wait(barS + 8 * sb, (uint32_t)((T >> 1) & 1), p.err);
-                if (t == 1 && tid == 0 && q_owed >= 0) release();
-                uint32_t sr[kPC][32];
+                // this thread's keys: 32 of the tile's first half, 32 of its second
+                uint32_t sr[2][32];
+                const uint32_t tS = tmem + sb * 128 + lane_off + pt * 32;
                 if (__all_sync(0xffffffffu, ok)) {
                     tc_fence_after();
-#pragma unroll
-                    for (int cc = 0; cc < kPC; ++cc) tmem_ld32(tmem + sb * 128 + lane_off + pt * kPK + cc * 32, sr[cc]);
+                    tmem_ld32(tS, sr[0]);
+                    tmem_ld32(tS + 64, sr[1]);
                     tmem_ld_wait();
                 } else {
                     ok = false;
                 }
-                const int key0 = t * kKeys + pt * kPK;
-                if (!__all_sync(0xffffffffu, key0 + kPK - 1 <= pos)) {   // tile crosses some row's causal edge
+                const int key0 = t * kKeys + pt * 32;
+                if (!__all_sync(0xffffffffu, key0 + 64 + 31 <= pos)) {   // tile crosses some row's causal edge
 #pragma unroll
-                    for (int cc = 0; cc < kPC; ++cc)
+                    for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (key0 + cc * 32 + i > pos) sr[cc][i] = __float_as_uint(-INFINITY);
-                }
-                // the row's maximum of the tile: both halves, so that both move alike
-                const float mine = max_tree64(sr[0], sr[1]);
-                mx[(sb * 2 + pt) * 128 + r] = mine;
-                if (part_or(warp, !ok || *abort_flag)) {   // give up
-                    *abort_flag = 1;
-                    mbar_arrive_u32(barP + 8 * sb);   // keep the arrival count balanced
-                    break;
-                }
-                const float mh = fmaxf(mine, mx[(sb * 2 + (pt ^ 1)) * 128 + r]);
-                const float mt_ = mh * c;
-                float alpha = 1.f;
-                if (mt_ > m_ref + kRescaleThreshold || (m_ref == -INFINITY && mt_ != -INFINITY)) {
-                    alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - mt_);
-                    m_ref = mt_;
+                            if (key0 + cc * 64 + i > pos) sr[cc][i] = __float_as_uint(-INFINITY);
                 }
                 const float2 c2 = make_float2(c, c);
-                const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-                const float2 nm2 = make_float2(nm, nm);
                 float2 ps2 = make_float2(0.f, 0.f), ps2b = make_float2(0.f, 0.f);
-                uint32_t pw[32];
-#pragma unroll
-                for (int cc = 0; cc < kPC; ++cc) {
+                uint32_t pw[16];
+                auto probabilities = [&](int cc) {   // of half cc, and their sums
+                    const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float2 x = __ffma2_rn(
@@ -528,63 +591,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                         if (e & 1) ps2b = __fadd2_rn(ps2b, pe);
                         else ps2 = __fadd2_rn(ps2, pe);
-                        pw[cc * 16 + e] = pack_bf16x2(pe.x, pe.y);
+                        pw[e] = pack_bf16x2(pe.x, pe.y);
                     }
-                }
-                // P as bf16 into the S columns read above; each probability one term (with
-                // few keys the plain kernel's grouped form takes two; a prompt's rows see many)
-                tmem_st32(tmem + sb * 128 + lane_off + pt * kPK, pw);
-                tmem_st_wait();
-                ps2 = __fadd2_rn(ps2, ps2b);
-                l = l * alpha + (ps2.x + ps2.y);
-                // rescale this thread's half of the accumulator's columns once P.V(T - 1) has
-                // completed (its barrier's previous phase, P.V(T - 3), completed before Q.K(T - 1)
-                // was issued, which S(T - 1), read before this tile, needed)
-                if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    const int tp = T - 1;
-                    mbar_wait(barOP + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1), p.err);
-                    tc_fence_after();
-#pragma unroll
-                    for (int cc = 0; cc < DH / 32; ++cc) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + pt * DH + lane_off + cc * 32, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st32(tO + pt * DH + lane_off + cc * 32, o);
+                };
+                // The first half's probabilities by the reference as it is, while the maximum is
+                // found; a barrier of the row's two warps then says whether any of their rows
+                // exceeds it by more than the threshold.  Rarely (and with the first tile): both
+                // threads of a row take the larger of their maxima and start over.
+                const float mine = max_tree64(sr[0], sr[1]);
+                const float mine_l = mine * c;
+                const bool trouble = !ok || *abort_flag;
+                bool give_up = false;
+                float alpha = 1.f;
+#pragma unroll 1
+                for (bool first = true;; first = false) {
+                    ps2 = ps2b = make_float2(0.f, 0.f);
+                    probabilities(0);
+                    if (!first || !part_or(warp, trouble || mine_l > m_ref + kRescaleThreshold ||
+                                                     (m_ref == -INFINITY && mine_l != -INFINITY)))
+                        break;
+                    mx[(sb * 2 + pt) * 128 + r] = mine_l;
+                    if (part_or(warp, trouble)) {
+                        give_up = true;
+                        break;
                     }
-                    tmem_st_wait();
-                }
-                // keys past the sequence end inside its last block: zero their V rows (their p is
-                // 0, but the slots may hold non-finite junk).  P.V(T - 1) is waited for first, so
-                // that the wait for the half's copy is exact: every half before tile T has then
-                // landed, and P.V(T) cannot take this one before P(T) is signalled below.
-                const int tail_lo = U.seq_end - t * kKeys;
-                if (tail_lo > 0 && tail_lo < kKeys && (U.seq_end % BS) != 0) {
-                    if (T > 0) {
+                    const float mt_ = fmaxf(mine_l, mx[(sb * 2 + (pt ^ 1)) * 128 + r]);
+                    if (mt_ > m_ref + kRescaleThreshold || (m_ref == -INFINITY && mt_ != -INFINITY)) {
+                        alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - mt_);
+                        m_ref = mt_;
+                    }
+                    // rescale this thread's half of the accumulator's columns once P.V(T - 1) has
+                    // completed (its barrier's previous phase, P.V(T - 3), completed before
+                    // Q.K(T - 1) was issued, which S(T - 1), read before this tile, needed)
+                    if (t > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         const int tp = T - 1;
                         mbar_wait(barOP + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1), p.err);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int cc = 0; cc < DH / 32; ++cc) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + pt * DH + lane_off + cc * 32, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(tO + pt * DH + lane_off + cc * 32, o);
+                        }
+                        tmem_st_wait();
                     }
-                    const int H = 2 * T + tail_lo / 64, sv = H % kVS;
-                    mbar_wait(barV + 8 * sv, (uint32_t)((H / kVS) & 1), p.err);
-                    const int lo = tail_lo % 64, nrows = (BS - U.seq_end % BS);   // to the block's end
-                    constexpr int kChunks = DV / 8;                               // 16-byte chunks of a row
-                    for (int idx = tid; idx < nrows * kChunks; idx += kSoftWarps * 32) {
-                        const int rr = lo + idx / kChunks, c16 = idx % kChunks;
-                        const uint32_t addr = sV + sv * SM::kVHalf + (uint32_t)(rr / BS) * kVBlock +
-                                              (uint32_t)(c16 / 8) * (BS * 128u) + (uint32_t)(rr % BS) * 128u +
-                                              (uint32_t)(c16 % 8) * 16u;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                tc_fence_before();
-                mbar_arrive_u32(barP + 8 * sb);
+                if (give_up) {
+                    *abort_flag = 1;
+                    mbar_arrive_u32(barP + 16 * sb);   // keep the arrival counts balanced
+                    mbar_arrive_u32(barP + 16 * sb + 8);
+                    break;
+                }
+                const int tail_lo = U.seq_end - t * kKeys;
+                const bool zero_tail = tail_lo > 0 && tail_lo < kKeys && (U.seq_end % BS) != 0;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    // P as bf16 into the columns its scores were read from, one rounding a
+                    // probability (with few keys pa_prefill.cu's grouped form takes two terms; a
+                    // prompt's rows see many)
+                    if (hf == 1) probabilities(1);
+                    tmem_st16(tS + hf * 64, pw);
+                    tmem_st_wait();
+                    // Keys past the sequence end inside its last block: zero their V rows (their p
+                    // is 0, but the slots may hold non-finite junk).  P.V(T - 1) is waited for
+                    // first, so that the wait for the half's copy is exact: every half before tile
+                    // T has then landed, and P.V of this one waits for the arrival below.
+                    if (zero_tail && tail_lo / 64 == hf) {
+                        if (T > 0) {
+                            const int tp = T - 1;
+                            mbar_wait(barOP + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1), p.err);
+                        }
+                        const int H = 2 * T + hf, sv = H % kVS;
+                        mbar_wait(barV + 8 * sv, (uint32_t)((H / kVS) & 1), p.err);
+                        const int lo = tail_lo % 64, nrows = BS - U.seq_end % BS;   // to the block's end
+                        constexpr int kChunks = DV / 8;                             // 16-byte chunks of a row
+                        for (int idx = tid; idx < nrows * kChunks; idx += kSoftWarps * 32) {
+                            const int rr = lo + idx / kChunks, c16 = idx % kChunks;
+                            const uint32_t addr = sV + sv * SM::kVHalf + (uint32_t)(rr / BS) * kVBlock +
+                                                  (uint32_t)(c16 / 8) * (BS * 128u) + (uint32_t)(rr % BS) * 128u +
+                                                  (uint32_t)(c16 % 8) * 16u;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    tc_fence_before();
+                    mbar_arrive_u32(barP + 16 * sb + 8 * hf);
+                }
+                ps2 = __fadd2_rn(ps2, ps2b);
+                l = l * alpha + (ps2.x + ps2.y);
                 done = t + 1;
             }
             // ---- epilogue.  The row's sum over both halves (the reference is one); -1: gave up
-            if (tid == 0 && q_owed >= 0) release();   // (units of one tile)
-            const bool fin = done == U.n_tiles && !*abort_flag && mbar_wait(barUnit, (uint32_t)(k & 1), p.err);
+            const bool fin = done == U.n_tiles && !*abort_flag && wait_cluster(barUnit, (uint32_t)(k & 1), p.err);
             float *lx = mx + (T & 1) * 256;           // the parity that the last tile did not use
             lx[pt * 128 + r] = fin ? l : -1.f;
             part_sync(warp);
@@ -594,66 +695,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float lt = l + lo;
             const float f = lt > 0.f ? lam / lt : 0.f;
             tc_fence_after();
-            // ---- the maps meet: x = this CTA's half of the columns, a quarter of 2d at a time
-            const uint32_t sX = sQ + (uint32_t)(k & 1) * SM::kQTile;
-            const uint32_t mine_x = sX + (uint32_t)(pt * (DH / 16) * 128 + r) * 16u;   // chunk i: + i * 2048
-            const uint32_t peer_x = peer_addr(mine_x, other);
+            // ---- the maps meet: x = this CTA's half of the columns.  Both CTAs' P.V of the unit
+            // have completed, so its last two value slots are free in both (a quarter of 2d each).
+            const uint32_t out_off = SM::kOffV + (uint32_t)((2 * T - 2) % kVS) * SM::kVHalf;
+            const uint32_t sX = base + out_off;
+            const uint32_t sY = sV + (uint32_t)((2 * T - 1) % kVS) * SM::kVHalf;
+            const uint32_t my_off = (uint32_t)(pt * (DH / 16) * 128 + r) * 16u;   // chunk i: + i * 2048
             constexpr int W = DH / 4;                 // columns of a thread and quarter
-            float x[2][W];
+            const uint32_t my_full = barFull + 8 * warp, my_norm = barNorm + 8 * (warp & 3);
+            float x[2][W], ss = 0.f;
+            if (ok) {
+                if (lane == 0) mbar_expect(my_full, 2 * 32 * W * 4);
+                if (lane == 0 && pt == 0 && p.norm_weight != nullptr) mbar_expect(my_norm, 2 * 32 * 4);
+                __syncwarp();
+                const uint32_t peer_full = peer_addr(my_full, other);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (!__all_sync(0xffffffffu, ok)) break;
-                const uint32_t ph = (uint32_t)((2 * k + q) & 1);
-                arrive_cluster(peer_addr(barGo + 8 * warp, other));    // this warp's place may be written
-                ok = ok && wait_cluster(barGo + 8 * warp, ph, p.err);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                {
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t dst = peer_addr((q == 0 ? sX : sY) + my_off, other);
                     uint32_t o[W];
                     tmem_ld<W>(tO + lane_off + other * DH + q * (DH / 2) + pt * W, o);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < W / 4; ++i)
-                        store_cluster(peer_x + i * 2048u, make_float4(__uint_as_float(o[4 * i]) * f,
-                                                                      __uint_as_float(o[4 * i + 1]) * f,
-                                                                      __uint_as_float(o[4 * i + 2]) * f,
-                                                                      __uint_as_float(o[4 * i + 3]) * f));
+                        store_async(dst + i * 2048u,
+                                    make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                                                __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f),
+                                    peer_full);
                 }
-                arrive_cluster(peer_addr(barFull + 8 * warp, other));
-                {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
                     uint32_t o[W];
                     tmem_ld<W>(tO + lane_off + rank * DH + q * (DH / 2) + pt * W, o);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < W; ++i) x[q][i] = __uint_as_float(o[i]) * f;
                 }
-                ok = ok && wait_cluster(barFull + 8 * warp, ph, p.err);
-                if (!__all_sync(0xffffffffu, ok)) break;
-#pragma unroll
-                for (int i = 0; i < W / 4; ++i) {
-                    const float4 v = lds_f4(mine_x + i * 2048u);
-                    x[q][4 * i] += v.x;
-                    x[q][4 * i + 1] += v.y;
-                    x[q][4 * i + 2] += v.z;
-                    x[q][4 * i + 3] += v.w;
-                }
             }
             // O has been read: the next unit's first P.V may overwrite it
             tc_fence_before();
             mbar_arrive_u32(barOfree);
-            float scale = p.out_scale;
-            if (p.norm_weight != nullptr && __all_sync(0xffffffffu, ok)) {
-                float ss = 0.f;
+            if (ok) ok = wait_cluster(my_full, (uint32_t)(k & 1), p.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i) {
+                        const float4 v = lds_f4((q == 0 ? sX : sY) + my_off + i * 2048u);
+                        x[q][4 * i] += v.x;
+                        x[q][4 * i + 1] += v.y;
+                        x[q][4 * i + 2] += v.z;
+                        x[q][4 * i + 3] += v.w;
+                    }
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
                     for (int i = 0; i < W; ++i) ss += x[q][i] * x[q][i];
+            }
+            float scale = p.out_scale;
+            if (p.norm_weight != nullptr) {
                 const int at = (int)(2 * rank) + pt;
-                const uint32_t bar = barNorm + 8 * (warp & 3);
                 mx[at * 128 + r] = ss;
-                store_cluster(peer_addr(smem_addr(mx + at * 128 + r), other), ss);
-                arrive_cluster(peer_addr(bar, rank));
-                arrive_cluster(peer_addr(bar, other));
-                ok = wait_cluster(bar, (uint32_t)(k & 1), p.err);
+                float4 four;      // lane i < 8 sends those of the warp's rows 4 i .. 4 i + 3
+                four.x = __shfl_sync(0xffffffffu, ss, (lane & 7) * 4);
+                four.y = __shfl_sync(0xffffffffu, ss, (lane & 7) * 4 + 1);
+                four.z = __shfl_sync(0xffffffffu, ss, (lane & 7) * 4 + 2);
+                four.w = __shfl_sync(0xffffffffu, ss, (lane & 7) * 4 + 3);
+                if (ok && lane < 8)
+                    store_async(peer_addr(smem_addr(mx + at * 128 + (warp & 3) * 32 + lane * 4), other), four,
+                                peer_addr(my_norm, other));
+                ok = !part_or(warp, !ok) && wait_cluster(my_norm, (uint32_t)(k & 1), p.err);
                 ss = (mx[r] + mx[128 + r]) + (mx[256 + r] + mx[384 + r]);
                 scale *= rsqrtf(ss * (1.f / DV) + p.eps);
             }
@@ -676,19 +787,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     float y[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] = x[q][i8 * 8 + e] * scale;
-                    if (p.norm_weight != nullptr) {
-                        const float4 *w4 =
-                            reinterpret_cast<const float4 *>(p.norm_weight + rank * DH + c0 + i8 * 8);
-                        const float4 wa = __ldg(w4), wb = __ldg(w4 + 1);
-                        y[0] *= wa.x;
-                        y[1] *= wa.y;
-                        y[2] *= wa.z;
-                        y[3] *= wa.w;
-                        y[4] *= wb.x;
-                        y[5] *= wb.y;
-                        y[6] *= wb.z;
-                        y[7] *= wb.w;
-                    }
+                    const float4 *w4 = reinterpret_cast<const float4 *>(weights + c0 + i8 * 8);
+                    const float4 wa = w4[0], wb = w4[1];
+                    y[0] *= wa.x;
+                    y[1] *= wa.y;
+                    y[2] *= wa.z;
+                    y[3] *= wa.w;
+                    y[4] *= wb.x;
+                    y[5] *= wb.y;
+                    y[6] *= wb.z;
+                    y[7] *= wb.w;
                     uint4 v;
                     v.x = pack_bf16x2(y[0], y[1]);
                     v.y = pack_bf16x2(y[2], y[3]);
@@ -698,34 +806,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (tma_out) {
                         // 16-byte chunk j of a 128-byte line goes to chunk j ^ (r % 8): the swizzle
                         // that the tensor store undoes
-                        const uint32_t line = sX + (uint32_t)(col / 64) * kHalf + (uint32_t)r * 128u;
+                        const uint32_t line = out_off + (uint32_t)(col / 64) * kHalf + (uint32_t)r * 128u;
                         const uint32_t c16 = (uint32_t)(col % 64) / 8;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line +
-                                                                                      ((c16 ^ ((uint32_t)r & 7u)) << 4)),
-                                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                                     : "memory");
+                        *reinterpret_cast<uint4 *>(smem_raw + line + ((c16 ^ ((uint32_t)r & 7u)) << 4)) = v;
                     } else if (row_ok) {
                         *reinterpret_cast<uint4 *>(dst + col) = v;
                     }
                 }
             }
-            if (tma_out) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                soft_sync();
-                if (tid == 0) {
-#pragma unroll
-                    for (int h = 0; h < SM::kHalves; ++h)
-                        tma_store_4d(&tmap_o, (int)rank * DH + h * 64, 0, U.g, U.s * p.chunk + U.j0, sX + h * kHalf);
-                    bulk_commit();
-                    q_owed = k & 1;   // released once the stores have read it
-                }
-            } else if (tid == 0) {
-                mbar_arrive_u32(barQfree + 8 * (k & 1));
-            }
-        }
-        if (tid == 0) {   // no store may still read shared memory, or be in flight, when the CTA ends
-            if (q_owed >= 0) release();
-            bulk_wait_all();
+            // staged (or written): the V warp may store it, and fill the slots again
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive_u32(barOut + 8 * (k & 1));
         }
     }
     tc_fence_before();
@@ -805,8 +896,8 @@ cudaError_t launch_pairs(const PrefillArgs &a, const pa_diff &diff, bool by_head
         const cuuint32_t box[5] = {64, (cuuint32_t)BS, 1, 1, 1};
         if (!encode_bf16(&mk, 5, a.pool.base, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    // values: one box per block, both heads
-    if (encode_pool_block_map(&mv, a.pool, 1, BS, 2) != cudaSuccess) return cudaErrorInvalidValue;
+    // values: one box per block and head
+    if (encode_pool_block_map(&mv, a.pool, 1, BS) != cudaSuccess) return cudaErrorInvalidValue;
     DiffParams prm;
     prm.out = static_cast<__nv_bfloat16 *>(a.out);
     prm.tables = a.tables;
