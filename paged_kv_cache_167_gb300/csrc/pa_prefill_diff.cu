@@ -73,7 +73,7 @@ template <int DH>
 struct DiffSmem {
     static constexpr int kHalves = DH / 64;                      // 64-wide halves of a head
     static constexpr uint32_t kQTile = kHalves * kHalf;          // [half][128 rows][128 B]
-    static constexpr uint32_t kKTile = kHalves * kHalf;          // [half][128 keys][128 B]
+    static constexpr uint32_t kKTile = kHalves * kHalf;          // [8 keys][half][8 keys][128 B]: see the map
     static constexpr uint32_t kVHalf = 64u * 2u * DH * 2u;       // 64 keys: [block][head][half][BS][128 B]
     static constexpr int kVSlots = 4;
     static constexpr uint32_t kOffQ = 0;
@@ -130,31 +130,6 @@ __device__ __forceinline__ void umma_commit_both(uint32_t bar) {
         "h"((uint16_t)3)
         : "memory");
 }
-// As mbar_wait, for a phase that the other CTA's stores complete.
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, unsigned int *err) {
-    for (int i = 0; i < 64; ++i)
-        if (try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (try_wait_cluster(bar, parity)) return true;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            raise_error(err, PA_DEVERR_TIMEOUT);
-            return false;
-        }
-    }
-}
-
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -320,8 +295,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kKWarp || warp == kVWarp) {
         // ---- copy warps: a lane per box, block ids in registers a load of 32 ahead.  The
         // K warp copies tiles of NBK blocks, the V warp halves of NBV.
-        const bool is_k = warp == kKWarp;
-        const int nb = is_k ? NBK : NBV, per_tile = is_k ? 1 : 2, spl = 32 / nb, slots = is_k ? 2 : kVS;
+        auto copy = [&](auto which) {
+        constexpr bool is_k = decltype(which)::value;
+        constexpr int nb = is_k ? NBK : NBV, per_tile = is_k ? 1 : 2, spl = 32 / nb, slots = is_k ? 2 : kVS;
         const uint32_t bar0 = is_k ? barK : barV, free0 = is_k ? barS : barVfree;
         auto ids_load = [&](const Unit &U, int c) -> int {
             const int bi = c * 32 + lane;
@@ -356,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!done) return false;
             if (lane == 0) arrive_cluster(peer_addr(barOtherOut + 8 * (x & 1), rank ^ 1u));
-            return __all_sync(0xffffffffu, wait_cluster(barOtherOut + 8 * (x & 1), (uint32_t)((x >> 1) & 1), p.err));
+            return __all_sync(0xffffffffu, mbar_wait(barOtherOut + 8 * (x & 1), (uint32_t)((x >> 1) & 1), p.err));
         };
         bool ok = true;
         int N = 0;      // tiles or halves issued so far
@@ -395,21 +371,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int ids_cur = ids_check(raw_cur, U, 0);
             const int steps = U.n_tiles * per_tile;
             for (int t = 0; t < steps; ++t, ++N) {
-                if (*abort_flag) {
-                    ok = false;
-                    break;
-                }
                 if (t > 0 && t % spl == 0) {
                     ids_cur = ids_check(raw_next, U, t / spl);
                     raw_next = ids_load(U, t / spl + 1);
                 }
                 const int tb = (t % spl) * nb, st = N % slots;
-                const int blk = is_k ? __shfl_sync(0xffffffffu, ids_cur, (tb + lane / SM::kHalves) & 31)
-                                     : __shfl_sync(0xffffffffu, ids_cur, (tb + lane) & 31);
+                const int blk = __shfl_sync(0xffffffffu, ids_cur, (tb + lane) & 31);
                 if (N >= slots) {   // the slot's previous tile has been consumed by its MMAs
                     const int np = N - slots;
                     const uint32_t bar = free0 + 8 * (np % slots), parity = (uint32_t)((np / slots) & 1);
-                    ok = __all_sync(0xffffffffu, is_k ? mbar_wait(bar, parity, p.err) : wait_cluster(bar, parity, p.err));
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err));
                     if (!ok) {
                         *abort_flag = 1;
                         break;
@@ -429,10 +400,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_expect(bar0 + 8 * st, is_k ? SM::kKTile : SM::kVHalf);
                 __syncwarp();
                 if (is_k) {
-                    const int b = lane / SM::kHalves, h = lane % SM::kHalves;
-                    if (b < NBK)
-                        tma_load_5d(sK + st * SM::kKTile + h * kHalf + b * (BS * 128), &tmap_k, h * 64, 0, key_head, 0,
-                                    blk, bar0 + 8 * st);
+                    if (lane < NBK)
+                        tma_load_5d(sK + st * SM::kKTile + lane * (uint32_t)(BS * DH * 2), &tmap_k, 0, 0, 0,
+                                    key_head * (BS / 8), blk, bar0 + 8 * st);
                 } else if (lane < NBV) {
                     // one of the block's two heads, to both CTAs; the other CTA copies the other
                     tma_load_5d_both(sV + st * SM::kVHalf + lane * kVBlock + rank * (kVBlock / 2), &tmap_v, 0, 0, 0,
@@ -458,6 +428,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (nq > 0) mbar_wait(barQ, (uint32_t)((nq - 1) & 1), p.err);
         }
         __syncwarp();
+        };
+        if (warp == kKWarp) copy(std::true_type());
+        else copy(std::false_type());
     } else if (warp == kMmaWarp || warp == kQkWarp) {
         // ---- two issuing warps, as in pa_prefill.cu.  The whole warp walks the tiles and one
         // lane issues, from descriptors that differ by an addition: issued by one lane on its
@@ -470,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err));
             return ok;
         };
-        const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(sK, 16, 1024);
+        const uint64_t dQ = smem_desc(sQ, 16, 1024), dK = smem_desc(sK, 16, SM::kHalves * 1024);
         const uint64_t dV = smem_desc(sV, BS * 128, BS >= 16 ? 1024 : kVBlock);
         int T = 0;
         for (int k = 0; k < my_units && ok && !*abort_flag; ++k) {
@@ -490,7 +463,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < DH / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                            umma(dst, desc_at(dQ, off), desc_at(dk, off), idesc_qk, kk > 0);
+                            const uint32_t k_off = (kk >> 2) * 1024 + (kk & 3) * 32;
+                            umma(dst, desc_at(dQ, off), desc_at(dk, k_off), idesc_qk, kk > 0);
                         }
                         umma_commit(barS + 8 * st);
                     }
@@ -685,7 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 done = t + 1;
             }
             // ---- epilogue.  The row's sum over both halves (the reference is one); -1: gave up
-            const bool fin = done == U.n_tiles && !*abort_flag && wait_cluster(barUnit, (uint32_t)(k & 1), p.err);
+            const bool fin = done == U.n_tiles && !*abort_flag && mbar_wait(barUnit, (uint32_t)(k & 1), p.err);
             float *lx = mx + (T & 1) * 256;           // the parity that the last tile did not use
             lx[pt * 128 + r] = fin ? l : -1.f;
             part_sync(warp);
@@ -734,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // O has been read: the next unit's first P.V may overwrite it
             tc_fence_before();
             mbar_arrive_u32(barOfree);
-            if (ok) ok = wait_cluster(my_full, (uint32_t)(k & 1), p.err);
+            if (ok) ok = mbar_wait(my_full, (uint32_t)(k & 1), p.err);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
 #pragma unroll
@@ -764,7 +738,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (ok && lane < 8)
                     store_async(peer_addr(smem_addr(mx + at * 128 + (warp & 3) * 32 + lane * 4), other), four,
                                 peer_addr(my_norm, other));
-                ok = !part_or(warp, !ok) && wait_cluster(my_norm, (uint32_t)(k & 1), p.err);
+                ok = !part_or(warp, !ok) && mbar_wait(my_norm, (uint32_t)(k & 1), p.err);
                 ss = (mx[r] + mx[128 + r]) + (mx[256 + r] + mx[384 + r]);
                 scale *= rsqrtf(ss * (1.f / DV) + p.eps);
             }
@@ -889,11 +863,12 @@ cudaError_t launch_pairs(const PrefillArgs &a, const pa_diff &diff, bool by_head
         const cuuint32_t box[4] = {64, G, 1, (cuuint32_t)std::max(1, std::min(kRows / G, a.chunk_len))};
         if (!encode_bf16(&mo, 4, a.out, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    {   // keys as (d, slot, kv-head, K|V, block); box one half of d of one head's block
-        const cuuint64_t dims[5] = {DH, (cuuint64_t)BS, (cuuint64_t)Hkv, 2, (cuuint64_t)a.pool.num_blocks};
-        const cuuint64_t strides[4] = {DH * 2, (cuuint64_t)BS * DH * 2, (cuuint64_t)a.pool.kv_stride * 2,
-                                       (cuuint64_t)a.pool.block_stride * 2};
-        const cuuint32_t box[5] = {64, (cuuint32_t)BS, 1, 1, 1};
+    {   // keys as (64 of d, slot in eight, half of d, eight of slots in a head, block): one box a
+        // block, laid out [eight slots][half][8][128 B], so that eights of keys lie evenly
+        // apart over the whole tile (boxes of one half each took twice as many copies)
+        const cuuint64_t dims[5] = {64, 8, DH / 64, (cuuint64_t)Hkv * (BS / 8), (cuuint64_t)a.pool.num_blocks};
+        const cuuint64_t strides[4] = {DH * 2, 128, 8 * DH * 2, (cuuint64_t)a.pool.block_stride * 2};
+        const cuuint32_t box[5] = {64, 8, DH / 64, (cuuint32_t)(BS / 8), 1};
         if (!encode_bf16(&mk, 5, a.pool.base, dims, strides, box)) return cudaErrorInvalidValue;
     }
     // values: one box per block and head
