@@ -15,31 +15,37 @@
 // each CTA finishes one half of the 2d columns, so it sends the other half of its own
 // map, divided by the row's sum and weighted, to the other CTA: 64 KB of fp32 (the
 // difference and the norm lose nothing before the one rounding to bf16), stored
-// asynchronously into the unit's query tile and its last value slot there, which
-// nothing reads any more; the bytes themselves complete the receiver's barrier.  (With
-// plain remote stores and a release at cluster scope, in two rounds through the query
-// tile alone, this took 20,000 cycles a unit; MEASURED_EXCHANGE.)
+// asynchronously into the unit's last two value slots there, which nothing reads any
+// more; the bytes themselves complete the receiver's barrier.  That takes some 4,500
+// cycles (15 bytes a cycle), the norm's sums and the output another 5,000, against
+// 2,000 for each of the unit's tiles.
+//
+// What bounds it: the tensor pipe.  GB300, 16 x (4,096 + 512) tokens of 64/8 heads, d =
+// 128: 1.08 ms, 1.62 PFLOP/s, 0.86 of the measured bf16 rate; 2,048 tokens from the start
+// (32/8 heads) 59 us, where a cluster has three or four units and their ends weigh more.
 //
 // Design, as far as it is not pa_prefill.cu's:
 //  * A unit is an M-tile of 128 rows (query j0 + r / G, pair r % G of the G query
 //    pairs that share their keys), one KV pair and one sequence; the grid is
 //    persistent, clusters walking units in rounds of alternating direction.
-//  * Rows' keys 0-63 and 64-127 belong to two threads of different warps, which share
-//    one accumulator, so they agree on the reference maximum: each writes its own
-//    maximum of the tile to shared memory and a barrier of the two warps makes both
-//    take the larger.  The reference moves only when it is exceeded by 8 (log2).  P.V
-//    of a half starts when that half's probabilities are there.
+//  * Rows' keys belong to two threads of different warps (32 of each half of the tile
+//    each), which share one accumulator, so they agree on the reference maximum.  A
+//    tile's first probabilities are made with the reference as it is, while each finds its
+//    maximum; a barrier of the two warps then says whether any row exceeds it by more than
+//    8 (log2), and only then do the maxima meet and the tile start over.  P.V of a half of
+//    the keys starts when that half's probabilities are there.
 //  * Shared memory (d = 128): one query tile 32 KB, two key tiles 64 KB, four half value
-//    tiles of 64 keys 128 KB.  With three of them (and two query tiles) the second half
-//    of a product waited for its copy.  The query tile is free once a unit's last scores
-//    are there, so the next unit's is copied under the last products; the exchange and
-//    the output tile use the unit's last two value slots, and the warp that copies
-//    values stores the output from there before it fills them again.
+//    tiles of 64 keys 128 KB.  The query tile is free once a unit's last scores are there,
+//    so the next unit's is copied under the last products; the warp that copies values
+//    stores a unit's output from its value slots before it fills them again.
 //  * Both maps multiply the same values: each CTA copies one head's half of them to both
-//    (multicast), which takes a third off what the SMs read from L2, 96 KB a tile and CTA
-//    without it (that read held a tile at 2,300 cycles; its products take 1,536).
-//  * A wait that another CTA's threads complete acquires at cluster scope; all waits
-//    are bounded, and both CTAs meet at the end before either's shared memory goes.
+//    (multicast), which takes a third off what the SMs read from L2.
+//  * The copying and issuing warps run few instructions a tile, all lanes together: with
+//    every descriptor put together anew by one lane, two copies a block of keys and waits
+//    that acquired at cluster scope, those warps, not the tensor pipe, made the tile
+//    (2,400 cycles, 1.40 ms a call).
+//  * All waits are bounded, and both CTAs meet at the end before either's shared memory
+//    goes.
 #include <algorithm>
 #include <type_traits>
 
@@ -63,6 +69,7 @@ struct DiffParams {
     int32_t num_mt;              // M-tiles per sequence
     int32_t num_kv;              // groups of G query pairs
     int32_t num_seqs;
+    int32_t by_length;           // units in the order of their tiles, not of their keys
     int32_t by_head;             // group u reads key head u for both maps, values of pair u / 2
     const float *lambda;         // [pairs]
     const float *norm_weight;    // [2 DH] or nullptr
@@ -186,7 +193,8 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
 // Barriers, as in pa_prefill.cu unless noted: Q landed, K landed[2], V half landed[4],
 // S ready[2] (a K slot is free with it), P ready[2][half of the keys], P.V done[2] (a S
 // buffer is free with it), V half free[4] (in both CTAs: two arrivals), Q free, unit's P.V
-// done (in both CTAs), O read, the two MMA lanes' drains; then full[8] (the other CTA's data for a warp has landed),
+// done (in both CTAs), O read, the two MMA lanes' drains; then full[8] (the other CTA's
+// data for a warp has landed),
 // norm[4] (its partial sums of squares of a lane quadrant's rows), out[2] (a unit's
 // output is staged in its last value slots, or written: by unit parity), other out[2]
 // (the other CTA's is stored).
@@ -263,8 +271,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     // ---- this cluster's units
     const int C = (int)gridDim.x / 2, cl = (int)blockIdx.x / 2;
-    const int per_seq = p.num_mt * p.num_kv;
-    const int n_units = usable ? per_seq * p.num_seqs : 0;
+    const int per_mt = p.num_kv * p.num_seqs;
+    const int n_units = usable ? p.num_mt * per_mt : 0;
     auto unit_index = [&](int k) { return k * C + ((k & 1) ? C - 1 - cl : cl); };
     const int rounds = (n_units + C - 1) / C;
     const int my_units = rounds > 0 ? rounds - 1 + (unit_index(rounds - 1) < n_units ? 1 : 0) : 0;
@@ -274,9 +282,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto unit = [&](int k) {
         Unit U;
         const int u = unit_index(k);
-        U.s = u / per_seq;
-        U.g = (u / p.num_mt) % p.num_kv;
-        U.j0 = (p.num_mt - 1 - u % p.num_mt) * QPT;     // the longest rows first
+        const int mt = p.by_length ? u / per_mt : u % p.num_mt, gs = p.by_length ? u % per_mt : u / p.num_mt;
+        U.g = gs % p.num_kv;
+        U.s = gs / p.num_kv;
+        U.j0 = (p.num_mt - 1 - mt) * QPT;     // the longest rows first
         int ctx = __ldg(p.ctx_lens + U.s);
         if (ctx < 0 || ctx > p.max_ctx_len) {
             raise_error(p.err, PA_DEVERR_SEQ_LEN);
@@ -888,6 +897,14 @@ cudaError_t launch_pairs(const PrefillArgs &a, const pa_diff &diff, bool by_head
     prm.num_mt = (a.chunk_len + kRows / G - 1) / (kRows / G);
     prm.num_kv = groups;
     prm.num_seqs = a.num_seqs;
+    // The order of the units.  By tile, longest first over all groups and sequences, balances
+    // the clusters best (2,048 tokens from the start, 32/8 heads: 71 us in the other order, 57
+    // in this), but neighbours then read different keys; where all keys and values are more
+    // than L2 keeps (16 x (4,096 + 512), 300 MB: 1,100 us, 1,350 by tile), or where the
+    // contexts, not the tiles, make the lengths (5 x 333 at up to 3,000: 36.3 us, 38.0 by
+    // tile), the tiles of one group and sequence follow each other and read them together.
+    prm.by_length = a.max_ctx_len < a.chunk_len &&
+                    (int64_t)a.num_seqs * ((int64_t)a.max_ctx_len + a.chunk_len) * Hkv * DH * 4 <= (48ll << 20);
     prm.by_head = by_head ? 1 : 0;
     prm.lambda = diff.lambda;
     prm.norm_weight = diff.norm_weight;
