@@ -13,10 +13,10 @@
 // How it runs on the plain kernel's frame: K rows [K1 | K2] and V rows [V1 | V2] of
 // 2d components are one row each (a copy box takes both heads of a slot, so a
 // pipeline stage is 16 tokens of twice the width), and the 2R maps are columns of the
-// score MMA: the first R of them read K1, the others K2.  Up to R = 4 all 2R columns
-// fit one n8 tile, which meets both key heads, and each column keeps the product with
-// its own (a product with zeros instead would carry another head's infinities over).
-// R = 8 has a tile for each key head.  The values are staged once and serve every column, so every byte of the
+// score MMA: the first R of them read K1, the others K2.  Up to R = 4 all 2R columns fit
+// one n8 tile, which meets both key heads, and each column keeps the product with its own
+// (a product with zeros instead would carry another head's infinities over).  R = 8 has
+// a tile for each key head, at d = 128 in a warp of its own.  The values are staged once and serve every column, so every byte of the
 // cache is read once; what the difference needs of two maps meets only where a unit's
 // rows are finished: one warp a query pair holds both maps' sums of a whole row, so
 // the norm is one warp reduction.
@@ -31,10 +31,19 @@
 namespace pa {
 namespace decode {
 
+// Warps that share a ring and its stages: two, one for each key head and its maps, where
+// rows of 256 components have sixteen maps (R = 8): a warp with all of them would run 800
+// instructions a stage, one warp to a scheduler, and that takes longer than the stage's 16
+// KB take to arrive (64 sequences of 600-850 tokens, 64/8 heads: 45.2 us, 42.4 with two).
+// (Two rings a CTA instead of four, so that two CTAs fit an SM: 43.0 us, and 90.4 instead
+// of 86.5 for 4 x 32,768 tokens.)
+template <int D, int G>
+constexpr int kDiffParts = D == 256 && G == 16 ? 2 : 1;
+
 template <int D, int G>
 struct DiffState {
     static constexpr int R = G / 2;           // query pairs of a unit
-    static constexpr int NB = G > 8 ? 2 : 1;  // n8 tiles of map columns
+    static constexpr int NB = G > 8 && kDiffParts<D, G> == 1 ? 2 : 1;  // n8 tiles of map columns a warp has
     float m[NB][2];           // running max (log2 domain) of columns 2t, 2t + 1 of each tile
     float l[NB][2];           // this lane's share of their denominators
     float o[D / 16][NB][4];   // O^T tiles
@@ -67,22 +76,24 @@ struct DiffOp {
     using S = Shape<D, BS>;
     using State = DiffState<D, G>;
     static constexpr int R = State::R, NB = State::NB;
+    static constexpr bool kSplit = kDiffParts<D, G> == 2;   // this warp has the maps of key head `part` alone
+    static constexpr int kCols = kSplit ? R : G;         // its columns: part * kCols + 0 .. kCols - 1
     static constexpr int d = D / 2;        // one head's components
     static constexpr int kCh = d / 32;     // 16-byte chunks of one key row that a lane reads
     struct Q {
         uint32_t w[NB][4 * kCh];           // this lane's column's q, in its K chunk order
     };
 
-    static __device__ __forceinline__ void load_q(Q &q, const __nv_bfloat16 *rows, int lane, bool by_head) {
+    static __device__ __forceinline__ void load_q(Q &q, const __nv_bfloat16 *rows, int lane, bool by_head, int part) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int c = nb * 8 + g;
-            const __nv_bfloat16 *row = rows + diff_head_of<G>(c < G ? c : 0, by_head) * d;
+            const int own = nb * 8 + g;      // among this warp's columns
+            const __nv_bfloat16 *row = rows + diff_head_of<G>(own < kCols ? part * kCols + own : 0, by_head) * d;
 #pragma unroll
             for (int idx = 0; idx < kCh; ++idx) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (c < G) v = *reinterpret_cast<const uint4 *>(row + (idx >> 1) * 64 + (2 * t + (idx & 1)) * 8);
+                if (own < kCols) v = *reinterpret_cast<const uint4 *>(row + (idx >> 1) * 64 + (2 * t + (idx & 1)) * 8);
                 q.w[nb][4 * idx + 0] = v.x;
                 q.w[nb][4 * idx + 1] = v.y;
                 q.w[nb][4 * idx + 2] = v.z;
@@ -93,17 +104,17 @@ struct DiffOp {
 
     // One pipeline stage, as stage_compute: 16 tokens, token tok0 + j valid while < tok_end.
     static __device__ __forceinline__ void compute(uint32_t kslot, uint32_t vslot, const Q &q, int tok0, int tok_end,
-                                                   float scale_log2, int lane, State &st) {
+                                                   float scale_log2, int lane, int part, State &st) {
         const int g = lane >> 2, t = lane & 3;
         const int nvalid = tok_end - tok0;
         const bool tail = nvalid < S::TPS;
         float c[2][4];   // by key head
 #pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {
+        for (int kh = 0; kh < (kSplit ? 1 : 2); ++kh) {
             c[kh][0] = c[kh][1] = c[kh][2] = c[kh][3] = 0.f;
 #pragma unroll
             for (int idx = 0; idx < kCh; ++idx) {
-                const int hh = kh * (d / 64) + (idx >> 1), ch = 2 * t + (idx & 1);
+                const int hh = (kh + part) * (d / 64) + (idx >> 1), ch = 2 * t + (idx & 1);
                 const uint4 a = lds128(kslot + chunk_at(row_off<D, BS>(g, hh), ch));
                 const uint4 b = lds128(kslot + chunk_at(row_off<D, BS>(g + 8, hh), ch));
                 const uint32_t *w = &q.w[NB == 2 ? kh : 0][4 * idx];
@@ -112,7 +123,10 @@ struct DiffOp {
             }
         }
         float x[NB][4];
-        if constexpr (NB == 2) {
+        if constexpr (kSplit) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[0][i] = c[0][i];
+        } else if constexpr (NB == 2) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[0][i] = c[0][i];
@@ -210,8 +224,8 @@ struct DiffOp {
     }
 
     // As warp_publish, by map column.
-    static __device__ __forceinline__ void publish(State &st, bool has_work, int lane, int warp, float *cm, float *cl,
-                                                   float *co) {
+    static __device__ __forceinline__ void publish(State &st, bool has_work, int lane, int warp, int part, float *cm,
+                                                   float *cl, float *co) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -223,8 +237,8 @@ struct DiffOp {
             }
 #pragma unroll
             for (int hi = 0; hi < 2; ++hi) {
-                const int c = nb * 8 + 2 * t + hi;
-                if (c >= G) continue;
+                const int own = nb * 8 + 2 * t + hi, c = part * kCols + own;
+                if (own >= kCols) continue;
                 float *dst = co + (warp * G + c) * D;
 #pragma unroll
                 for (int hp = 0; hp < D / 128; ++hp)
@@ -245,6 +259,9 @@ struct DiffOp {
         }
     }
 
+    // (What is summed for each map is written as the operations that are meant: contracted
+    // differently for the two, equal maps would not cancel.)
+
     // A finished row of query pair h (of the whole batch's row `row`): the lane's four
     // components of every 128, already divided by their maps' sums.
     static __device__ __forceinline__ void finish_row(const Params &p, size_t row, int h, int lane,
@@ -255,7 +272,7 @@ struct DiffOp {
         for (int k = 0; k < D / 128; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[k][e] = a[k][e] - lam * b[k][e];
+                x[k][e] = __fmaf_rn(-lam, b[k][e], a[k][e]);
                 ss += x[k][e] * x[k][e];
             }
         float f = p.out_scale;
@@ -282,7 +299,7 @@ struct DiffOp {
                                                          float *o_base, float *ml_base) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const bool by_head = p.by_head != 0;
-        for (int r = warp; r < R; r += kWarps) {
+        for (int r = warp; r < R; r += kWarps * kDiffParts<D, G>) {
             float acc[2][D / 128][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -294,7 +311,7 @@ struct DiffOp {
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     f[w] = M == -INFINITY ? 0.f : fast_exp2(cm[w * G + c] - M);
-                    lsum += cl[w * G + c] * f[w];
+                    lsum = __fmaf_rn(cl[w * G + c], f[w], lsum);
                 }
                 const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
 #pragma unroll
@@ -304,15 +321,15 @@ struct DiffOp {
                     for (int w = 0; w < kWarps; ++w) {
                         const float4 v =
                             *reinterpret_cast<const float4 *>(co + (w * G + c) * D + k * 128 + lane * 4);
-                        s.x += v.x * f[w];
-                        s.y += v.y * f[w];
-                        s.z += v.z * f[w];
-                        s.w += v.w * f[w];
+                        s.x = __fmaf_rn(v.x, f[w], s.x);
+                        s.y = __fmaf_rn(v.y, f[w], s.y);
+                        s.z = __fmaf_rn(v.z, f[w], s.z);
+                        s.w = __fmaf_rn(v.w, f[w], s.w);
                     }
-                    acc[j][k][0] = s.x * inv;
-                    acc[j][k][1] = s.y * inv;
-                    acc[j][k][2] = s.z * inv;
-                    acc[j][k][3] = s.w * inv;
+                    acc[j][k][0] = __fmul_rn(s.x, inv);
+                    acc[j][k][1] = __fmul_rn(s.y, inv);
+                    acc[j][k][2] = __fmul_rn(s.z, inv);
+                    acc[j][k][3] = __fmul_rn(s.w, inv);
                     if (!final)
                         *reinterpret_cast<float4 *>(o_base + (size_t)c * D + k * 128 + lane * 4) =
                             make_float4(acc[j][k][0], acc[j][k][1], acc[j][k][2], acc[j][k][3]);
@@ -327,61 +344,67 @@ struct DiffOp {
     // one's is record 2 ca + first_rec, the others' 2 cc): a warp a query pair.
     static __device__ __forceinline__ void merge(const Params &p, int ca, int cb, int first_rec, size_t row0,
                                                  int pair0, int warp, int nwarps, int lane) {
-        constexpr int kR = 4;   // records loaded together
+        constexpr int kR = 2;   // records of both maps loaded together
         for (int r = warp; r < R; r += nwarps) {
-            float out[2][D / 128][4];
+            float M[2] = {-INFINITY, -INFINITY}, wsum[2] = {0.f, 0.f}, out[2][D / 128][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = diff_column_of<G>(r, j, p.by_head != 0);
-                float M = -INFINITY, wsum = 0.f, acc[D / 128][4];
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int k = 0; k < D / 128; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-                for (int c0 = ca; c0 <= cb; c0 += kR) {
-                    float2 ml[kR];
-                    float4 ov[kR][D / 128];
+                for (int k = 0; k < D / 128; ++k) out[j][k][0] = out[j][k][1] = out[j][k][2] = out[j][k][3] = 0.f;
+            const int c0 = diff_column_of<G>(r, 0, p.by_head != 0), c1 = diff_column_of<G>(r, 1, p.by_head != 0);
+            for (int first = ca; first <= cb; first += kR) {
+                float2 ml[2][kR];
+                float4 ov[2][kR][D / 128];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int q = 0; q < kR; ++q) {
-                        const int cc = c0 + q;
-                        ml[q] = make_float2(-INFINITY, 0.f);
+                        const int cc = first + q;
+                        ml[j][q] = make_float2(-INFINITY, 0.f);
                         if (cc <= cb) {
-                            const size_t rec = 2 * (size_t)cc + (cc == ca ? first_rec : 0);
-                            ml[q] = *reinterpret_cast<const float2 *>(p.ws_ml + (rec * G + c) * 2);
+                            const size_t rec = (2 * (size_t)cc + (cc == ca ? first_rec : 0)) * G + (j == 0 ? c0 : c1);
+                            ml[j][q] = *reinterpret_cast<const float2 *>(p.ws_ml + rec * 2);
 #pragma unroll
                             for (int k = 0; k < D / 128; ++k)
-                                ov[q][k] = *reinterpret_cast<const float4 *>(p.ws_o + (rec * G + c) * D + k * 128 +
-                                                                             lane * 4);
+                                ov[j][q][k] =
+                                    *reinterpret_cast<const float4 *>(p.ws_o + rec * D + k * 128 + lane * 4);
                         }
                     }
-                    float Mn = M;
 #pragma unroll
-                    for (int q = 0; q < kR; ++q) Mn = fmaxf(Mn, ml[q].x);
+                for (int j = 0; j < 2; ++j) {
+                    float Mn = M[j];
+#pragma unroll
+                    for (int q = 0; q < kR; ++q) Mn = fmaxf(Mn, ml[j][q].x);
                     if (Mn == -INFINITY) continue;
-                    const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
-                    wsum *= f;
+                    const float f = M[j] == -INFINITY ? 0.f : fast_exp2(M[j] - Mn);
+                    wsum[j] = __fmul_rn(wsum[j], f);
 #pragma unroll
                     for (int k = 0; k < D / 128; ++k)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[k][e] *= f;
+                        for (int e = 0; e < 4; ++e) out[j][k][e] = __fmul_rn(out[j][k][e], f);
 #pragma unroll
                     for (int q = 0; q < kR; ++q) {
-                        if (ml[q].x == -INFINITY) continue;
-                        const float w = ml[q].y * fast_exp2(ml[q].x - Mn);
-                        wsum += w;
+                        if (ml[j][q].x == -INFINITY) continue;
+                        const float w = __fmul_rn(ml[j][q].y, fast_exp2(ml[j][q].x - Mn));
+                        wsum[j] = __fadd_rn(wsum[j], w);
 #pragma unroll
                         for (int k = 0; k < D / 128; ++k) {
-                            acc[k][0] += w * ov[q][k].x;
-                            acc[k][1] += w * ov[q][k].y;
-                            acc[k][2] += w * ov[q][k].z;
-                            acc[k][3] += w * ov[q][k].w;
+                            out[j][k][0] = __fmaf_rn(w, ov[j][q][k].x, out[j][k][0]);
+                            out[j][k][1] = __fmaf_rn(w, ov[j][q][k].y, out[j][k][1]);
+                            out[j][k][2] = __fmaf_rn(w, ov[j][q][k].z, out[j][k][2]);
+                            out[j][k][3] = __fmaf_rn(w, ov[j][q][k].w, out[j][k][3]);
                         }
                     }
-                    M = Mn;
+                    M[j] = Mn;
                 }
-                const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float inv = wsum[j] > 0.f ? 1.f / wsum[j] : 0.f;
 #pragma unroll
                 for (int k = 0; k < D / 128; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) out[j][k][e] = acc[k][e] * inv;
+                    for (int e = 0; e < 4; ++e) out[j][k][e] = __fmul_rn(out[j][k][e], inv);
             }
             finish_row(p, row0 + r, pair0 + r, lane, out[0], out[1]);
         }

@@ -160,7 +160,7 @@ struct alignas(16) SkSmem {
     float co[kWarps * G * D];         // warps' numerators
     __nv_bfloat16 q[2][G * DQ];       // q of the current and next unit
     int seg_s[kMaxSegs], seg_g[kMaxSegs], seg_kb[kMaxSegs], seg_ke[kMaxSegs], seg_lb[kMaxSegs + 1];
-    int scan[kWarps];                 // block-scan scratch
+    int scan[2 * kWarps];             // block-scan scratch
     int found_s, found_base, nseg, more, next_pos;
     uint64_t qbar[2];
 };
@@ -594,15 +594,15 @@ struct PlainOp {
     struct Q {
         uint32_t w[D / 8];
     };
-    static __device__ __forceinline__ void load_q(Q &q, const __nv_bfloat16 *rows, int lane, bool) {
+    static __device__ __forceinline__ void load_q(Q &q, const __nv_bfloat16 *rows, int lane, bool, int) {
         load_qf<D, G, true>(q.w, rows, lane);
     }
     static __device__ __forceinline__ void compute(uint32_t kslot, uint32_t vslot, const Q &q, int tok0, int tok_end,
-                                                   float scale_log2, int lane, State &st) {
+                                                   float scale_log2, int lane, int, State &st) {
         stage_compute<D, G, BS>(kslot, vslot, q.w, tok0, tok_end, scale_log2, lane, st);
     }
-    static __device__ __forceinline__ void publish(State &st, bool has_work, int lane, int warp, float *cm, float *cl,
-                                                   float *co) {
+    static __device__ __forceinline__ void publish(State &st, bool has_work, int lane, int warp, int, float *cm,
+                                                   float *cl, float *co) {
         warp_publish<D, G>(st, has_work, lane, warp, cm, cl, co);
     }
 };
@@ -788,6 +788,20 @@ __global__ void __launch_bounds__(G *D / 4) paged_decode_reduce_kernel(const Par
 
 // ---- stream-K kernel -------------------------------------------------------------
 
+// Two warps meet on named barrier `id`; whether `mine` holds in both.
+__device__ __forceinline__ bool pair_and(int id, bool mine) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)mine), "r"(id)
+        : "memory");
+    return all != 0;
+}
+
 // Stages of one sequence (one kv-head); lengths validated as in effective_len.
 template <int BS>
 __device__ __forceinline__ int seq_stages(const Params &p, int s, bool report) {
@@ -800,8 +814,9 @@ __device__ __forceinline__ int seq_stages(const Params &p, int s, bool report) {
 // work order: its stages, then kUnitCost stages of no work (none if empty).
 __device__ __forceinline__ int unit_span(int ns) { return ns > 0 ? ns + kUnitCost : 0; }
 
-// Inclusive block-wide scan of one int per thread (kWarps * 32 threads); also
+// Inclusive block-wide scan of one int per thread (NW * 32 threads); also
 // returns the block total.  Safe to call back to back (it synchronises first).
+template <int NW>
 __device__ __forceinline__ int block_inclusive_scan(int v, int *scratch, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -814,7 +829,7 @@ __device__ __forceinline__ int block_inclusive_scan(int v, int *scratch, int &to
     __syncthreads();
     int offset = 0, tot = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < NW; ++w) {
         const int x = scratch[w];
         offset += w < warp ? x : 0;
         tot += x;
@@ -824,14 +839,18 @@ __device__ __forceinline__ int block_inclusive_scan(int v, int *scratch, int &to
 }
 
 // Differential attention (kDiff): D is two heads wide, G = 2R map columns, and a
-// "kv-head" g is the pair of KV heads (2g, 2g + 1).  Two CTAs an SM where the rings
-// allow it (D = 256: one, with twice the bytes a stage).
+// "kv-head" g is the pair of KV heads (2g, 2g + 1); kSkParts warps share a ring.  Two CTAs
+// an SM where the rings allow it (D = 256: one, with twice the bytes a stage).
+template <int D, int G, bool kDiff>
+constexpr int kSkParts = kDiff ? kDiffParts<D, G> : 1;
+
 template <int D, int G, int BS, bool kDiff = false>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
+__global__ void __launch_bounds__(kWarps * kSkParts<D, G, kDiff> * 32, D == 256 ? 1 : kMinCtas)
     paged_decode_sk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                            const Params p) {
     using S = Shape<D, BS>;
     using WR = WarpRing<D, BS, kSkStages>;
+    constexpr int kParts = kSkParts<D, G, kDiff>;     // warps that share a ring
     using SP = SmemPlan<D, BS, kSkStages>;
     constexpr int DQ = kDiff ? D / 2 : D;      // components of a query row
     constexpr int HB = kDiff ? 2 : 1;          // KV heads of a copy box
@@ -839,14 +858,16 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
     using Op = typename std::conditional<kDiff, DiffOp<D, G, BS>, PlainOp<D, G, BS>>::type;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = align1024(smem_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int warp = kParts == 1 ? tid >> 5 : (tid >> 5) % kWarps;   // whose ring
+    const int part = kParts == 1 ? 0 : (tid >> 5) / kWarps;
     const uint32_t ring = smem_addr(smem) + warp * (uint32_t)sizeof(WR);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + SP::kRings) + warp * kSkStages;
     SK *sk = reinterpret_cast<SK *>(smem + SP::kRings + SP::kBars);
-    constexpr int NT = kWarps * 32;
+    constexpr int NW = kWarps * kParts, NT = NW * 32;
     const int Hkv = p.num_kv_heads, B = p.num_seqs, c = blockIdx.x;
 
-    if (lane == 0) {
+    if (lane == 0 && part == 0) {
 #pragma unroll
         for (int st = 0; st < kSkStages; ++st) mbar_init(&bar[st], 1);
         if (warp == 0) {
@@ -873,7 +894,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
         const int ns = s < B ? seq_stages<BS>(p, s, c == 0) : 0;
         const int v = Hkv * unit_span(ns);
         int chunk;
-        const int inc = block_inclusive_scan(v, sk->scan, chunk);
+        const int inc = block_inclusive_scan<NW>(v, sk->scan, chunk);
         my_ns = ns;
         my_first = total + inc - v;
         total += chunk;
@@ -897,7 +918,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
             const int s = base + tid;
             const int v = s < B ? Hkv * unit_span(seq_stages<BS>(p, s, false)) : 0;
             int chunk;
-            const int inc = block_inclusive_scan(v, sk->scan, chunk);
+            const int inc = block_inclusive_scan<NW>(v, sk->scan, chunk);
             const int excl = run + inc - v;
             if (s < B && v > 0 && excl <= gs && gs < excl + v) {
                 sk->found_s = s;
@@ -935,8 +956,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
                 r += min(ge, u0 + my_ns) - max(pos, u0);
             }
             int nall, rall;
-            const int base = block_inclusive_scan(n, sk->scan, nall) - n;
-            int local = block_inclusive_scan(r, sk->scan, rall) - r;
+            const int base = block_inclusive_scan<NW>(n, sk->scan, nall) - n;
+            int local = block_inclusive_scan<NW>(r, sk->scan, rall) - r;
             for (int k = 0; k < n; ++k) {
                 const int idx = base + k;
                 if (idx > kMaxSegs) break;
@@ -1051,7 +1072,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
                              : "memory");
             }
 #pragma unroll 1
-            for (int k = 0; k < kSkPrefetch && k < my_n && (k + 1) * S::BPS <= 32; ++k) {
+            for (int k = 0; part == 0 && k < kSkPrefetch && k < my_n && (k + 1) * S::BPS <= 32; ++k) {
                 const int i = warp + k * kWarps;
                 int j = 0;
                 while (j + 1 < nseg && sk->seg_lb[j + 1] <= i) ++j;
@@ -1082,7 +1103,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
             issue_q(1);
         }
         auto issue = [&](int k) {   // warp-uniform k
-            if (k >= my_n) return;
+            if (k >= my_n || part != 0) return;
             if (k * S::BPS - kb_base >= 32) {
                 kb_base = k * S::BPS;
                 id_cache = load_ids(kb_base);
@@ -1172,7 +1193,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
                 break;
             }
             typename Op::Q qf;
-            Op::load_q(qf, sk->q[jg & 1], lane, p.by_head != 0);
+            Op::load_q(qf, sk->q[jg & 1], lane, p.by_head != 0, part);
             typename Op::State st;
             st.reset();
             const int lend = sk->seg_lb[j + 1];
@@ -1182,19 +1203,28 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : kMinCtas)
                 const int slot = (kq + k) % kSkStages;
                 const bool arrived =
                     mbar_wait_bounded(&bar[slot], (uint32_t)(((kq + k) / kSkStages) & 1), p.err);
-                if (!__all_sync(0xffffffffu, arrived)) {
+                const bool here = __all_sync(0xffffffffu, arrived);
+                if (kParts == 1 && !here) {
                     ok = false;
                     break;
                 }
                 const int tok0 = (sk->seg_kb[j] + i - sk->seg_lb[j]) * S::TPS;
-                Op::compute(ring + slot * S::SLOT, ring + (kSkStages + slot) * S::SLOT, qf, tok0, L, p.scale_log2,
-                            lane, st);
-                __syncwarp();   // every lane is done with the slot before it is refilled
+                if (kParts == 1 || here)
+                    Op::compute(ring + slot * S::SLOT, ring + (kSkStages + slot) * S::SLOT, qf, tok0, L, p.scale_log2,
+                                lane, part, st);
+                // every lane, of both warps where they share a ring, is done with the slot
+                // before it is refilled (and two warps give up together)
+                if constexpr (kParts == 1) {
+                    __syncwarp();
+                } else if (!pair_and(1 + warp, here)) {
+                    ok = false;
+                    break;
+                }
                 issue(k + kSkStages);
                 ++k;
                 ++done;
             }
-            Op::publish(st, done > 0, lane, warp, sk->cm, sk->cl, sk->co);
+            Op::publish(st, done > 0, lane, warp, part, sk->cm, sk->cl, sk->co);
             if (!__syncthreads_and(ok)) {
                 ok = false;
                 break;
@@ -1546,8 +1576,8 @@ cudaError_t launch_diff_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, co
     static bool configured[64] = {};
     cudaError_t e = ensure_smem(paged_decode_sk_kernel<D, G, BS, true>, smem, configured);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(paged_decode_sk_kernel<D, G, BS, true>, dim3(prm.num_ctas), dim3(kWarps * 32), smem, stream, tmk,
-                   tmv, prm);
+    e = launch_pdl(paged_decode_sk_kernel<D, G, BS, true>, dim3(prm.num_ctas),
+                   dim3(kWarps * kSkParts<D, G, true> * 32), smem, stream, tmk, tmv, prm);
     if (e != cudaSuccess) return e;
     return launch_pdl(paged_decode_sk_merge_kernel<D, G, BS, true>, dim3(prm.num_ctas), dim3(kMergeThreads), 0, stream,
                       prm);
