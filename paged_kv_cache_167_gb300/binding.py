@@ -576,6 +576,12 @@ def rotary_turns(angular) -> np.ndarray:
     return out
 
 
+class RotaryAxes(np.ndarray):
+    """The axis of each pair, with its address at hand: numpy takes a microsecond to
+    tell it, a tenth of a call."""
+    address = None
+
+
 def rotary_axes(sections: Sequence[int], order: str = "blocks") -> np.ndarray:
     """pa_rotary_sections: the axis of each pair (uint8 numpy array, ``axes`` of
     rotate and rotate_and_cache) for axes that own sections[a] pairs each.  order:
@@ -583,7 +589,8 @@ def rotary_axes(sections: Sequence[int], order: str = "blocks") -> np.ndarray:
     if order not in AXES_ORDERS:
         raise ValueError(f"order must be one of {sorted(AXES_ORDERS)}")
     own = np.ascontiguousarray(sections, dtype=np.int32).reshape(-1)
-    out = np.empty(max(int(own.sum()), 1), dtype=np.uint8)
+    out = np.empty(max(int(own.sum()), 1), dtype=np.uint8).view(RotaryAxes)
+    out.address = out.ctypes.data
     _check(lib().pa_rotary_sections(own.ctypes.data_as(_P), len(own), AXES_ORDERS[order], int(own.sum()),
                                     out.ctypes.data_as(_P)), "pa_rotary_sections")
     return out
@@ -591,7 +598,7 @@ def rotary_axes(sections: Sequence[int], order: str = "blocks") -> np.ndarray:
 
 def _axes(axes: np.ndarray, positions: torch.Tensor, n: int, freqs: torch.Tensor, device: int):
     """(description, address of the positions) of int64 [num_axes][tokens]."""
-    if not isinstance(axes, np.ndarray) or axes.dtype != np.uint8 or not axes.flags.c_contiguous:
+    if not isinstance(axes, np.ndarray) or axes.dtype.char != "B" or not axes.flags.c_contiguous:
         raise TypeError("axes must be a contiguous uint8 numpy array (rotary_axes)")
     if axes.size != freqs.numel():
         raise ValueError("axes must name one axis a pair")
@@ -602,7 +609,8 @@ def _axes(axes: np.ndarray, positions: torch.Tensor, n: int, freqs: torch.Tensor
     s0, s1 = positions.stride()
     if n > 1 and (s1 != 1 or (positions.shape[0] > 1 and s0 < n)):
         raise ValueError("each axis's positions must be dense")
-    return PaRotaryAxes(axes.ctypes.data, positions.shape[0], s0 if positions.shape[0] > 1 else 0), \
+    address = axes.address if type(axes) is RotaryAxes else None   # (a slice or copy has none of its own)
+    return PaRotaryAxes(address or axes.ctypes.data, positions.shape[0], s0 if positions.shape[0] > 1 else 0), \
         positions.data_ptr()
 
 

@@ -11,8 +11,11 @@
 //
 // With positions of several axes (time, height, width: pair i is turned by the
 // position on axis(i)) a thread loads the token's position on every axis beside its
-// components and picks one a pair by a two-bit code from the parameters; nothing
-// else differs.
+// components and picks one a pair by a two-bit code from the parameters.  It takes as
+// many registers as leave an SM the CTAs it has with one axis (8,192 tokens of 64/8 heads of
+// 128, three axes: 53.9 us, 58.3 with one CTA fewer), and where a token's heads are
+// few a CTA takes several tokens, so that a thread still has several heads to one set of
+// angles (5,001 tokens of 16 heads of 80: 5.9 us, 8.1 with a head a thread).
 //
 // What bounds it: every component is read and written once (two operations a
 // byte), so DRAM, and the host's call where tokens are few.  GB300, of the measured
@@ -45,6 +48,7 @@ struct RotateParams {
     int32_t chunks;              // rot_chunks + (d - rot_dim) / V
     float mscale;
     int32_t inverse;
+    int64_t num_tokens;
     unsigned int *err;
 };
 
@@ -52,16 +56,25 @@ struct OneAxis {};   // in AxesView's place where every pair is turned by the sa
 
 constexpr int kRotateThreads = 128;
 
-// grid (tokens, head groups of Y * U, chunk groups), block (X, Y).
+// The CTAs an SM that a thread of U heads leaves room for (0: no bound).
+template <int V, int U, class Axes>
+constexpr int kRotateCtas =
+    V != 8 || std::is_same<Axes, OneAxis>::value ? 0 : U == 5 ? 5 : U == 4 ? 6 : U == 3 ? 8 : U == 2 ? 9 : 0;
+
+// grid (tokens / Z, head groups of Y * U, chunk groups), block (X, Y, Z); Z is 1 with one axis.
 template <int V, bool INTERLEAVED, int U, bool CACHE, class Axes>
-__global__ void __launch_bounds__(kRotateThreads)
+__global__ void __launch_bounds__(kRotateThreads, kRotateCtas<V, U, Axes>)
     rotate_kernel(const RotateParams p, const __grid_constant__ Axes axes) {
     using Vec = typename BfVec<V>::type;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int64_t n = blockIdx.x;
+    int64_t n = blockIdx.x;
     const int c = blockIdx.z * blockDim.x + threadIdx.x;
     if (c >= p.chunks) return;
+    if constexpr (!std::is_same<Axes, OneAxis>::value) {
+        n = n * blockDim.z + threadIdx.z;
+        if (n >= p.num_tokens) return;
+    }
     const bool turning = c < p.rot_chunks;
     const int half = p.rot_chunks * V;
     // where the chunk's first vector lies in a head, and its second one
@@ -153,7 +166,19 @@ cudaError_t launch_rotate_v(RotateParams &p, const Axes &axes, int64_t tokens, c
     // us, with several 2.8.
     const int rows = (heads + y - 1) / y, groups = (rows + 5) / 6, most = (rows + groups - 1) / groups;
     const bool wide = tokens * groups * gz >= 4ll * device_sm_count();
-    const int u = wide ? (V == 8 ? most : most > 2 ? 4 : most) : 1;
+    int u = wide ? (V == 8 ? most : most > 2 ? 4 : most) : 1;
+    if constexpr (!std::is_same<Axes, OneAxis>::value) {
+        // few heads: up to four a thread, and the CTA's other threads on further tokens
+        const int few = heads < 4 ? heads : 4, fy = (heads + few - 1) / few, z = kRotateThreads / (x * fy);
+        if (V == 8 && u == 1 && few > 1 && z > 1 && (tokens + z - 1) / z * gz >= 4ll * device_sm_count()) {
+            const dim3 fgrid((unsigned)((tokens + z - 1) / z), 1, gz), fblock(x, fy, z);
+            switch (few) {
+                case 2: return launch_pdl(rotate_kernel<V, INTERLEAVED, 2, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
+                case 3: return launch_pdl(rotate_kernel<V, INTERLEAVED, 3, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
+                default: return launch_pdl(rotate_kernel<V, INTERLEAVED, 4, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
+            }
+        }
+    }
     const dim3 grid((unsigned)tokens, (unsigned)((heads + y * u - 1) / (y * u)), gz), block(x, y);
     if constexpr (V == 8) {
         switch (u) {
@@ -174,6 +199,7 @@ template <bool CACHE, class Axes>
 cudaError_t launch_rotate_any(RotateParams &p, const Axes &axes, int32_t rot_dim, bool interleaved, int64_t tokens,
                               cudaStream_t stream) {
     const int v = rotary_vec(rot_dim);
+    p.num_tokens = tokens;
     p.rot_chunks = rot_dim / 2 / v;
     p.chunks = p.rot_chunks + (p.d - rot_dim) / v;
     switch (v) {

@@ -317,6 +317,46 @@ def test_rotate_axes_of_equal_positions_is_one_axis(pa):
     assert np.array_equal(bits(one), bits(three))
 
 
+@pytest.mark.parametrize("heads,d,rot", [(1, 128, 128), (2, 128, 64), (3, 80, 48), (5, 64, 64), (16, 80, 48),
+                                         (9, 1024, 1024), (80, 128, 128), (31, 64, 32)])
+def test_rotate_axes_many_tokens(pa, heads, d, rot):
+    """Calls that fill the GPU, few heads and many: each axis on its own gives, for its pairs,
+    the bits of the call with that axis's position for all."""
+    n = 6007 if heads < 80 else 700
+    x = normal((n, heads, d), seed=heads)
+    axis = pa.rotary_axes([rot // 2 - rot // 4 - 1, rot // 4, 1], "cycled")
+    pos = torch.stack([torch.arange(n, device="cuda") * 3, torch.arange(n, device="cuda") // 7 + 10 ** 6,
+                       5 - torch.arange(n, device="cuda")])
+    freqs = cuda(pa.rotary_frequencies(rot))
+    got, one = torch.empty_like(x), torch.empty_like(x)
+    pa.rotate(got, x, pos, freqs, axes=axis)
+    for a in range(3):
+        pa.rotate(one, x, pos[a].contiguous(), freqs)
+        pairs = cuda(np.nonzero(axis == a)[0])
+        for part in (pairs, pairs + rot // 2):
+            assert torch.equal(got[:, :, part].view(torch.int16), one[:, :, part].view(torch.int16))
+    assert torch.equal(got[:, :, rot:], x[:, :, rot:]) and pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (0, 2), (4, 2), (64, 8)])
+def test_rotate_and_cache_axes_many_tokens(pa, hq, hkv):
+    """The same with the slot writer, against the call with one axis: equal positions."""
+    n, d, b = 5003, 128, 16
+    q, k, v = normal((n, max(hq, 1), d), seed=1), normal((n, hkv, d), seed=2), normal((n, hkv, d), seed=3)
+    slots = torch.randperm(5008, generator=torch.Generator().manual_seed(4))[:n].cuda()
+    slots[::5] = -1
+    pos = torch.arange(n, device="cuda") + 77
+    freqs = cuda(pa.rotary_frequencies(d))
+    pools, outs = [], []
+    for axes in (None, pa.rotary_axes([16, 24, 24])):
+        pool, out = torch.zeros((313, 2, hkv, b, d), dtype=torch.bfloat16, device="cuda"), torch.zeros_like(q)
+        pa.rotate_and_cache(pool, out if hq else None, q if hq else None, k, v,
+                            pos if axes is None else pos.expand(3, n).contiguous(), slots, freqs, axes=axes)
+        pools.append(pool)
+        outs.append(out)
+    assert torch.equal(pools[0], pools[1]) and torch.equal(outs[0], outs[1]) and pa.get_device_error() == 0
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotate_axes_inverse_is_the_gradient(pa, interleaved):
     """R^T g by the inverse call, against the formula and against the columns of R (the
