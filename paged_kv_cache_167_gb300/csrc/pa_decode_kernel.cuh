@@ -1284,11 +1284,18 @@ constexpr int kMergeThreads = PA_MERGE_THREADS;
 // uneven placement of warps: at 56, some SMs kept the next call's decode CTAs
 // waiting for merge blocks to exit (34.93 against 34.43 us a call on the
 // Llama-shaped batch).
+// Differential attention: a warp merges both maps of a query pair at a time, so a unit
+// of eight pairs has eight warps (64 x 600-850 tokens, 64/8 heads, d = 128: 40.2 us a call,
+// 42.5 with four).
+template <int G, bool kDiff>
+constexpr int kMergeWide = kDiff && G == 16 ? 2 : 1;
+
 template <int D, int G, int BS, bool kDiff = false>
-__global__ void __launch_bounds__(kMergeThreads, kDiff ? 4 : PA_MERGE_MIN_BLOCKS)
+__global__ void __launch_bounds__(kMergeThreads *kMergeWide<G, kDiff>,
+                                  kDiff ? 4 / kMergeWide<G, kDiff> : PA_MERGE_MIN_BLOCKS)
     paged_decode_sk_merge_kernel(const Params p) {
     grid_launch_dependents();   // the next kernel waits for this grid's completion before using its data
-    constexpr int NT = kMergeThreads, NW = NT / 32;
+    constexpr int NT = kMergeThreads * kMergeWide<G, kDiff>, NW = NT / 32;
     __shared__ int scan[NW];
     __shared__ int found[3];    // sequence, kv-head and work position of the unit to merge (sequence -1: none)
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1579,8 +1586,8 @@ cudaError_t launch_diff_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, co
     e = launch_pdl(paged_decode_sk_kernel<D, G, BS, true>, dim3(prm.num_ctas),
                    dim3(kWarps * kSkParts<D, G, true> * 32), smem, stream, tmk, tmv, prm);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_decode_sk_merge_kernel<D, G, BS, true>, dim3(prm.num_ctas), dim3(kMergeThreads), 0, stream,
-                      prm);
+    return launch_pdl(paged_decode_sk_merge_kernel<D, G, BS, true>, dim3(prm.num_ctas),
+                      dim3(kMergeThreads * kMergeWide<G, true>), 0, stream, prm);
 }
 
 template <int D, int G>

@@ -731,9 +731,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         x[q][4 * i + 3] += v.w;
                     }
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+                for (int q = 0; q < 2; ++q) {
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};   // four chains, not one as long as the row
 #pragma unroll
-                    for (int i = 0; i < W; ++i) ss += x[q][i] * x[q][i];
+                    for (int i = 0; i < W; ++i) s4[i & 3] += x[q][i] * x[q][i];
+                    ss += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                }
             }
             float scale = p.out_scale;
             if (p.norm_weight != nullptr) {
