@@ -168,6 +168,36 @@ def test_extend_nothing(pa):
     s.check(pa)
 
 
+@pytest.mark.parametrize("n,room,b", [(600, 0, 16), (4096, 100000, 7), (20011, 50, 16), (70001, 0, 32), (300000, 9, 16)])
+def test_extend_many_sequences(pa, n, room, b):
+    """Sequences by the thousands, with and without a range of places for each CTA of a
+    cluster, pieces of more than 128; against sums of the lengths."""
+    rng = np.random.default_rng(n)
+    ctx = rng.integers(0, 3 * b, size=n)
+    new = rng.choice([0, 1, 1, 1, 2, 9], size=n)
+    have, end = -(-ctx // b), -(-(ctx + new) // b)
+    need = end - have
+    ids = rng.permutation(int(end.sum()) + 10)
+    tables = np.full((n, 5), -1, np.int64)
+    tables[np.arange(5)[None, :] < have[:, None]] = ids[:have.sum()]
+    s = Step(tables, ctx, new, ids[have.sum():], 3, b, len(ids), int(new.sum()) + room)
+    s.call(pa)
+    first = np.cumsum(new) - new
+    assert np.array_equal(s.starts.cpu().numpy(), np.append(first, new.sum()))
+    assert np.array_equal(s.lens.cpu().numpy(), ctx + new) and s.cursor_out.item() == 3 + need.sum()
+    fresh = (np.arange(5)[None, :] >= have[:, None]) & (np.arange(5)[None, :] < end[:, None])
+    tables[fresh] = ids[have.sum() + 3:][:need.sum()]      # row by row, in the sequences' order
+    assert np.array_equal(s.tables.cpu().numpy(), tables)
+    seq = np.repeat(np.arange(n), new)
+    pos = ctx[seq] + np.arange(len(seq)) - first[seq]
+    want = np.full(s.slots.numel(), -1)
+    want[:len(seq)] = tables[seq, pos // b] * b + pos % b
+    assert np.array_equal(s.slots.cpu().numpy(), want)
+    want[:] = 0
+    want[:len(seq)] = pos
+    assert np.array_equal(s.positions.cpu().numpy(), want) and pa.get_device_error() == 0
+
+
 def test_extend_many_sequences_far_tables(pa):
     """More sequences than a scan holds by far, and a table row beyond 2^31 bytes."""
     s = make(20000, 16, 3, ONE, seed=5, width=2)
