@@ -564,10 +564,12 @@ pa_status pa_decode_diff(void *out, const void *q, const pa_kv_pool *pool, const
  * queries, positions and causal mask.
  *   out          device, [num_seqs][chunk_len][num_q_heads / 2][2 * head_dim] bf16
  *   q, block_tables, ctx_lens, max_ctx_len, scale  as pa_prefill_chunk
- * The chunk's own K/V must already be in the pool.  Both products run on the tcgen05
- * tensor cores with fp32 accumulation, a cluster of two CTAs a tile of queries, one
- * for each map; a probability is rounded to bf16 (relative 2^-8, its sum is not), the
- * difference and the norm are fp32, and out is rounded once.
+ * The chunk's own K/V must already be in the pool, finite at every position up to
+ * ctx_lens[s] + chunk_len - 1 (a value that the mask hides from a query is multiplied by
+ * zero, which an infinity or NaN survives; slots behind that may hold anything).  Both
+ * products run on the tcgen05 tensor cores with fp32 accumulation, a cluster of two
+ * CTAs a tile of queries, one for each map; a probability is rounded to bf16 (relative
+ * 2^-8, its sum is not), the difference and the norm are fp32, and out is rounded once.
  * Supported: head_dim 64 or 128; an even num_kv_heads; R 1, 2, 4 or 8; block_size 8, 16,
  * 32 or 64; at most 65,535 sequences.  Errors as pa_prefill_chunk;
  * PA_ERR_INVALID_ARG for a bad pa_diff.

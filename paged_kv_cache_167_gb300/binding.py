@@ -699,14 +699,18 @@ def extend_tables(block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens
         raise ValueError("positions and slot_mapping must be of one size, cursor and cursor_out one number")
     dev = torch.cuda.current_device()
     i32, i64 = torch.int32, torch.int64
-    _check(lib().pa_extend_tables(
-        _at(block_tables, i32, "block_tables", dev), W, _at(seq_lens, i32, "seq_lens", dev),
-        _at(cu_seqlens, i32, "cu_seqlens", dev), _at(positions, i64, "positions", dev),
-        _at(slot_mapping, i64, "slot_mapping", dev), slot_mapping.numel(), _at(ctx_lens, i32, "ctx_lens", dev),
-        _at(new_lens, i32, "new_lens", dev),
-        _at(position_offsets, i32, "position_offsets", dev) if position_offsets is not None else None, B,
-        _at(free_blocks, i32, "free_blocks", dev), free_blocks.numel(), _at(cursor, i32, "cursor", dev),
-        _at(cursor_out, i32, "cursor_out", dev), block_size, num_blocks, _handle(stream, dev)), "pa_extend_tables")
+    # (eleven arrays: checked in line, a fifth of the call; _at says what is wrong with one)
+    tables, lens, starts, pos, slots, ctx, new, free, cur, cur_out = [
+        t.data_ptr() if t.dtype is kind and t.get_device() == dev and t.is_contiguous() else _at(t, kind, name, dev)
+        for t, kind, name in ((block_tables, i32, "block_tables"), (seq_lens, i32, "seq_lens"),
+                              (cu_seqlens, i32, "cu_seqlens"), (positions, i64, "positions"),
+                              (slot_mapping, i64, "slot_mapping"), (ctx_lens, i32, "ctx_lens"),
+                              (new_lens, i32, "new_lens"), (free_blocks, i32, "free_blocks"),
+                              (cursor, i32, "cursor"), (cursor_out, i32, "cursor_out"))]
+    offsets = _at(position_offsets, i32, "position_offsets", dev) if position_offsets is not None else None
+    _check(lib().pa_extend_tables(tables, W, lens, starts, pos, slots, slot_mapping.numel(), ctx, new, offsets, B, free,
+                                  free_blocks.numel(), cur, cur_out, block_size, num_blocks, _handle(stream, dev)),
+           "pa_extend_tables")
 
 
 def compact_tokens(pool: torch.Tensor, src_tables: torch.Tensor, dst_tables: torch.Tensor, seq_lens: torch.Tensor,

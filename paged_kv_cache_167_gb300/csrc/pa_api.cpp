@@ -374,6 +374,7 @@ pa_status pa_prefill_diff(void *out, const void *q, const pa_kv_pool *pool, cons
     if (!out || !q || !block_tables || !ctx_lens || max_blocks_per_seq <= 0) return PA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(q) || !std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
     if ((int64_t)max_ctx_len + chunk_len > (int64_t)max_blocks_per_seq * view.block_size) return PA_ERR_INVALID_ARG;
+    if ((int64_t)max_ctx_len + chunk_len > (int64_t)INT32_MAX - 256) return PA_ERR_INVALID_ARG;   // whole tiles
     PrefillArgs a;
     a.out = out;
     a.q = q;

@@ -16,16 +16,18 @@
 // score MMA: the first R of them read K1, the others K2.  Up to R = 4 all 2R columns fit
 // one n8 tile, which meets both key heads, and each column keeps the product with its own
 // (a product with zeros instead would carry another head's infinities over).  R = 8 has
-// a tile for each key head, at d = 128 in a warp of its own.  The values are staged once and serve every column, so every byte of the
-// cache is read once; what the difference needs of two maps meets only where a unit's
-// rows are finished: one warp a query pair holds both maps' sums of a whole row, so
-// the norm is one warp reduction.
+// a tile for each key head, at d = 128 in a warp of its own.  The values are staged once
+// and serve every column, so every byte of the cache is read once; what the difference
+// needs of two maps meets only where a unit's rows are finished: one warp a query pair
+// holds both maps' sums of a whole row, so the norm is one warp reduction.
 //
 // The probabilities enter P.V as two bf16 terms, as in the plain kernel: the
 // difference of two maps is smaller than either, and the norm scales it up again, so
 // a rounding of p (2^-9) would weigh more here than there.
 //
-// What bounds it: DRAM, as the plain kernel.
+// What bounds it: DRAM, as the plain kernel.  GB300, of the measured copy bandwidth: 4 x
+// 32,768 tokens of 32/8 heads, d = 128, 87 us (0.91); 64 x 600-850 of 64/8 40.2 us (0.71: the
+// start, a unit's end to every 46 stages, the merge behind); 33 x 1-3,000, d = 64, 37 us (0.81).
 #pragma once
 
 namespace pa {

@@ -194,10 +194,9 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
 // S ready[2] (a K slot is free with it), P ready[2][half of the keys], P.V done[2] (a S
 // buffer is free with it), V half free[4] (in both CTAs: two arrivals), Q free, unit's P.V
 // done (in both CTAs), O read, the two MMA lanes' drains; then full[8] (the other CTA's
-// data for a warp has landed),
-// norm[4] (its partial sums of squares of a lane quadrant's rows), out[2] (a unit's
-// output is staged in its last value slots, or written: by unit parity), other out[2]
-// (the other CTA's is stored).
+// data for a warp has landed), norm[4] (its partial sums of squares of a lane quadrant's
+// rows), out[2] (a unit's output is staged in its last value slots, or written: by unit
+// parity), other out[2] (the other CTA's is stored).
 // The tiles of the CTA's units are numbered T = 0, 1, ...; its value halves H = 2T, 2T + 1.
 template <int DH, int G, int BS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -216,10 +215,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t base = smem_addr(smem_raw);
     const uint32_t sQ = base + SM::kOffQ, sK = base + SM::kOffK, sV = base + SM::kOffV;
     const uint32_t barQ = base + SM::kOffBar, barK = barQ + 8, barV = barK + 16, barS = barV + 8 * kVS,
-                   barP = barS + 16, barOP = barP + 32, barVfree = barOP + 16, barQfree = barVfree + 8 * kVS, barUnit = barQfree + 8,
-                   barOfree = barUnit + 8, barEnd = barOfree + 8, barEndQk = barEnd + 8, barFull = barEndQk + 8,
-                   barNorm = barFull + 64, barOut = barNorm + 32,
-                   barOtherOut = barOut + 16;
+                   barP = barS + 16, barOP = barP + 32, barVfree = barOP + 16, barQfree = barVfree + 8 * kVS,
+                   barUnit = barQfree + 8, barOfree = barUnit + 8, barEnd = barOfree + 8, barEndQk = barEnd + 8,
+                   barFull = barEndQk + 8, barNorm = barFull + 64, barOut = barNorm + 32, barOtherOut = barOut + 16;
     constexpr int kNumBars = 1 + 2 + kVS + 2 + 4 + 2 + kVS + 1 + 1 + 1 + 1 + 1 + 8 + 4 + 2 + 2;
     static_assert(8 * kNumBars + 8 <= 384, "barrier area");
     static_assert(kVS == 4, "two tiles of value halves");
@@ -305,138 +303,141 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- copy warps: a lane per box, block ids in registers a load of 32 ahead.  The
         // K warp copies tiles of NBK blocks, the V warp halves of NBV.
         auto copy = [&](auto which) {
-        constexpr bool is_k = decltype(which)::value;
-        constexpr int nb = is_k ? NBK : NBV, per_tile = is_k ? 1 : 2, spl = 32 / nb, slots = is_k ? 2 : kVS;
-        const uint32_t bar0 = is_k ? barK : barV, free0 = is_k ? barS : barVfree;
-        auto ids_load = [&](const Unit &U, int c) -> int {
-            const int bi = c * 32 + lane;
-            return bi < U.nblk && bi < U.n_tiles * NBK ? __ldg(p.tables + (size_t)U.s * p.max_blocks + bi) : 0;
-        };
-        auto ids_check = [&](int v, const Unit &U, int c) -> int {   // out-of-bounds coordinate: zero fill
-            const int bi = c * 32 + lane;
-            if (!(bi < U.nblk && bi < U.n_tiles * NBK)) return (int)p.num_blocks;
-            if (v < 0 || v >= p.num_blocks) {
-                raise_error(p.err, PA_DEVERR_BLOCK_ID);
-                return (int)p.num_blocks;
-            }
-            return v;
-        };
-        // Unit x's output, from its value slot to memory; then both CTAs' value slots of the
-        // unit are free for copies from either (V warp; every unit once, in order: two barriers
-        // by parity, so that none is lapped).
-        int out_slot[2] = {0, 0};
-        auto store_out = [&](int x) -> bool {
-            const bool done = __all_sync(0xffffffffu, mbar_wait(barOut + 8 * (x & 1), (uint32_t)((x >> 1) & 1), p.err));
-            const Unit Y = unit(x);
-            if (done && Y.j0 + min(QPT, p.chunk) <= p.chunk) {
-                if (lane == 0) {
-                    const uint32_t src = sV + (uint32_t)(x & 1 ? out_slot[1] : out_slot[0]) * SM::kVHalf;
+            constexpr bool is_k = decltype(which)::value;
+            constexpr int nb = is_k ? NBK : NBV, per_tile = is_k ? 1 : 2, spl = 32 / nb, slots = is_k ? 2 : kVS;
+            const uint32_t bar0 = is_k ? barK : barV, free0 = is_k ? barS : barVfree;
+            auto ids_load = [&](const Unit &U, int c) -> int {
+                const int bi = c * 32 + lane;
+                return bi < U.nblk && bi < U.n_tiles * NBK ? __ldg(p.tables + (size_t)U.s * p.max_blocks + bi) : 0;
+            };
+            auto ids_check = [&](int v, const Unit &U, int c) -> int {   // out-of-bounds coordinate: zero fill
+                const int bi = c * 32 + lane;
+                if (!(bi < U.nblk && bi < U.n_tiles * NBK)) return (int)p.num_blocks;
+                if (v < 0 || v >= p.num_blocks) {
+                    raise_error(p.err, PA_DEVERR_BLOCK_ID);
+                    return (int)p.num_blocks;
+                }
+                return v;
+            };
+            // Unit x's output, from its value slot to memory; then both CTAs' value slots of the
+            // unit are free for copies from either (V warp; every unit once, in order: two barriers
+            // by parity, so that none is lapped).
+            int out_slot[2] = {0, 0};
+            auto store_out = [&](int x) -> bool {
+                const uint32_t parity = (uint32_t)((x >> 1) & 1);
+                const bool done = __all_sync(0xffffffffu, mbar_wait(barOut + 8 * (x & 1), parity, p.err));
+                const Unit Y = unit(x);
+                if (done && Y.j0 + min(QPT, p.chunk) <= p.chunk) {
+                    if (lane == 0) {
+                        const uint32_t src = sV + (uint32_t)(x & 1 ? out_slot[1] : out_slot[0]) * SM::kVHalf;
 #pragma unroll
-                    for (int h = 0; h < SM::kHalves; ++h)
-                        tma_store_4d(&tmap_o, (int)rank * DH + h * 64, 0, Y.g, Y.s * p.chunk + Y.j0, src + h * kHalf);
-                    bulk_commit();
-                    bulk_wait_read();
+                        for (int h = 0; h < SM::kHalves; ++h)
+                            tma_store_4d(&tmap_o, (int)rank * DH + h * 64, 0, Y.g, Y.s * p.chunk + Y.j0,
+                                         src + h * kHalf);
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!done) return false;
+                if (lane == 0) arrive_cluster(peer_addr(barOtherOut + 8 * (x & 1), rank ^ 1u));
+                return __all_sync(0xffffffffu, mbar_wait(barOtherOut + 8 * (x & 1), parity, p.err));
+            };
+            bool ok = true;
+            int N = 0;      // tiles or halves issued so far
+            int nq = 0;     // query tiles issued (K warp)
+            int prev_steps = 0;
+            Unit U;
+            int raw_cur = 0, raw_next = 0;
+            if (my_units > 0) {
+                U = unit(0);
+                raw_cur = ids_load(U, 0);
+                raw_next = ids_load(U, 1);
             }
-            if (!done) return false;
-            if (lane == 0) arrive_cluster(peer_addr(barOtherOut + 8 * (x & 1), rank ^ 1u));
-            return __all_sync(0xffffffffu, mbar_wait(barOtherOut + 8 * (x & 1), (uint32_t)((x >> 1) & 1), p.err));
-        };
-        bool ok = true;
-        int N = 0;      // tiles or halves issued so far
-        int nq = 0;     // query tiles issued (K warp)
-        int prev_steps = 0;
-        Unit U;
-        int raw_cur = 0, raw_next = 0;
-        if (my_units > 0) {
-            U = unit(0);
-            raw_cur = ids_load(U, 0);
-            raw_next = ids_load(U, 1);
-        }
-        for (int k = 0; k < my_units && ok; ++k) {
-            Unit X = U;            // the next unit, and its first ids
-            int nraw_cur = 0, nraw_next = 0;
-            if (k + 1 < my_units) {
-                X = unit(k + 1);
-                nraw_cur = ids_load(X, 0);
-                nraw_next = ids_load(X, 1);
-            }
-            if (is_k) {
-                if (k > 0)     // the previous unit's Q.K have all read the query tile
-                    ok = __all_sync(0xffffffffu, mbar_wait(barQfree, (uint32_t)((k - 1) & 1), p.err));
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
+            for (int k = 0; k < my_units && ok; ++k) {
+                Unit X = U;            // the next unit, and its first ids
+                int nraw_cur = 0, nraw_next = 0;
+                if (k + 1 < my_units) {
+                    X = unit(k + 1);
+                    nraw_cur = ids_load(X, 0);
+                    nraw_next = ids_load(X, 1);
                 }
-                nq = k + 1;
-                if (lane == 0) mbar_expect(barQ, SM::kQTile);
-                __syncwarp();
-                if (lane < SM::kHalves)
-                    tma_load_5d(sQ + lane * kHalf, &tmap_q, lane * 64, (int)rank, 0, U.g, U.s * p.chunk + U.j0, barQ);
-            }
-            const int key_head = p.by_head ? U.g : 2 * U.g + (int)rank;
-            const int value_head = p.by_head ? (U.g >> 1) * 2 : 2 * U.g;
-            int ids_cur = ids_check(raw_cur, U, 0);
-            const int steps = U.n_tiles * per_tile;
-            for (int t = 0; t < steps; ++t, ++N) {
-                if (t > 0 && t % spl == 0) {
-                    ids_cur = ids_check(raw_next, U, t / spl);
-                    raw_next = ids_load(U, t / spl + 1);
-                }
-                const int tb = (t % spl) * nb, st = N % slots;
-                const int blk = __shfl_sync(0xffffffffu, ids_cur, (tb + lane) & 31);
-                if (N >= slots) {   // the slot's previous tile has been consumed by its MMAs
-                    const int np = N - slots;
-                    const uint32_t bar = free0 + 8 * (np % slots), parity = (uint32_t)((np / slots) & 1);
-                    ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err));
+                if (is_k) {
+                    if (k > 0)     // the previous unit's Q.K have all read the query tile
+                        ok = __all_sync(0xffffffffu, mbar_wait(barQfree, (uint32_t)((k - 1) & 1), p.err));
                     if (!ok) {
                         *abort_flag = 1;
                         break;
                     }
+                    nq = k + 1;
+                    if (lane == 0) mbar_expect(barQ, SM::kQTile);
+                    __syncwarp();
+                    if (lane < SM::kHalves)
+                        tma_load_5d(sQ + lane * kHalf, &tmap_q, lane * 64, (int)rank, 0, U.g, U.s * p.chunk + U.j0,
+                                    barQ);
                 }
-                // A unit's last two value slots also hold its exchange and its output, and are
-                // next filled four halves on: from this unit's third half on, or, behind a unit
-                // of two halves, from the first of the unit after.
-                if (!is_k) {
-                    const int x = t == 2 ? k - 1 : t == 0 && prev_steps == 2 ? k - 2 : -1;
-                    if (x >= 0 && !store_out(x)) {
-                        ok = false;
-                        *abort_flag = 1;
-                        break;
+                const int key_head = p.by_head ? U.g : 2 * U.g + (int)rank;
+                const int value_head = p.by_head ? (U.g >> 1) * 2 : 2 * U.g;
+                int ids_cur = ids_check(raw_cur, U, 0);
+                const int steps = U.n_tiles * per_tile;
+                for (int t = 0; t < steps; ++t, ++N) {
+                    if (t > 0 && t % spl == 0) {
+                        ids_cur = ids_check(raw_next, U, t / spl);
+                        raw_next = ids_load(U, t / spl + 1);
+                    }
+                    const int tb = (t % spl) * nb, st = N % slots;
+                    const int blk = __shfl_sync(0xffffffffu, ids_cur, (tb + lane) & 31);
+                    if (N >= slots) {   // the slot's previous tile has been consumed by its MMAs
+                        const int np = N - slots;
+                        const uint32_t bar = free0 + 8 * (np % slots), parity = (uint32_t)((np / slots) & 1);
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err));
+                        if (!ok) {
+                            *abort_flag = 1;
+                            break;
+                        }
+                    }
+                    // A unit's last two value slots also hold its exchange and its output, and are
+                    // next filled four halves on: from this unit's third half on, or, behind a unit
+                    // of two halves, from the first of the unit after.
+                    if (!is_k) {
+                        const int x = t == 2 ? k - 1 : t == 0 && prev_steps == 2 ? k - 2 : -1;
+                        if (x >= 0 && !store_out(x)) {
+                            ok = false;
+                            *abort_flag = 1;
+                            break;
+                        }
+                    }
+                    if (lane == 0) mbar_expect(bar0 + 8 * st, is_k ? SM::kKTile : SM::kVHalf);
+                    __syncwarp();
+                    if (is_k) {
+                        if (lane < NBK)
+                            tma_load_5d(sK + st * SM::kKTile + lane * (uint32_t)(BS * DH * 2), &tmap_k, 0, 0, 0,
+                                        key_head * (BS / 8), blk, bar0 + 8 * st);
+                    } else if (lane < NBV) {
+                        // one of the block's two heads, to both CTAs; the other CTA copies the other
+                        tma_load_5d_both(sV + st * SM::kVHalf + lane * kVBlock + rank * (kVBlock / 2), &tmap_v, 0, 0, 0,
+                                         value_head + (int)rank, blk, bar0 + 8 * st);
                     }
                 }
-                if (lane == 0) mbar_expect(bar0 + 8 * st, is_k ? SM::kKTile : SM::kVHalf);
-                __syncwarp();
-                if (is_k) {
-                    if (lane < NBK)
-                        tma_load_5d(sK + st * SM::kKTile + lane * (uint32_t)(BS * DH * 2), &tmap_k, 0, 0, 0,
-                                    key_head * (BS / 8), blk, bar0 + 8 * st);
-                } else if (lane < NBV) {
-                    // one of the block's two heads, to both CTAs; the other CTA copies the other
-                    tma_load_5d_both(sV + st * SM::kVHalf + lane * kVBlock + rank * (kVBlock / 2), &tmap_v, 0, 0, 0,
-                                     value_head + (int)rank, blk, bar0 + 8 * st);
-                }
+                prev_steps = steps;
+                if (k & 1) out_slot[1] = (N + kVS - 2) % kVS;     // where this unit's output will be staged
+                else out_slot[0] = (N + kVS - 2) % kVS;
+                U = X;
+                raw_cur = nraw_cur;
+                raw_next = nraw_next;
             }
-            prev_steps = steps;
-            if (k & 1) out_slot[1] = (N + kVS - 2) % kVS;     // where this unit's output will be staged
-            else out_slot[0] = (N + kVS - 2) % kVS;
-            U = X;
-            raw_cur = nraw_cur;
-            raw_next = nraw_next;
-        }
-        if (!is_k) {    // the outputs no later half waited for
-            for (int x = max(0, my_units - (prev_steps == 2 ? 2 : 1)); x < my_units && ok && !*abort_flag; ++x)
-                ok = store_out(x);
-            if (lane == 0) bulk_wait_all();   // no store in flight when the CTA ends
-        }
-        if (!ok || *abort_flag) {
-            // wait (bounded) for this warp's copies still in flight before the memory is released
-            for (int t = max(0, N - slots); t < N; ++t)
-                mbar_wait(bar0 + 8 * (t % slots), (uint32_t)((t / slots) & 1), p.err);
-            if (nq > 0) mbar_wait(barQ, (uint32_t)((nq - 1) & 1), p.err);
-        }
-        __syncwarp();
+            if (!is_k) {    // the outputs no later half waited for
+                for (int x = max(0, my_units - (prev_steps == 2 ? 2 : 1)); x < my_units && ok && !*abort_flag; ++x)
+                    ok = store_out(x);
+                if (lane == 0) bulk_wait_all();   // no store in flight when the CTA ends
+            }
+            if (!ok || *abort_flag) {
+                // wait (bounded) for this warp's copies still in flight before the memory is released
+                for (int t = max(0, N - slots); t < N; ++t)
+                    mbar_wait(bar0 + 8 * (t % slots), (uint32_t)((t / slots) & 1), p.err);
+                if (nq > 0) mbar_wait(barQ, (uint32_t)((nq - 1) & 1), p.err);
+            }
+            __syncwarp();
         };
         if (warp == kKWarp) copy(std::true_type());
         else copy(std::false_type());

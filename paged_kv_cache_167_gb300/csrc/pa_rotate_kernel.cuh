@@ -173,9 +173,12 @@ cudaError_t launch_rotate_v(RotateParams &p, const Axes &axes, int64_t tokens, c
         if (V == 8 && u == 1 && few > 1 && z > 1 && (tokens + z - 1) / z * gz >= 4ll * device_sm_count()) {
             const dim3 fgrid((unsigned)((tokens + z - 1) / z), 1, gz), fblock(x, fy, z);
             switch (few) {
-                case 2: return launch_pdl(rotate_kernel<V, INTERLEAVED, 2, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
-                case 3: return launch_pdl(rotate_kernel<V, INTERLEAVED, 3, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
-                default: return launch_pdl(rotate_kernel<V, INTERLEAVED, 4, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
+                case 2:
+                    return launch_pdl(rotate_kernel<V, INTERLEAVED, 2, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
+                case 3:
+                    return launch_pdl(rotate_kernel<V, INTERLEAVED, 3, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
+                default:
+                    return launch_pdl(rotate_kernel<V, INTERLEAVED, 4, CACHE, Axes>, fgrid, fblock, stream, 0, p, axes);
             }
         }
     }

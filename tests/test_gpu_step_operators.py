@@ -168,7 +168,8 @@ def test_extend_nothing(pa):
     s.check(pa)
 
 
-@pytest.mark.parametrize("n,room,b", [(600, 0, 16), (4096, 100000, 7), (20011, 50, 16), (70001, 0, 32), (300000, 9, 16)])
+@pytest.mark.parametrize("n,room,b", [(600, 0, 16), (4096, 100000, 7), (20011, 50, 16), (70001, 0, 32),
+                                      (300000, 9, 16)])
 def test_extend_many_sequences(pa, n, room, b):
     """Sequences by the thousands, with and without a range of places for each CTA of a
     cluster, pieces of more than 128; against sums of the lengths."""

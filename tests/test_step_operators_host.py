@@ -97,8 +97,8 @@ def test_extend_refusals(B, kw):
     assert _extend(B, **kw) == INVALID
 
 
-@pytest.mark.parametrize("kw", [dict(lens=FAKE + (5 << 16)), dict(lens=FAKE + (6 << 16) + 8), dict(starts=FAKE + (5 << 16)),
-                                dict(cursor_out=FAKE + (8 << 16)), dict(offsets=FAKE + (1 << 16)),
+@pytest.mark.parametrize("kw", [dict(lens=FAKE + (5 << 16)), dict(lens=FAKE + (6 << 16) + 8),
+                                dict(starts=FAKE + (5 << 16)), dict(cursor_out=FAKE + (8 << 16)), dict(offsets=FAKE + (1 << 16)),
                                 dict(free=FAKE + (3 << 16) + 60), dict(ctx=FAKE + 44), dict(new=FAKE + (4 << 16) + 60)])
 def test_extend_refuses_overlap(B, kw):
     """Inputs that another CTA may still read while one writes them."""
@@ -165,6 +165,14 @@ def _prefill_diff(B, hkv=2, hq=4, d=64, b=16, seqs=3, chunk=5, ctx=30, q=FAKE, l
                                 dict(hkv=-2, hq=4)])
 def test_prefill_diff_refusals(B, kw):
     assert _prefill_diff(B, **kw) == INVALID
+
+
+def test_prefill_diff_refuses_positions_that_pass_31_bits(B):
+    pool = B.PaKvPool(FAKE, 1 << 28, 2, 16, 64, 0, 0, 0)
+    weights = B.PaDiff(FAKE, FAKE, 1e-5, 1.0, 0)
+    for chunk, ctx in [(5, 2 ** 31 - 10), (2 ** 31 - 1, 2 ** 31 - 1), (300, 2 ** 31 - 301)]:
+        assert B.lib().pa_prefill_diff(FAKE, FAKE, ctypes.byref(pool), FAKE, 1 << 27, FAKE, 1, chunk, 4, ctx, 0.1,
+                                       ctypes.byref(weights), None) == INVALID
 
 
 def test_prefill_diff_more_refusals(B):
