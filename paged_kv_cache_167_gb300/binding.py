@@ -607,7 +607,7 @@ def _axes(axes: np.ndarray, positions: torch.Tensor, n: int, freqs: torch.Tensor
     if positions.dim() != 2 or positions.shape[1] != n:
         raise ValueError("positions must be [num_axes][tokens]")
     s0, s1 = positions.stride()
-    if n > 1 and (s1 != 1 or (positions.shape[0] > 1 and s0 < n)):
+    if (n > 1 and s1 != 1) or (positions.shape[0] > 1 and s0 < n):
         raise ValueError("each axis's positions must be dense")
     address = axes.address if type(axes) is RotaryAxes else None   # (a slice or copy has none of its own)
     return PaRotaryAxes(address or axes.ctypes.data, positions.shape[0], s0 if positions.shape[0] > 1 else 0), \

@@ -5,6 +5,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import operators as ref
 
@@ -148,6 +149,26 @@ def test_decode_diff_more_refusals(B):
     assert _decode_diff(B, seqs=0) == 0 and _decode_diff(B, seqs=0, weight=None, eps=0.0) == 0
     pool = B.PaKvPool(FAKE, 64, 3, 16, 64, 0, 0, 0)
     assert B.lib().pa_decode_diff_workspace_size(ctypes.byref(pool), 4, 6, 100) == 0
+
+
+@pytest.mark.parametrize("shape,strides,ok", [((3, 1), (1, 1), True), ((3, 1), (0, 1), False), ((3, 1), (7, 0), True),
+                                              ((1, 1), (0, 0), True), ((2, 4), (4, 1), True), ((2, 4), (9, 1), True),
+                                              ((2, 4), (0, 1), False), ((2, 4), (3, 1), False),
+                                              ((2, 4), (8, 2), False), ((2, 4), (1, 2), False)])
+def test_axes_positions_of_any_stride(B, shape, strides, ok):
+    """What reaches the library is the distance of the axes' rows; rows that share their
+    memory (one position for all axes, expanded) have none and are refused."""
+    positions = torch.arange(64).as_strided(shape, strides)
+    axes = B.rotary_axes([2] * shape[0])
+    freqs = torch.zeros(2 * shape[0], dtype=torch.int64)
+    if not ok:
+        with pytest.raises(ValueError, match="dense"):
+            B._axes(axes, positions, shape[1], freqs, -1)
+        return
+    desc, address = B._axes(axes, positions, shape[1], freqs, -1)
+    assert address == positions.data_ptr() and desc.num_axes == shape[0]
+    for a in range(1, shape[0]):     # 0: num_tokens
+        assert (desc.position_stride or shape[1]) * a == positions.stride(0) * a
 
 
 def _prefill_diff(B, hkv=2, hq=4, d=64, b=16, seqs=3, chunk=5, ctx=30, q=FAKE, lam=FAKE, eps=1e-5, scale=0.1,
