@@ -169,7 +169,9 @@ cudaError_t launch_rotate_v(RotateParams &p, const Axes &axes, int64_t tokens, c
     int u = wide ? (V == 8 ? most : most > 2 ? 4 : most) : 1;
     if constexpr (!std::is_same<Axes, OneAxis>::value) {
         // few heads: up to four a thread, and the CTA's other threads on further tokens
-        const int few = heads < 4 ? heads : 4, fy = (heads + few - 1) / few, z = kRotateThreads / (x * fy);
+        // (64: a block's largest z)
+        const int few = heads < 4 ? heads : 4, fy = (heads + few - 1) / few;
+        const int z = kRotateThreads / (x * fy) < 64 ? kRotateThreads / (x * fy) : 64;
         if (V == 8 && u == 1 && few > 1 && z > 1 && (tokens + z - 1) / z * gz >= 4ll * device_sm_count()) {
             const dim3 fgrid((unsigned)((tokens + z - 1) / z), 1, gz), fblock(x, fy, z);
             switch (few) {

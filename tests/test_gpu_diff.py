@@ -166,6 +166,27 @@ def test_decode_diff_flat_and_sharp(pa, spread):
     x.check(pa)
 
 
+@pytest.mark.parametrize("norm", [False, True])
+def test_decode_diff_nothing_cached(pa, norm):
+    """No sequence has a token: zeros, with a bound of 0 tokens and with a larger one."""
+    for max_len in (0, 1, 5000):
+        x = Batch([0] * 5, 8, 2, 64, 16, seed=1, norm=norm)
+        x.max_len = max_len
+        x.decode(pa)
+        assert torch.equal(x.out, torch.zeros_like(x.out)) and pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 1.5])
+def test_decode_diff_scales(pa, scale):
+    """Any finite scale; a negative one is the positive one of negated queries."""
+    x = Batch([200, 3, 65], 16, 2, 128, 16, seed=4)
+    x.scale = scale
+    x.decode(pa)
+    if scale < 0:
+        x.scale, x.q = -scale, -x.q
+    x.check(pa, what=f"scale {scale}")
+
+
 def test_decode_diff_equal_maps_cancel(pa):
     """The same query and key heads in both maps, lambda 1: nothing is left, whatever a
     unit's cuts; the norm of zeros is zero."""

@@ -369,6 +369,20 @@ def test_rotate_axes_many_tokens(pa, heads, d, rot):
     assert torch.equal(got[:, :, rot:], x[:, :, rot:]) and pa.get_device_error() == 0
 
 
+@pytest.mark.parametrize("heads", [2, 3, 4, 5, 8])
+@pytest.mark.parametrize("d,rot", [(16, 16), (24, 16), (32, 32)])
+def test_rotate_axes_small_heads_many_tokens(pa, heads, d, rot):
+    """Tokens of one or two chunks, of which a CTA could hold more than a block has places."""
+    n = 100003
+    x = normal((n, heads, d), seed=heads)
+    pos = torch.arange(n, device="cuda") * 5 - 1000
+    freqs = cuda(pa.rotary_frequencies(rot))
+    one, two = torch.empty_like(x), torch.empty_like(x)
+    pa.rotate(one, x, pos, freqs)
+    pa.rotate(two, x, pos.expand(2, n).contiguous(), freqs, axes=pa.rotary_axes([rot // 2 - 3, 3], "cycled"))
+    assert np.array_equal(bits(one), bits(two)) and pa.get_device_error() == 0
+
+
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (0, 2), (4, 2), (64, 8)])
 def test_rotate_and_cache_axes_many_tokens(pa, hq, hkv):
     """The same with the slot writer, against the call with one axis: equal positions."""
