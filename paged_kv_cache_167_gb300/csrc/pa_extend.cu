@@ -18,7 +18,7 @@
 // workspace is needed.
 //
 // What bounds it: latency (16 bytes a token are written, some 12 a sequence read).  GB300:
-// 64 sequences of a token 2.9 us, one of 131,071 tokens 3.6, 4,096 mixed 7.1 us, 16,384 of a
+// 64 sequences of a token 2.8 us, one of 131,071 tokens 3.5, 4,096 mixed 6.0 us, 16,384 of a
 // token 8.8 us, 65,536 24 (8.0, 17.6 and 49 with every CTA adding up all of them).
 #include "pa_device.cuh"
 #include "pa_internal.h"

@@ -21,8 +21,9 @@
 // 2,000 for each of the unit's tiles.
 //
 // What bounds it: the tensor pipe.  GB300, 16 x (4,096 + 512) tokens of 64/8 heads, d =
-// 128: 1.08 ms, 1.62 PFLOP/s, 0.86 of the measured bf16 rate; 2,048 tokens from the start
-// (32/8 heads) 59 us, where a cluster has three or four units and their ends weigh more.
+// 128: 1.08 to 1.14 ms (power), 1.54 to 1.62 PFLOP/s, 0.82 to 0.86 of the measured bf16 rate;
+// 2,048 tokens from the start (32/8 heads) 59 us, where a cluster has three or four units and
+// their ends weigh more.
 //
 // Design, as far as it is not pa_prefill.cu's:
 //  * A unit is an M-tile of 128 rows (query j0 + r / G, pair r % G of the G query
