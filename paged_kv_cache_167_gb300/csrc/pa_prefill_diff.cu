@@ -17,8 +17,10 @@
 // difference and the norm lose nothing before the one rounding to bf16), stored
 // asynchronously into the unit's last two value slots there, which nothing reads any
 // more; the bytes themselves complete the receiver's barrier.  That takes some 4,500
-// cycles (15 bytes a cycle), the norm's sums and the output another 5,000, against
-// 2,000 for each of the unit's tiles.
+// cycles (15 bytes a cycle; nothing but such stores reaches 19, bulk copies 15), the norm's
+// sums and the output another 5,000, against 2,000 for each of the unit's tiles.  (The
+// halves staged and sent as bulk copies: 61.3 us instead of 58.7 for 2,048 tokens; cut to 24
+// bits a value: 57.5, too little for a rounding more.)
 //
 // What bounds it: the tensor pipe.  GB300, 16 x (4,096 + 512) tokens of 64/8 heads, d =
 // 128: 1.08 to 1.14 ms (power), 1.54 to 1.62 PFLOP/s, 0.82 to 0.86 of the measured bf16 rate;
@@ -680,7 +682,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float lt = l + lo;
             const float f = lt > 0.f ? lam / lt : 0.f;
             tc_fence_after();
-            // ---- the maps meet: x = this CTA's half of the columns.  Both CTAs' P.V of the unit
+            // ---- the maps meet: x = this CTA's half of the columns (its product rounded as the
+            // other's is: contracted with the sum, equal maps would not cancel).  Both CTAs' P.V of the unit
             // have completed, so its last two value slots are free in both (a quarter of 2d each).
             const uint32_t out_off = SM::kOffV + (uint32_t)((2 * T - 2) % kVS) * SM::kVHalf;
             const uint32_t sX = base + out_off;
@@ -713,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_ld<W>(tO + lane_off + rank * DH + q * (DH / 2) + pt * W, o);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < W; ++i) x[q][i] = __uint_as_float(o[i]) * f;
+                    for (int i = 0; i < W; ++i) x[q][i] = __fmul_rn(__uint_as_float(o[i]), f);
                 }
             }
             // O has been read: the next unit's first P.V may overwrite it

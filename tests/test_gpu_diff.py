@@ -361,6 +361,16 @@ def test_prefill_diff_flat_and_sharp(pa, spread):
     x.check_prefill(pa)
 
 
+@pytest.mark.parametrize("d,norm", [(64, True), (128, True), (128, False)])
+def test_prefill_diff_equal_maps_cancel(pa, d, norm):
+    """As in decode: the maps meet as the same bits, so nothing is left."""
+    x = Batch([300, 77, 150], 8, 4, d, 16, seed=6, keys="head", chunk=70, norm=norm)
+    x.q[:, :, 1::2] = x.q[:, :, 0::2]
+    x.lam.fill_(1.0)
+    x.prefill(pa)
+    assert torch.equal(x.out, torch.zeros_like(x.out)) and pa.get_device_error() == 0
+
+
 def test_prefill_diff_agrees_with_decode(pa):
     """A chunk of one token is a decode step: both within the definition's bounds."""
     x = chunked([300, 64, 0], 1, 16, 4, 128, 16, seed=23)
