@@ -153,6 +153,29 @@ __device__ __forceinline__ bool elect_one() {
 // A matrix descriptor that lies `bytes` behind another.
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) { return desc + (uint64_t)(bytes >> 4); }
 
+// Waits for a barrier that the other CTA's threads, stores or MMAs complete: its acquire is
+// at cluster scope, which orders what that CTA did before (its reads of slots that are
+// stored to or filled next, the data it stored here) before what this thread does now.  The
+// waits within a CTA, several a tile, acquire at its own scope.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned int *err) {
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            raise_error(err, PA_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 // Named barriers whose threads all learn whether any of them saw `mine`: the two warps
 // of the same rows, and all softmax warps.  A warp that gives up alone would leave the
 // others waiting for it, and these barriers have no limit; so giving up is decided
@@ -344,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (!done) return false;
                 if (lane == 0) arrive_cluster(peer_addr(barOtherOut + 8 * (x & 1), rank ^ 1u));
-                return __all_sync(0xffffffffu, mbar_wait(barOtherOut + 8 * (x & 1), parity, p.err));
+                return __all_sync(0xffffffffu, mbar_wait_cluster(barOtherOut + 8 * (x & 1), parity, p.err));
             };
             bool ok = true;
             int N = 0;      // tiles or halves issued so far
@@ -393,7 +416,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (N >= slots) {   // the slot's previous tile has been consumed by its MMAs
                         const int np = N - slots;
                         const uint32_t bar = free0 + 8 * (np % slots), parity = (uint32_t)((np / slots) & 1);
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err));
+                        ok = __all_sync(0xffffffffu, is_k ? mbar_wait(bar, parity, p.err)
+                                                          : mbar_wait_cluster(bar, parity, p.err));
                         if (!ok) {
                             *abort_flag = 1;
                             break;
@@ -672,7 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 done = t + 1;
             }
             // ---- epilogue.  The row's sum over both halves (the reference is one); -1: gave up
-            const bool fin = done == U.n_tiles && !*abort_flag && mbar_wait(barUnit, (uint32_t)(k & 1), p.err);
+            const bool fin = done == U.n_tiles && !*abort_flag && mbar_wait_cluster(barUnit, (uint32_t)(k & 1), p.err);
             float *lx = mx + (T & 1) * 256;           // the parity that the last tile did not use
             lx[pt * 128 + r] = fin ? l : -1.f;
             part_sync(warp);
@@ -722,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // O has been read: the next unit's first P.V may overwrite it
             tc_fence_before();
             mbar_arrive_u32(barOfree);
-            if (ok) ok = mbar_wait(my_full, (uint32_t)(k & 1), p.err);
+            if (ok) ok = mbar_wait_cluster(my_full, (uint32_t)(k & 1), p.err);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
 #pragma unroll
@@ -755,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (ok && lane < 8)
                     store_async(peer_addr(smem_addr(mx + at * 128 + (warp & 3) * 32 + lane * 4), other), four,
                                 peer_addr(my_norm, other));
-                ok = !part_or(warp, !ok) && mbar_wait(my_norm, (uint32_t)(k & 1), p.err);
+                ok = !part_or(warp, !ok) && mbar_wait_cluster(my_norm, (uint32_t)(k & 1), p.err);
                 ss = (mx[r] + mx[128 + r]) + (mx[256 + r] + mx[384 + r]);
                 scale *= rsqrtf(ss * (1.f / DV) + p.eps);
             }

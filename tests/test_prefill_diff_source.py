@@ -1,0 +1,31 @@
+"""What the differential prefill kernel's source must hold to, and no run can show: the
+memory model's order between the two CTAs of a cluster."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_kv_cache_167_gb300", "csrc")
+
+
+def code(name):
+    """A source file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = re.sub(r"/\*.*?\*/", " ", f.read(), flags=re.S)
+    return re.sub(r"//[^\n]*", " ", text)
+
+
+def waits(text):
+    """(wait, its barrier's expression) of every call."""
+    return re.findall(r"\b(mbar_wait\w*)\((\w+)", text)
+
+
+def test_waits_for_the_other_cta_acquire_at_cluster_scope():
+    """Barriers that another CTA completes (an arrival, a commit or a store of its own) are
+    waited for with an acquire at cluster scope: at the CTA's scope, the default, nothing
+    orders the reads behind the wait after what the other CTA wrote."""
+    text = code("pa_prefill_diff.cu")
+    assert ".acquire.cluster." in text
+    remote = {"barUnit", "my_full", "my_norm"} | ({"barOtherOut"} if "barOtherOut" in text else set())
+    seen = waits(text)
+    for name in remote:
+        kinds = {kind for kind, bar in seen if bar == name}
+        assert kinds == {"mbar_wait_cluster"}, f"{name}: {sorted(kinds)}"
