@@ -41,8 +41,8 @@
 //    tiles of 64 keys 128 KB.  The query tile is free once a unit's last scores are there,
 //    so the next unit's is copied under the last products; the warp that copies values
 //    stores a unit's output from its value slots before it fills them again.
-//  * Both maps multiply the same values: each CTA copies one head's half of them to both
-//    (multicast), which takes a third off what the SMs read from L2.
+//  * Both maps multiply the same values, and each CTA copies all of them for itself (96 KB a
+//    tile and CTA from L2; neighbouring clusters' tiles share them there).
 //  * The copying and issuing warps run few instructions a tile, all lanes together: with
 //    every descriptor put together anew by one lane, two copies a block of keys and waits
 //    that acquired at cluster scope, those warps, not the tensor pipe, made the tile
@@ -119,18 +119,6 @@ __device__ __forceinline__ void store_async(uint32_t addr, float4 v, uint32_t ba
         "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
         "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
         : "memory");
-}
-// A box to the same place in both CTAs, completing its bytes on the same barrier in each.
-__device__ __forceinline__ void tma_load_5d_both(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                                 int c4, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar), "h"((uint16_t)3)
-        : "memory");
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t addr) {   // a shared::cluster address
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // Arrives, once this thread's MMAs so far have completed, on the barrier at this offset
 // in the other CTA as well.
@@ -218,11 +206,10 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
 
 // Barriers, as in pa_prefill.cu unless noted: Q landed, K landed[2], V half landed[4],
 // S ready[2] (a K slot is free with it), P ready[2][half of the keys], P.V done[2] (a S
-// buffer is free with it), V half free[4] (in both CTAs: two arrivals), Q free, unit's P.V
-// done (in both CTAs), O read, the two MMA lanes' drains; then full[8] (the other CTA's
-// data for a warp has landed), norm[4] (its partial sums of squares of a lane quadrant's
-// rows), out[2] (a unit's output is staged in its last value slots, or written: by unit
-// parity), other out[2] (the other CTA's is stored).
+// buffer is free with it), V half free[4], Q free, unit's P.V done (in both CTAs: two
+// arrivals), O read, the two MMA lanes' drains; then full[8] (the other CTA's data for a warp
+// has landed), norm[4] (its partial sums of squares of a lane quadrant's rows), out[2] (a
+// unit's output is staged in its last value slots, or written: by unit parity).
 // The tiles of the CTA's units are numbered T = 0, 1, ...; its value halves H = 2T, 2T + 1.
 template <int DH, int G, int BS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -243,8 +230,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t barQ = base + SM::kOffBar, barK = barQ + 8, barV = barK + 16, barS = barV + 8 * kVS,
                    barP = barS + 16, barOP = barP + 32, barVfree = barOP + 16, barQfree = barVfree + 8 * kVS,
                    barUnit = barQfree + 8, barOfree = barUnit + 8, barEnd = barOfree + 8, barEndQk = barEnd + 8,
-                   barFull = barEndQk + 8, barNorm = barFull + 64, barOut = barNorm + 32, barOtherOut = barOut + 16;
-    constexpr int kNumBars = 1 + 2 + kVS + 2 + 4 + 2 + kVS + 1 + 1 + 1 + 1 + 1 + 8 + 4 + 2 + 2;
+                   barFull = barEndQk + 8, barNorm = barFull + 64, barOut = barNorm + 32;
+    constexpr int kNumBars = 1 + 2 + kVS + 2 + 4 + 2 + kVS + 1 + 1 + 1 + 1 + 1 + 8 + 4 + 2;
     static_assert(8 * kNumBars + 8 <= 384, "barrier area");
     static_assert(kVS == 4, "two tiles of value halves");
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + SM::kOffBar + 8 * kNumBars);
@@ -267,8 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kNumBars; ++i) {
             const uint32_t b = barQ + 8 * i;
             uint32_t count = 1;
-            if ((b >= barP && b < barOP) || b == barOfree || (b >= barOut && b < barOtherOut)) count = kSoftWarps * 32;
-            if (b >= barVfree && b < barQfree) count = 2;    // both CTAs' P.V lanes
+            if ((b >= barP && b < barOP) || b == barOfree || b >= barOut) count = kSoftWarps * 32;
             if (b == barUnit) count = 2;                     // both CTAs' P.V lanes
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(count) : "memory");
         }
@@ -345,9 +331,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 return v;
             };
-            // Unit x's output, from its value slot to memory; then both CTAs' value slots of the
-            // unit are free for copies from either (V warp; every unit once, in order: two barriers
-            // by parity, so that none is lapped).
+            // Unit x's output, from its value slot to memory; then the unit's value slots are free
+            // for copies again: what the other CTA stored in them has been read before the output
+            // was staged (V warp; every unit once, in order: two barriers by parity, so that none is
+            // lapped).
             int out_slot[2] = {0, 0};
             auto store_out = [&](int x) -> bool {
                 const uint32_t parity = (uint32_t)((x >> 1) & 1);
@@ -365,9 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (!done) return false;
-                if (lane == 0) arrive_cluster(peer_addr(barOtherOut + 8 * (x & 1), rank ^ 1u));
-                return __all_sync(0xffffffffu, mbar_wait_cluster(barOtherOut + 8 * (x & 1), parity, p.err));
+                return done;
             };
             bool ok = true;
             int N = 0;      // tiles or halves issued so far
@@ -416,8 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (N >= slots) {   // the slot's previous tile has been consumed by its MMAs
                         const int np = N - slots;
                         const uint32_t bar = free0 + 8 * (np % slots), parity = (uint32_t)((np / slots) & 1);
-                        ok = __all_sync(0xffffffffu, is_k ? mbar_wait(bar, parity, p.err)
-                                                          : mbar_wait_cluster(bar, parity, p.err));
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err));
                         if (!ok) {
                             *abort_flag = 1;
                             break;
@@ -441,9 +425,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tma_load_5d(sK + st * SM::kKTile + lane * (uint32_t)(BS * DH * 2), &tmap_k, 0, 0, 0,
                                         key_head * (BS / 8), blk, bar0 + 8 * st);
                     } else if (lane < NBV) {
-                        // one of the block's two heads, to both CTAs; the other CTA copies the other
-                        tma_load_5d_both(sV + st * SM::kVHalf + lane * kVBlock + rank * (kVBlock / 2), &tmap_v, 0, 0, 0,
-                                         value_head + (int)rank, blk, bar0 + 8 * st);
+                        tma_load_5d(sV + st * SM::kVHalf + lane * kVBlock, &tmap_v, 0, 0, 0, value_head, blk,
+                                    bar0 + 8 * st);
                     }
                 }
                 prev_steps = steps;
@@ -534,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 umma_ts(tO, tP + (kk >> 1) * 32 + (kk & 1) * 8, desc_at(dv, v_off), idesc_pv,
                                         (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
                             }
-                            umma_commit_both(barVfree + 8 * st);
+                            umma_commit(barVfree + 8 * st);
                             if (hf == 1) umma_commit(barOP + 8 * sb);
                         }
                         __syncwarp();
@@ -912,8 +895,8 @@ cudaError_t launch_pairs(const PrefillArgs &a, const pa_diff &diff, bool by_head
         const cuuint32_t box[5] = {64, 8, DH / 64, (cuuint32_t)(BS / 8), 1};
         if (!encode_bf16(&mk, 5, a.pool.base, dims, strides, box)) return cudaErrorInvalidValue;
     }
-    // values: one box per block and head
-    if (encode_pool_block_map(&mv, a.pool, 1, BS) != cudaSuccess) return cudaErrorInvalidValue;
+    // values: one box per block, of both heads
+    if (encode_pool_block_map(&mv, a.pool, 1, BS, 2) != cudaSuccess) return cudaErrorInvalidValue;
     DiffParams prm;
     prm.out = static_cast<__nv_bfloat16 *>(a.out);
     prm.tables = a.tables;

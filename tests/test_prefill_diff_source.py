@@ -1,5 +1,5 @@
-"""What the differential prefill kernel's source must hold to, and no run can show: the
-memory model's order between the two CTAs of a cluster."""
+"""What the kernels' sources must hold to, and no run can show: the memory model's order
+between the two CTAs of a cluster, and copies that stay within a CTA."""
 import os
 import re
 
@@ -24,8 +24,18 @@ def test_waits_for_the_other_cta_acquire_at_cluster_scope():
     orders the reads behind the wait after what the other CTA wrote."""
     text = code("pa_prefill_diff.cu")
     assert ".acquire.cluster." in text
-    remote = {"barUnit", "my_full", "my_norm"} | ({"barOtherOut"} if "barOtherOut" in text else set())
+    remote = {"barUnit", "my_full", "my_norm"}
     seen = waits(text)
     for name in remote:
         kinds = {kind for kind, bar in seen if bar == name}
         assert kinds == {"mbar_wait_cluster"}, f"{name}: {sorted(kinds)}"
+
+
+def test_no_load_is_multicast():
+    """The library runs on every GPU of a machine and takes any pool's address: no tensor or
+    bulk copy in it writes to several CTAs.  (A commit that arrives on several is no copy.)"""
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith((".cu", ".cuh", ".cpp", ".h")):
+            joined = re.sub(r'"\s*"', "", code(name))          # string literals of one instruction
+            copies = [line for line in re.findall(r"cp\.async\.bulk[\w.:]*", joined) if "multicast" in line]
+            assert not copies, f"{name}: {copies}"
