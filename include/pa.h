@@ -528,6 +528,9 @@ pa_status pa_extend_tables(int32_t *block_tables, int32_t max_blocks_per_seq, in
 #define PA_DIFF_KEYS_BY_HEAD 0x1u /* query head i reads key head i / R (both maps of a query
                                    * pair the same one where R is even), instead of the
                                    * pair's first and second by the map                 */
+#define PA_DIFF_ONE_TERM 0x2u     /* pa_prefill_diff alone (pa_decode_diff refuses it): a
+                                   * probability enters its product rounded to bf16, not as
+                                   * two bf16 terms                                       */
 typedef struct {
     const float *lambda;      /* device, [num_q_heads / 2]: of the layer's learned vectors */
     const float *norm_weight; /* device, [2 * head_dim], 16-byte aligned; NULL: no norm    */
@@ -568,8 +571,14 @@ pa_status pa_decode_diff(void *out, const void *q, const pa_kv_pool *pool, const
  * ctx_lens[s] + chunk_len - 1 (a value that the mask hides from a query is multiplied by
  * zero, which an infinity or NaN survives; slots behind that may hold anything).  Both
  * products run on the tcgen05 tensor cores with fp32 accumulation, a cluster of two
- * CTAs a tile of queries, one for each map; a probability is rounded to bf16 (relative
- * 2^-8, its sum is not), the difference and the norm are fp32, and out is rounded once.
+ * CTAs a tile of queries, one for each map.  Sums, softmax statistics, the difference and
+ * the norm are fp32; a probability enters its product as two bf16 terms, and out is
+ * rounded once: a token has the same accuracy here as in pa_decode_diff.  With
+ * PA_DIFF_ONE_TERM a probability is rounded to bf16 (by up to 2^-8 of it; its sum is not),
+ * which takes two thirds of the time for long contexts.  That error weighs more the more of
+ * the maps cancels: with the norm, outputs are off by 0.002 of their size on average for
+ * independent maps, 0.005 to 0.010 for maps correlated by 0.99 and 0.005 to 0.03 by 0.999
+ * (two terms: 0.0017, what rounding them costs).
  * Supported: head_dim 64 or 128; an even num_kv_heads; R 1, 2, 4 or 8; block_size 8, 16,
  * 32 or 64; at most 65,535 sequences.  Errors as pa_prefill_chunk;
  * PA_ERR_INVALID_ARG for a bad pa_diff.

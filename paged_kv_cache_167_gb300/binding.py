@@ -28,6 +28,7 @@ DEVERR_KEEP, DEVERR_VALUE, DEVERR_NO_ROOM = 0x20, 0x40, 0x80
 PA_DTYPE_BF16, PA_DTYPE_F32 = 0, 1
 PA_ROTARY_INTERLEAVED, PA_ROTARY_INVERSE = 0x1, 0x2
 DIFF_KEYS = {"map": 0, "head": 1}          # PA_DIFF_KEYS_BY_HEAD
+PA_DIFF_ONE_TERM = 0x2
 AXES_ORDERS = {"blocks": 0, "cycled": 1}
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "parts": 3, "parts_index": 4}
 
@@ -751,7 +752,7 @@ def decode_diff_workspace_size(pool: torch.Tensor, num_seqs: int, num_q_heads: i
 
 
 def _diff(lam: torch.Tensor, norm_weight: Optional[torch.Tensor], eps: float, out_scale: float, keys: str, hq: int,
-          d: int, device: int) -> PaDiff:
+          d: int, device: int, flags: int = 0) -> PaDiff:
     if keys not in DIFF_KEYS:
         raise ValueError(f"keys must be one of {sorted(DIFF_KEYS)}")
     if 2 * lam.numel() != hq:
@@ -761,7 +762,8 @@ def _diff(lam: torch.Tensor, norm_weight: Optional[torch.Tensor], eps: float, ou
         if norm_weight.numel() != 2 * d:
             raise ValueError("norm_weight must hold 2 * head_dim weights")
         weight = _at(norm_weight, torch.float32, "norm_weight", device)
-    return PaDiff(_at(lam, torch.float32, "lam", device), weight, eps, out_scale, DIFF_KEYS[keys])
+    return PaDiff(_at(lam, torch.float32, "lam", device), weight, eps, out_scale,
+                  DIFF_KEYS[keys] | flags)
 
 
 def decode_diff(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor, block_tables: torch.Tensor,
@@ -804,10 +806,11 @@ def decode_diff(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor, block_ta
 def prefill_diff(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor, block_tables: torch.Tensor,
                  ctx_lens: torch.Tensor, max_ctx_len: int, scale: float, lam: torch.Tensor,
                  norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-5, out_scale: float = 1.0,
-                 keys: str = "map", layer: Optional[int] = None, stream=None) -> None:
+                 keys: str = "map", layer: Optional[int] = None, stream=None, one_term: bool = False) -> None:
     """pa_prefill_diff: q [B][C][Hq][d] over KV heads in pairs -> out
     [B][C][Hq / 2][2 d], causal; the weights as decode_diff, the rest as
-    prefill_chunk."""
+    prefill_chunk.  one_term (PA_DIFF_ONE_TERM): probabilities rounded to bf16,
+    faster, and further from the definition where the two maps are alike."""
     desc = pool_desc(pool, layer)
     B, C, Hq, d = q.shape
     if d != desc.head_dim or Hq % 2 or tuple(out.shape) != (B, C, Hq // 2, 2 * d):
@@ -817,7 +820,7 @@ def prefill_diff(out: torch.Tensor, q: torch.Tensor, pool: torch.Tensor, block_t
     dev = torch.cuda.current_device()
     if pool.get_device() != dev:
         _refuse(pool, torch.bfloat16, "pool", dev)
-    weights = _diff(lam, norm_weight, eps, out_scale, keys, Hq, d, dev)
+    weights = _diff(lam, norm_weight, eps, out_scale, keys, Hq, d, dev, PA_DIFF_ONE_TERM if one_term else 0)
     _check(lib().pa_prefill_diff(_at(out, torch.bfloat16, "out", dev), _at(q, torch.bfloat16, "q", dev),
                                  ctypes.byref(desc), _at(block_tables, torch.int32, "block_tables", dev),
                                  block_tables.shape[1], _at(ctx_lens, torch.int32, "ctx_lens", dev), B, C, Hq,

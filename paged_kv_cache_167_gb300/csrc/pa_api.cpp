@@ -129,9 +129,9 @@ pa_status plan_decode_diff(const PoolView &pool, int32_t num_seqs, int32_t num_q
     return PA_OK;
 }
 
-bool diff_ok(const pa_diff *d) {
+bool diff_ok(const pa_diff *d, uint32_t flags) {   // flags: those that the call knows
     if (!d || !d->lambda || (reinterpret_cast<uintptr_t>(d->lambda) & 3u) != 0) return false;
-    if (!std::isfinite(d->out_scale) || (d->flags & ~PA_DIFF_KEYS_BY_HEAD) != 0) return false;
+    if (!std::isfinite(d->out_scale) || (d->flags & ~flags) != 0) return false;
     return !d->norm_weight || (aligned16(d->norm_weight) && std::isfinite(d->eps) && d->eps > 0.f);
 }
 
@@ -318,7 +318,7 @@ pa_status pa_decode_diff(void *out, const void *q, const pa_kv_pool *pool, const
                          int32_t num_q_heads, int32_t max_seq_len, float scale, const pa_diff *diff,
                          void *workspace, size_t workspace_bytes, const void *new_k, const void *new_v,
                          uint32_t flags, cudaStream_t stream) {
-    if ((flags & ~PA_DECODE_EARLY_METADATA) != 0 || !diff_ok(diff)) return PA_ERR_INVALID_ARG;
+    if ((flags & ~PA_DECODE_EARLY_METADATA) != 0 || !diff_ok(diff, PA_DIFF_KEYS_BY_HEAD)) return PA_ERR_INVALID_ARG;
     if ((new_k == nullptr) != (new_v == nullptr)) return PA_ERR_INVALID_ARG;
     if (new_k && (!aligned16(new_k) || !aligned16(new_v))) return PA_ERR_INVALID_ARG;
     PoolView view;
@@ -364,7 +364,8 @@ pa_status pa_prefill_diff(void *out, const void *q, const pa_kv_pool *pool, cons
     PoolView view;
     pa_status st = resolve_pool(pool, &view);
     if (st != PA_OK) return st;
-    if (num_seqs < 0 || chunk_len < 0 || num_q_heads <= 0 || max_ctx_len < 0 || !diff_ok(diff))
+    if (num_seqs < 0 || chunk_len < 0 || num_q_heads <= 0 || max_ctx_len < 0 ||
+        !diff_ok(diff, PA_DIFF_KEYS_BY_HEAD | PA_DIFF_ONE_TERM))
         return PA_ERR_INVALID_ARG;
     if (num_q_heads % view.num_kv_heads != 0 || view.num_kv_heads % 2 != 0) return PA_ERR_INVALID_ARG;
     if (!prefill_diff_supported(view.head_dim, num_q_heads / view.num_kv_heads, view.block_size))

@@ -23,7 +23,7 @@
 //
 // The probabilities enter P.V as two bf16 terms, as in the plain kernel: the
 // difference of two maps is smaller than either, and the norm scales it up again, so
-// a rounding of p (2^-9) would weigh more here than there.
+// a rounding of p (up to 2^-8) would weigh more here than there.
 //
 // What bounds it: DRAM, as the plain kernel.  GB300, of the measured copy bandwidth: 4 x
 // 32,768 tokens of 32/8 heads, d = 128, 87 us (0.91); 64 x 600-850 of 64/8 40.2 us (0.71: the

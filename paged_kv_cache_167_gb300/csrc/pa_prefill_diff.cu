@@ -9,23 +9,33 @@
 // Why a cluster of two CTAs: one map of a 128-row tile holds 128 x 2d fp32 sums, half
 // of an SM's tensor memory at d = 128; with two score tiles beside it the other half
 // is gone as well, so the two maps cannot share an SM.  CTA r of a cluster runs map r
-// as an attention of its own (scores 128 x 128 x d, products 128 x 2d x 128: with
-// values twice as wide the tensor cores have one and a half times the work a score
-// that plain attention has, against one exponential).  The maps meet once a unit:
-// each CTA finishes one half of the 2d columns, so it sends the other half of its own
-// map, divided by the row's sum and weighted, to the other CTA: 64 KB of fp32 (the
-// difference and the norm lose nothing before the one rounding to bf16), stored
-// asynchronously into the unit's last two value slots there, which nothing reads any
-// more; the bytes themselves complete the receiver's barrier.  That takes some 4,500
-// cycles (15 bytes a cycle; nothing but such stores reaches 19, bulk copies 15), the norm's
-// sums and the output another 5,000, against 2,000 for each of the unit's tiles.  (The
-// halves staged and sent as bulk copies: 61.3 us instead of 58.7 for 2,048 tokens; cut to 24
-// bits a value: 57.5, too little for a rounding more.)
+// as an attention of its own (scores 128 x 128 x d, products 128 x 2d x 128 for each
+// term of the probabilities: with values twice as wide and two terms the tensor cores
+// have two and a half times the work a score that plain attention has, against one
+// exponential).  The maps meet once a unit: each CTA finishes one half of the 2d
+// columns, so it sends the other half of its own map, divided by the row's sum and
+// weighted, to the other CTA: 64 KB of fp32 (the difference and the norm lose nothing
+// before the one rounding to bf16), stored asynchronously into the unit's last two value
+// slots there, which nothing reads any more; the bytes themselves complete the receiver's
+// barrier.  That takes some 4,500 cycles (15 bytes a cycle; nothing but such stores
+// reaches 19, bulk copies 15), the norm's sums and the output another 5,000, against 2,000
+// for each of the unit's tiles with one term.  (With one term, the halves staged and sent
+// as bulk copies: 61.3 us instead of 58.7 for 2,048 tokens; cut to 24 bits a value: 57.5,
+// too little for a rounding more.)
 //
-// What bounds it: the tensor pipe.  GB300, 16 x (4,096 + 512) tokens of 64/8 heads, d =
-// 128: 1.08 to 1.14 ms (power), 1.54 to 1.62 PFLOP/s, 0.82 to 0.86 of the measured bf16 rate;
-// 2,048 tokens from the start (32/8 heads) 59 us, where a cluster has three or four units and
-// their ends weigh more.
+// A probability enters P.V as two bf16 terms, its rounding and what that left, as in decode
+// and for its reason: what the difference takes out of two maps that are alike leaves the
+// roundings of both, and the norm scales them up.  Off from the definition on average, maps
+// correlated by 0, 0.99 or 0.999, lambda 0.8 or 1, 40 to 2,048 keys: 0.0017 of the output,
+// what rounding the output costs.  With PA_DIFF_ONE_TERM a probability is rounded once, by up
+// to 2^-8 of it: 0.0020 to 0.0022, 0.0045 to 0.0104 and 0.0052 to 0.0315, for two thirds of
+// the time.
+//
+// What bounds it: the tensor pipe.  GB300, by graph replay: 16 x (4,096 + 512) tokens of 64/8
+// heads, d = 128: 1.64 to 1.69 ms, 1.04 to 1.07 PFLOP/s of the definition's 6d a key and query
+// head (a term more: 1.73 to 1.78, 0.92 to 0.95 of the measured bf16 rate); with one term 1.09
+// to 1.11 ms (1.58 to 1.61 PFLOP/s).  2,048 tokens from the start (32/8 heads) 75 us, 57 with
+// one term: a cluster has three or four units, and their ends weigh more.
 //
 // Design, as far as it is not pa_prefill.cu's:
 //  * A unit is an M-tile of 128 rows (query j0 + r / G, pair r % G of the G query
@@ -35,7 +45,8 @@
 //    each), which share one accumulator, so they agree on the reference maximum.  A
 //    tile's first probabilities are made with the reference as it is, while each finds its
 //    maximum; a barrier of the two warps then says whether any row exceeds it by more than
-//    8 (log2), and only then do the maxima meet and the tile start over.  P.V of a half of
+//    8 (log2), and only then do the maxima meet and the tile start over, from its scores in
+//    tensor memory (the probabilities have taken their registers).  P.V of a half of
 //    the keys starts when that half's probabilities are there.
 //  * Shared memory (d = 128): one query tile 32 KB, two key tiles 64 KB, four half value
 //    tiles of 64 keys 128 KB.  The query tile is free once a unit's last scores are there,
@@ -211,7 +222,7 @@ __device__ __forceinline__ float4 lds_f4(uint32_t addr) {
 // has landed), norm[4] (its partial sums of squares of a lane quadrant's rows), out[2] (a
 // unit's output is staged in its last value slots, or written: by unit parity).
 // The tiles of the CTA's units are numbered T = 0, 1, ...; its value halves H = 2T, 2T + 1.
-template <int DH, int G, int BS>
+template <int DH, int G, int BS, int TERMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_diff_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
@@ -514,8 +525,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 // lies in 16 columns, the first half of those its scores had.
                                 const uint32_t v_off =
                                     (uint32_t)(kk * 16 / BS) * kVBlock + (uint32_t)((kk * 16) % BS) * 128u;
-                                umma_ts(tO, tP + (kk >> 1) * 32 + (kk & 1) * 8, desc_at(dv, v_off), idesc_pv,
-                                        (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
+                                const uint32_t a = tP + (kk >> 1) * 32 + (kk & 1) * 8;
+                                umma_ts(tO, a, desc_at(dv, v_off), idesc_pv, (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
+                                if (TERMS == 2) umma_ts(tO, a + 16, desc_at(dv, v_off), idesc_pv, 1u);
                             }
                             umma_commit(barVfree + 8 * st);
                             if (hf == 1) umma_commit(barOP + 8 * sb);
@@ -565,17 +577,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = false;
                 }
                 const int key0 = t * kKeys + pt * 32;
-                if (!__all_sync(0xffffffffu, key0 + 64 + 31 <= pos)) {   // tile crosses some row's causal edge
+                const bool edge = !__all_sync(0xffffffffu, key0 + 64 + 31 <= pos);   // some row's causal edge
+                auto hide = [&](int cc) {
 #pragma unroll
-                    for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (key0 + cc * 64 + i > pos) sr[cc][i] = __float_as_uint(-INFINITY);
+                    for (int i = 0; i < 32; ++i)
+                        if (key0 + cc * 64 + i > pos) sr[cc][i] = __float_as_uint(-INFINITY);
+                };
+                if (edge) {
+                    hide(0);
+                    hide(1);
                 }
                 const float2 c2 = make_float2(c, c);
                 float2 ps2 = make_float2(0.f, 0.f), ps2b = make_float2(0.f, 0.f);
-                uint32_t pw[16];
-                auto probabilities = [&](int cc) {   // of half cc, and their sums
+                auto probabilities = [&](int cc) {   // of half cc, in its scores' place, and their sums
                     const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
                     const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
@@ -585,7 +599,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                         if (e & 1) ps2b = __fadd2_rn(ps2b, pe);
                         else ps2 = __fadd2_rn(ps2, pe);
-                        pw[e] = pack_bf16x2(pe.x, pe.y);
+                        sr[cc][2 * e] = __float_as_uint(pe.x);
+                        sr[cc][2 * e + 1] = __float_as_uint(pe.y);
                     }
                 };
                 // The first half's probabilities by the reference as it is, while the maximum is
@@ -600,6 +615,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (bool first = true;; first = false) {
                     ps2 = ps2b = make_float2(0.f, 0.f);
+                    if (!first) {      // the scores once more
+                        tmem_ld32(tS, sr[0]);
+                        tmem_ld_wait();
+                        if (edge) hide(0);
+                    }
                     probabilities(0);
                     if (!first || !part_or(warp, trouble || mine_l > m_ref + kRescaleThreshold ||
                                                      (m_ref == -INFINITY && mine_l != -INFINITY)))
@@ -643,11 +663,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool zero_tail = tail_lo > 0 && tail_lo < kKeys && (U.seq_end % BS) != 0;
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    // P as bf16 into the columns its scores were read from, one rounding a
-                    // probability (with few keys pa_prefill.cu's grouped form takes two terms; a
-                    // prompt's rows see many)
+                    // P into the columns its scores were read from: hi = bf16(p) into the first
+                    // half of them, lo = bf16(p - hi) into the second
                     if (hf == 1) probabilities(1);
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        pw[e] = pack_bf16x2(__uint_as_float(sr[hf][2 * e]), __uint_as_float(sr[hf][2 * e + 1]));
                     tmem_st16(tS + hf * 64, pw);
+                    if (TERMS == 2) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float lo0 = __uint_as_float(sr[hf][2 * e]) - __uint_as_float(pw[e] << 16);
+                            const float lo1 = __uint_as_float(sr[hf][2 * e + 1]) - __uint_as_float(pw[e] & 0xffff0000u);
+                            pw[e] = pack_bf16x2(lo0, lo1);
+                        }
+                        tmem_st16(tS + hf * 64 + 16, pw);
+                    }
                     tmem_st_wait();
                     // Keys past the sequence end inside its last block: zero their V rows (their p
                     // is 0, but the slots may hold non-finite junk).  P.V(T - 1) is waited for
@@ -828,14 +860,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---- host side --------------------------------------------------------------------
 
-template <int DH, int G, int BS>
+template <int DH, int G, int BS, int TERMS>
 cudaError_t launch_kernel(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
                           const DiffParams &prm, cudaStream_t stream) {
     static bool configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && !configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_diff_kernel<DH, G, BS>,
+        cudaError_t e = cudaFuncSetAttribute(prefill_diff_kernel<DH, G, BS, TERMS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)DiffSmem<DH>::kBytes);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
@@ -858,7 +890,14 @@ cudaError_t launch_kernel(const CUtensorMap &mq, const CUtensorMap &mk, const CU
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefill_diff_kernel<DH, G, BS>, mq, mk, mv, mo, prm);
+    return cudaLaunchKernelEx(&cfg, prefill_diff_kernel<DH, G, BS, TERMS>, mq, mk, mv, mo, prm);
+}
+
+template <int DH, int G, int BS>
+cudaError_t launch_terms(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
+                         const DiffParams &prm, bool one, cudaStream_t stream) {
+    return one ? launch_kernel<DH, G, BS, 1>(mq, mk, mv, mo, prm, stream)
+               : launch_kernel<DH, G, BS, 2>(mq, mk, mv, mo, prm, stream);
 }
 
 bool encode_bf16(CUtensorMap *map, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
@@ -925,11 +964,12 @@ cudaError_t launch_pairs(const PrefillArgs &a, const pa_diff &diff, bool by_head
     prm.norm_weight = diff.norm_weight;
     prm.eps = diff.eps;
     prm.out_scale = diff.out_scale;
+    const bool one = (diff.flags & PA_DIFF_ONE_TERM) != 0;
     switch (BS) {
-        case 8: return launch_kernel<DH, G, 8>(mq, mk, mv, mo, prm, stream);
-        case 16: return launch_kernel<DH, G, 16>(mq, mk, mv, mo, prm, stream);
-        case 32: return launch_kernel<DH, G, 32>(mq, mk, mv, mo, prm, stream);
-        case 64: return launch_kernel<DH, G, 64>(mq, mk, mv, mo, prm, stream);
+        case 8: return launch_terms<DH, G, 8>(mq, mk, mv, mo, prm, one, stream);
+        case 16: return launch_terms<DH, G, 16>(mq, mk, mv, mo, prm, one, stream);
+        case 32: return launch_terms<DH, G, 32>(mq, mk, mv, mo, prm, one, stream);
+        case 64: return launch_terms<DH, G, 64>(mq, mk, mv, mo, prm, one, stream);
         default: return cudaErrorInvalidValue;
     }
 }
