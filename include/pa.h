@@ -704,7 +704,9 @@ typedef struct {
  * num_pairs together).  PA_AXES_BLOCKS: the sections one behind the other.
  * PA_AXES_CYCLED: pair i belongs to axis i mod num_axes while i < num_axes *
  * sections[that axis], every other pair to axis 0, so that each axis has fast and
- * slow pairs alike.  Frequencies that begin anew in each section are the caller's
+ * slow pairs alike.  (An axis a > 0 whose last pair, num_axes * (sections[a] - 1) + a,
+ * would lie behind the head's pairs owns those that do not, and axis 0 the rest.)
+ * Frequencies that begin anew in each section are the caller's
  * own: pa_rotary_turns, or pa_rotary_frequencies of each section, one behind the
  * other. */
 #define PA_AXES_BLOCKS 0

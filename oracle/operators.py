@@ -1,5 +1,5 @@
 """fp64 restatements of the rotary positions, the compaction of cached tokens,
-beam search's selection, a step's tables and differential attention, for the
+beam search's selection, a step's tables and positions of several axes, for the
 tests: plain numpy, one token or row at a time, sharing no code with the library."""
 from __future__ import annotations
 

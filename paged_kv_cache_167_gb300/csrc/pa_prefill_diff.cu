@@ -32,10 +32,13 @@
 // the time.
 //
 // What bounds it: the tensor pipe.  GB300, by graph replay: 16 x (4,096 + 512) tokens of 64/8
-// heads, d = 128: 1.64 to 1.69 ms, 1.04 to 1.07 PFLOP/s of the definition's 6d a key and query
-// head (a term more: 1.73 to 1.78, 0.92 to 0.95 of the measured bf16 rate); with one term 1.09
-// to 1.11 ms (1.58 to 1.61 PFLOP/s).  2,048 tokens from the start (32/8 heads) 75 us, 57 with
-// one term: a cluster has three or four units, and their ends weigh more.
+// heads, d = 128: 1.64 to 1.71 ms, 1.02 to 1.07 PFLOP/s of the definition's 6d a key and query
+// head (with the second term's 4d: 1.71 to 1.78, 0.91 to 0.95 of the measured bf16 rate in a
+// burst, all of the sustained one); with one term 1.08 to 1.11 ms (1.58 to 1.63 PFLOP/s).  2,048
+// tokens from the start (32/8 heads) 74 to 77 us, 57 to 63 with one term: a cluster has three
+// or four units, and their ends weigh more.  5 x 333 tokens at up to 3,000 (16/8 heads, d = 64)
+// 44 to 68 us by their lengths, 39 to 59 with one term: 120 units dealt to 76 clusters by
+// number, so the busiest has 1.6 times the mean's tiles.
 //
 // Design, as far as it is not pa_prefill.cu's:
 //  * A unit is an M-tile of 128 rows (query j0 + r / G, pair r % G of the G query
@@ -952,11 +955,13 @@ cudaError_t launch_pairs(const PrefillArgs &a, const pa_diff &diff, bool by_head
     prm.num_kv = groups;
     prm.num_seqs = a.num_seqs;
     // The order of the units.  By tile, longest first over all groups and sequences, balances
-    // the clusters best (2,048 tokens from the start, 32/8 heads: 71 us in the other order, 57
-    // in this), but neighbours then read different keys; where all keys and values are more
-    // than L2 keeps (16 x (4,096 + 512), 300 MB: 1,100 us, 1,350 by tile), or where the
-    // contexts, not the tiles, make the lengths (5 x 333 at up to 3,000: 36.3 us, 38.0 by
+    // the clusters best (2,048 tokens from the start, 32/8 heads, 8 MB: 94 us in the other order,
+    // 74 in this), but neighbours then read different keys; where all keys and values are more
+    // than L2 keeps (16 x (4,096 + 512), 300 MB: 1,680 us, 1,940 by tile), or where the
+    // contexts, not the tiles, make the lengths (5 x 333 at up to 3,000: 44.4 us, 47.1 by
     // tile), the tiles of one group and sequence follow each other and read them together.
+    // 48 MB lies between the sizes measured, well within L2.  The host knows bounds, not
+    // lengths: short prompts called with a large max_ctx_len take the second order.
     prm.by_length = a.max_ctx_len < a.chunk_len &&
                     (int64_t)a.num_seqs * ((int64_t)a.max_ctx_len + a.chunk_len) * Hkv * DH * 4 <= (48ll << 20);
     prm.by_head = by_head ? 1 : 0;
